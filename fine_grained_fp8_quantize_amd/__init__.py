@@ -42,6 +42,13 @@ Layouts (row-major, K contiguous for GEMM operands):
   quantizes both GEMM operands in one launch.
 * ``fp8_gemm_tensor`` -- one scale per operand, the whole K sum in the MFMA
   accumulators.
+* ``fp4_quantize_mx(x)`` / ``fp4_quantize_mx_scatter(x, dst_rows, m_total)`` /
+  ``fp4_dequantize_mx(q, scale, rows, cols)`` -- FP4 microscaling (E2M1 codes,
+  1x32 blocks along rows or, transposed, columns) in tiles of 16 rows x 128 k,
+  and back.
+* ``fp4_gemm_mx(a, a_scale, b, b_scale, m, n)`` / ``fp4_grouped_gemm_mx(...)``
+  -- products of FP4 matrices: one, or one per expert over an expert-sorted
+  row layout.
 
 E4M3 tensors are returned as ``torch.float8_e4m3fn`` (OCP E4M3FN bytes);
 ``uint8`` tensors are accepted wherever codes are inputs.
@@ -70,6 +77,11 @@ __all__ = [
     "fp8_gemm_mx",
     "fp8_retile_act_128x1",
     "fp8_gemm_tensor",
+    "fp4_quantize_mx",
+    "fp4_quantize_mx_scatter",
+    "fp4_dequantize_mx",
+    "fp4_gemm_mx",
+    "fp4_grouped_gemm_mx",
     "fp8q_status_string",
     "fp8q_last_hip_error",
     "Fp8qError",
@@ -766,3 +778,8 @@ def fp8_gemm_tensor(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_s
                                  _ptr(b_scale), _ptr(out), out.stride(0), oc, _stream(stream))
     _check(st, "fp8_gemm_tensor")
     return out
+
+
+# (at the end: this module uses the helpers above)
+from ._mx4 import (  # noqa: E402
+    fp4_dequantize_mx, fp4_gemm_mx, fp4_grouped_gemm_mx, fp4_quantize_mx, fp4_quantize_mx_scatter)

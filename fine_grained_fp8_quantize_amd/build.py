@@ -19,8 +19,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfp8q.so")
 
-SOURCES = ["api.cpp", "quant.hip", "gemm.hip"]
-HEADERS = ["fp8q_device.h", "gemm_common.h", "launch.h"]
+SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "mx4/mx4_api.cpp", "mx4/mx4_quant.hip", "mx4/mx4_gemm.hip"]
+HEADERS = ["fp8q_device.h", "gemm_common.h", "launch.h", "host_checks.hpp", "mx4/mx4.h"]
+PUBLIC_HEADERS = ["fp8q.h", "fp8q_mx4.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -41,7 +42,7 @@ def sources() -> list[str]:
 
 
 def build(force: bool = True, verbose: bool = False) -> str:
-    deps = sources() + [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "fp8q.h")]
+    deps = sources() + [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, h) for h in PUBLIC_HEADERS]
     if not force and os.path.exists(LIB) and all(os.path.getmtime(LIB) >= os.path.getmtime(d) for d in deps):
         return LIB
     tmp = LIB + ".tmp%d" % os.getpid()

@@ -12,6 +12,7 @@
 
 #include <vector>
 
+#include "host_checks.hpp"
 #include "launch.h"
 
 namespace {
@@ -20,11 +21,21 @@ thread_local int g_last_hip_error = 0;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+}  // namespace
+
+namespace fp8q {
+
 int hip_status(hipError_t e) {
     if (e == hipSuccess) return FP8Q_OK;
     g_last_hip_error = (int)e;
     return FP8Q_ERR_HIP;
 }
+
+}  // namespace fp8q
+
+using fp8q::hip_status;
+
+namespace {
 
 // A grid of more than 2^31 - 1 blocks is not launchable.
 bool grid_ok(int64_t blocks) { return blocks >= 0 && blocks <= 0x7FFFFFFFLL; }

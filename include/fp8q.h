@@ -546,4 +546,6 @@ int fp8q_last_hip_error(void);
 }
 #endif
 
+#include "fp8q_mx4.h" /* FP4 microscaling quantization and products */
+
 #endif /* FP8Q_H */
