@@ -49,6 +49,10 @@ Layouts (row-major, K contiguous for GEMM operands):
 * ``fp4_gemm_mx(a, a_scale, b, b_scale, m, n)`` / ``fp4_grouped_gemm_mx(...)``
   -- products of FP4 matrices: one, or one per expert over an expert-sorted
   row layout.
+* ``moe_dispatch(ids, experts)`` -- the expert-sorted row layout of a batch's
+  routes: what the scattering quantizers and the grouped GEMMs take.
+* ``moe_balance_loss(logits, ids)`` / ``moe_balance_loss_backward(...)`` -- the
+  router's balance loss with per-expert counts, and its gradient.
 
 E4M3 tensors are returned as ``torch.float8_e4m3fn`` (OCP E4M3FN bytes);
 ``uint8`` tensors are accepted wherever codes are inputs.
@@ -82,6 +86,9 @@ __all__ = [
     "fp4_dequantize_mx",
     "fp4_gemm_mx",
     "fp4_grouped_gemm_mx",
+    "moe_dispatch",
+    "moe_balance_loss",
+    "moe_balance_loss_backward",
     "fp8q_status_string",
     "fp8q_last_hip_error",
     "Fp8qError",
@@ -780,6 +787,7 @@ def fp8_gemm_tensor(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_s
     return out
 
 
-# (at the end: this module uses the helpers above)
+# (at the end: these modules use the helpers above)
 from ._mx4 import (  # noqa: E402
     fp4_dequantize_mx, fp4_gemm_mx, fp4_grouped_gemm_mx, fp4_quantize_mx, fp4_quantize_mx_scatter)
+from ._moe import moe_balance_loss, moe_balance_loss_backward, moe_dispatch  # noqa: E402

@@ -19,9 +19,10 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfp8q.so")
 
-SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "mx4/mx4_api.cpp", "mx4/mx4_quant.hip", "mx4/mx4_gemm.hip"]
-HEADERS = ["fp8q_device.h", "gemm_common.h", "launch.h", "host_checks.hpp", "mx4/mx4.h"]
-PUBLIC_HEADERS = ["fp8q.h", "fp8q_mx4.h"]
+SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "mx4/mx4_api.cpp", "mx4/mx4_quant.hip", "mx4/mx4_gemm.hip",
+           "moe/moe_api.cpp", "moe/moe.hip"]
+HEADERS = ["fp8q_device.h", "gemm_common.h", "launch.h", "host_checks.hpp", "mx4/mx4.h", "moe/moe.h"]
+PUBLIC_HEADERS = ["fp8q.h", "fp8q_mx4.h", "fp8q_moe.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

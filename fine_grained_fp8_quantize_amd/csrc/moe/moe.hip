@@ -1,0 +1,566 @@
+// moe.hip -- MoE routing kernels for gfx950: the expert-sorted row layout of
+// a batch's routes, and the balance loss with its gradient (formulas in
+// include/fp8q_moe.h).
+#include "moe/moe.h"
+
+#include "fp8q_device.h"
+
+#include <math.h>
+
+#include <type_traits>
+
+namespace fp8q {
+namespace moe {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWaves = kThreads / 64;
+
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ int wave_inclusive_sum(int v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(v, d);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp<0xB1>(v);
+    v += dpp<0x4E>(v);
+    v += dpp<0x141>(v);
+    v += dpp<0x140>(v);
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    return v;
+}
+
+__device__ __forceinline__ float wave_fmax(float v) {
+    v = fmaxf(v, dpp<0xB1>(v));
+    v = fmaxf(v, dpp<0x4E>(v));
+    v = fmaxf(v, dpp<0x141>(v));
+    v = fmaxf(v, dpp<0x140>(v));
+    v = fmaxf(v, __shfl_xor(v, 16));
+    v = fmaxf(v, __shfl_xor(v, 32));
+    return v;
+}
+
+// ---------------------------------------------------------------- dispatch
+
+// Routes of one part, counted per expert in LDS (integer sums: any order
+// gives the same).
+__global__ __launch_bounds__(kThreads) void dispatch_count_kernel(DispatchArgs p, int64_t per_part) {
+    __shared__ int hist[kMaxExperts];
+    const int tid = threadIdx.x;
+    if (tid < p.experts) hist[tid] = 0;
+    __syncthreads();
+    const int64_t beg = (int64_t)blockIdx.x * per_part, end = min(beg + per_part, p.routes);
+    for (int64_t i = beg + tid; i < end; i += kThreads) {
+        const int64_t e = (int64_t)p.ids[i] - p.first;
+        if (e >= 0 && e < p.experts) atomicAdd(&hist[e], 1);
+    }
+    __syncthreads();
+    if (tid < p.experts) p.counts[(int64_t)blockIdx.x * p.experts + tid] = hist[tid];
+}
+
+// Destinations of one part's routes. A wave owns a contiguous run of the
+// part; its routes' places are: start of the expert's segment + routes of
+// earlier parts + of earlier waves + of earlier lanes and rounds of its own.
+// Lanes with the same expert find each other with one ballot per bit of the
+// expert's number. SINGLE: the part is the whole batch, and the counts are
+// its own.
+template <bool SINGLE>
+__global__ __launch_bounds__(kThreads) void dispatch_place_kernel(DispatchArgs p, int64_t per_part, int parts) {
+    __shared__ int next[kWaves][kMaxExperts];
+    __shared__ int wave_total[kWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int experts = p.experts;
+    for (int i = lane; i < experts; i += 64) next[wave][i] = 0;
+    wave_lds_fence();
+    const int64_t per_wave = per_part / kWaves;  // a multiple of 64
+    const int64_t beg = (int64_t)blockIdx.x * per_part + wave * per_wave;
+    const int64_t end = min(beg + per_wave, p.routes);
+    for (int64_t i = beg + lane; i < end; i += 64) {
+        const int64_t e = (int64_t)p.ids[i] - p.first;
+        if (e >= 0 && e < experts) atomicAdd(&next[wave][e], 1);
+    }
+    int total = 0, before = 0;
+    if (!SINGLE && tid < experts) {
+        for (int c = 0; c < parts; ++c) {
+            const int v = p.counts[(int64_t)c * experts + tid];
+            total += v;
+            before += c < (int)blockIdx.x ? v : 0;
+        }
+    }
+    __syncthreads();
+    if (SINGLE && tid < experts) {
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) total += next[w][tid];
+    }
+    // start of every expert's segment: running sum of the padded counts
+    const int padded = (int)(((int64_t)total + p.align - 1) / p.align * p.align);
+    const int incl = wave_inclusive_sum(padded);
+    if (lane == 63) wave_total[wave] = incl;
+    __syncthreads();
+    int start = incl - padded;
+    for (int w = 0; w < wave; ++w) start += wave_total[w];
+    if (tid < experts) {
+        if (blockIdx.x == 0) {
+            p.offsets[tid] = start;
+            p.rows[tid] = total;
+            if (tid == experts - 1) p.offsets[experts] = start + padded;
+        }
+        int at = start + before;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const int v = next[w][tid];
+            next[w][tid] = at;
+            at += v;
+        }
+    }
+    __syncthreads();
+    const int bits = 32 - __clz(experts - 1);  // (__clz(0) = 32: one expert, no bits)
+    for (int64_t i0 = beg; i0 < end; i0 += 64) {
+        const int64_t i = i0 + lane;
+        const int64_t id = i < end ? (int64_t)p.ids[i] - p.first : -1;
+        const bool valid = id >= 0 && id < experts;
+        const int e = valid ? (int)id : 0;
+        unsigned long long peers = __ballot(valid);
+        for (int b = 0; b < bits; ++b) {
+            const bool set = (e >> b) & 1;
+            const unsigned long long m = __ballot(set);
+            peers &= set ? m : ~m;
+        }
+        const int rank = __popcll(peers & ((1ull << lane) - 1));
+        int dst = -1;
+        if (valid) dst = next[wave][e] + rank;
+        wave_lds_fence();
+        if (valid && rank == 0) next[wave][e] += __popcll(peers);
+        wave_lds_fence();
+        if (i < end) p.dst[i] = dst;
+    }
+}
+
+// ----------------------------------------------------------------- balance
+
+// The tokens are cut into parts of `chunk` tokens, sequence by sequence. A
+// part's workgroup leaves its score sums and route counts per expert and one
+// record; the finish kernel adds a sequence's parts in order.
+struct Part {
+    int seq, first;  // its sequence (-1: unused) and that sequence's first part
+    int tokens, routes;
+};
+
+constexpr int kChunk = 64;
+constexpr int64_t kMaxParts = 1024;  // beyond the sequences' ragged ends
+
+struct BalancePlan {
+    int64_t chunk, parts;
+    Part* info;
+    float* sums;    // [parts][experts]
+    int* counts;    // [parts][experts]
+    float* losses;  // one per workgroup of the finish kernel
+    unsigned* done;
+    int64_t bytes;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+BalancePlan plan_of(int64_t tokens, int64_t experts, int64_t seqs, void* workspace) {
+    BalancePlan b;
+    b.chunk = kChunk * (tokens > kChunk * kMaxParts ? ceil_div(tokens, kChunk * kMaxParts) : 1);
+    b.parts = ceil_div(tokens, b.chunk) + seqs;
+    char* at = static_cast<char*>(workspace);
+    b.info = reinterpret_cast<Part*>(at);
+    at += b.parts * sizeof(Part);
+    b.sums = reinterpret_cast<float*>(at);
+    at += b.parts * experts * sizeof(float);
+    b.counts = reinterpret_cast<int*>(at);
+    at += b.parts * experts * sizeof(int);
+    b.losses = reinterpret_cast<float*>(at);
+    at += seqs * ceil_div(experts, 64) * sizeof(float);
+    b.done = reinterpret_cast<unsigned*>(at);
+    at += sizeof(unsigned);
+    b.bytes = at - static_cast<char*>(workspace);
+    return b;
+}
+
+// Tokens [beg, end) of sequence s, kept inside the batch.
+__device__ __forceinline__ void sequence_span(const BalanceArgs& p, int s, int64_t& beg, int64_t& end) {
+    beg = 0;
+    end = p.tokens;
+    if (p.seq_offsets) {
+        beg = p.seq_offsets[s];
+        end = p.seq_offsets[s + 1];
+    }
+    beg = beg < 0 ? 0 : (beg > p.tokens ? p.tokens : beg);
+    end = end < beg ? beg : (end > p.tokens ? p.tokens : end);
+}
+
+// The sequence of part `slot`, its first part and the part's first token;
+// false past the last. Every lane of the wave must take part.
+__device__ __forceinline__ bool find_part(const BalanceArgs& p, int64_t chunk, int64_t slot, int& seq, int64_t& first,
+                                          int64_t& beg, int64_t& end) {
+    const int lane = threadIdx.x & 63;
+    int64_t before = 0;
+    for (int base = 0; base < p.seqs; base += 64) {
+        int64_t b = 0, e = 0;
+        if (base + lane < p.seqs) sequence_span(p, base + lane, b, e);
+        const int parts = (int)((e - b + chunk - 1) / chunk);
+        const int incl = wave_inclusive_sum(parts);
+        const int all = __builtin_amdgcn_readfirstlane(__shfl(incl, 63));
+        if (slot < before + all) {
+            const int l = __ffsll((unsigned long long)__ballot(before + incl > slot)) - 1;
+            seq = __builtin_amdgcn_readfirstlane(base + l);
+            first = before + __builtin_amdgcn_readfirstlane(__shfl(incl - parts, l));
+            sequence_span(p, seq, b, e);
+            beg = b + (slot - first) * chunk;
+            end = min(e, beg + chunk);
+            return true;
+        }
+        before += all;
+    }
+    return false;
+}
+
+template <bool F32>
+__device__ __forceinline__ float load_logit(const void* base, int64_t at) {
+    if constexpr (F32) return static_cast<const float*>(base)[at];
+    return __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[at] << 16);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// log sigmoid(x) = min(x, 0) - log(1 + exp(-|x|)): the scores of a row are a
+// softmax of these, which holds where the sigmoids themselves underflow.
+__device__ __forceinline__ float log_sigmoid(float x) {
+    return fminf(x, 0.0f) - kLn2 * __builtin_amdgcn_logf(1.0f + fast_exp(-fabsf(x)));
+}
+
+// Scores of one row, lane l holding experts l + 64 i; x past the last expert
+// must be -inf. A row without a finite score gets zeros, a NaN reaches every
+// score of its row.
+template <int V, bool SIGMOID>
+__device__ __forceinline__ void row_scores(const float (&x)[V], float (&s)[V]) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        s[i] = SIGMOID ? log_sigmoid(x[i]) : x[i];
+        top = fmaxf(top, s[i]);
+    }
+    top = wave_fmax(top);
+    top = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        s[i] = fast_exp(s[i] - top);
+        sum += s[i];
+    }
+    sum = wave_sum(sum);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] *= inv;
+}
+
+constexpr int kTokensAtOnce = 4;  // rows a wave has in flight
+
+// Whether a token has a valid route, for the wave (every lane gets it).
+__device__ __forceinline__ int valid_route(const BalanceArgs& p, int64_t token) {
+    const int lane = threadIdx.x & 63;
+    int id = -1;
+    if (lane < p.topk) id = p.ids[token * p.topk + lane];
+    return id >= 0 && id < p.experts ? id : -1;
+}
+
+template <int V, bool F32, bool SIGMOID>
+__global__ __launch_bounds__(kThreads) void balance_part_kernel(BalanceArgs p, BalancePlan b) {
+    __shared__ float sums[kWaves][64 * V];
+    __shared__ int hist[64 * V];
+    __shared__ int seen[2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (blockIdx.x == 0 && tid == 0) *b.done = 0;  // for the finish kernel
+    int seq;
+    int64_t first, beg, end;
+    if (!find_part(p, b.chunk, blockIdx.x, seq, first, beg, end)) {
+        if (tid == 0) b.info[blockIdx.x] = Part{-1, 0, 0, 0};
+        return;
+    }
+    if (tid < 64 * V) hist[tid] = 0;
+    if (tid < 2) seen[tid] = 0;
+    __syncthreads();
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    int tokens = 0, routes = 0;
+    // wave w takes the w-th run of the part's tokens
+    const int64_t run = b.chunk / kWaves;
+    const int64_t stop = min(end, beg + (wave + 1) * run);
+    for (int64_t t0 = beg + wave * run; t0 < stop; t0 += kTokensAtOnce) {
+        float x[kTokensAtOnce][V];
+        int id[kTokensAtOnce];
+#pragma unroll
+        for (int u = 0; u < kTokensAtOnce; ++u) {
+            const int64_t t = t0 + u;
+            id[u] = t < stop ? valid_route(p, t) : -1;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane + 64 * i;
+                x[u][i] = t < stop && e < p.experts ? load_logit<F32>(p.logits, t * p.ld + e) : -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kTokensAtOnce; ++u) {
+            const unsigned long long valid = __ballot(id[u] >= 0);
+            if (valid == 0) continue;
+            if (id[u] >= 0) atomicAdd(&hist[id[u]], 1);
+            tokens += 1;
+            routes += __popcll(valid);
+            float s[V];
+            row_scores<V, SIGMOID>(x[u], s);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += s[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) sums[wave][lane + 64 * i] = acc[i];
+    if (lane == 0) {
+        atomicAdd(&seen[0], tokens);
+        atomicAdd(&seen[1], routes);
+    }
+    __syncthreads();
+    if (tid < p.experts) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) v += sums[w][tid];
+        b.sums[(int64_t)blockIdx.x * p.experts + tid] = v;
+        b.counts[(int64_t)blockIdx.x * p.experts + tid] = hist[tid];
+    }
+    if (tid == 0) b.info[blockIdx.x] = Part{seq, (int)first, seen[0], seen[1]};
+}
+
+// Adds up one sequence's parts for 64 experts per workgroup (16 waves share
+// the parts), then writes its counts and coefficients; the last workgroup to
+// finish adds the losses, in their order.
+__global__ __launch_bounds__(kThreads) void balance_finish_kernel(BalanceArgs p, BalancePlan b, int slices) {
+    __shared__ float sums[kWaves][64];
+    __shared__ int counts[kWaves][64];
+    __shared__ int live, seq_first, seq_parts, seq_tokens, seq_routes;
+    __shared__ int last;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int s = (int)(blockIdx.x / slices), e = (int)(blockIdx.x % slices) * 64 + lane;
+    if (tid == 0) live = seq_first = seq_parts = seq_tokens = seq_routes = 0;
+    __syncthreads();
+    // every sequence's totals, from its first part on
+    for (int64_t i = tid; i < b.parts; i += kThreads) {
+        const Part a = b.info[i];
+        if (a.seq < 0 || a.first != i) continue;
+        int tokens = 0, routes = 0, n = 0;
+        for (int64_t j = i; j < b.parts; ++j, ++n) {
+            const Part q = b.info[j];
+            if (q.seq != a.seq) break;
+            tokens += q.tokens;
+            routes += q.routes;
+        }
+        if (tokens > 0) atomicAdd(&live, 1);
+        if (a.seq == s) {
+            seq_first = (int)i;
+            seq_parts = n;
+            seq_tokens = tokens;
+            seq_routes = routes;
+        }
+    }
+    __syncthreads();
+    float sum = 0.0f;
+    int count = 0;
+    if (e < p.experts) {
+        for (int i = wave; i < seq_parts; i += kWaves) {
+            const int64_t at = (int64_t)(seq_first + i) * p.experts + e;
+            sum += b.sums[at];
+            count += b.counts[at];
+        }
+    }
+    sums[wave][lane] = sum;
+    counts[wave][lane] = count;
+    __syncthreads();
+    if (wave == 0) {
+        for (int w = 1; w < kWaves; ++w) {
+            sum += sums[w][lane];
+            count += counts[w][lane];
+        }
+        float part = 0.0f;
+        if (e < p.experts) {
+            const float f = seq_tokens > 0 ? p.alpha * (float)p.experts * (float)count / (float)seq_routes : 0.0f;
+            const float w = seq_tokens > 0 ? f / ((float)seq_tokens * (float)live) : 0.0f;
+            p.counts[(int64_t)s * p.experts + e] = count;
+            p.coef[(int64_t)s * p.experts + e] = w;
+            part = w * sum;
+        }
+        part = wave_sum(part);
+        if (lane == 0) {
+            __hip_atomic_store(&b.losses[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            last = __hip_atomic_fetch_add(b.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (!last || wave != 0) return;
+    float v = 0.0f;
+    for (unsigned i = lane; i < gridDim.x; i += 64)
+        v += __hip_atomic_load(&b.losses[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    v = wave_sum(v);
+    if (lane == 0) *p.loss = v;
+}
+
+template <int V, bool F32, bool SIGMOID>
+__global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs p) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * kTokensAtOnce;
+    if (t0 >= p.tokens) return;
+    float x[kTokensAtOnce][V];
+    int id[kTokensAtOnce];
+#pragma unroll
+    for (int u = 0; u < kTokensAtOnce; ++u) {
+        const int64_t t = t0 + u;
+        id[u] = t < p.tokens ? valid_route(p, t) : -1;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 64 * i;
+            x[u][i] = t < p.tokens && e < p.experts ? load_logit<F32>(p.logits, t * p.ld + e) : -INFINITY;
+        }
+    }
+    const float g = p.grad ? *p.grad : 1.0f;
+    // the sequence of the first row: the last one that starts at or before it
+    int seq = 0;
+    if (p.seq_offsets) {
+        int hi = p.seqs;  // seq_offsets[seq] <= t0 < seq_offsets[hi]
+        while (hi - seq > 1) {
+            const int mid = (seq + hi) / 2;
+            if (p.seq_offsets[mid] <= t0) seq = mid; else hi = mid;
+        }
+    }
+    float w[V];
+    int have = -1;
+#pragma unroll
+    for (int u = 0; u < kTokensAtOnce; ++u) {
+        const int64_t t = t0 + u;
+        if (t >= p.tokens) break;
+        if (p.seq_offsets)
+            while (seq + 1 < p.seqs && p.seq_offsets[seq + 1] <= t) ++seq;
+        float d[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = 0.0f;
+        if (__ballot(id[u] >= 0) != 0) {
+            if (have != seq) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int e = lane + 64 * i;
+                    w[i] = e < p.experts ? p.coef[(int64_t)seq * p.experts + e] : 0.0f;
+                }
+                have = seq;
+            }
+            float s[V];
+            row_scores<V, SIGMOID>(x[u], s);
+            float dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) dot += s[i] * w[i];
+            dot = wave_sum(dot);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                d[i] = g * s[i] * (w[i] - dot);
+                if (SIGMOID) d[i] *= 1.0f / (1.0f + fast_exp(x[u][i]));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 64 * i;
+            if (e >= p.experts) continue;
+            if constexpr (F32)
+                static_cast<float*>(p.dlogits)[t * p.ld_d + e] = d[i];
+            else
+                static_cast<uint16_t*>(p.dlogits)[t * p.ld_d + e] = (uint16_t)pack_bf16x2(d[i], 0.0f);
+        }
+    }
+}
+
+// One launch for the values-per-lane, type and score of the arguments.
+template <int V, class F>
+hipError_t with_types(const BalanceArgs& p, F&& launch) {
+    if (p.f32) {
+        if (p.sigmoid) launch(std::integral_constant<int, V>{}, std::true_type{}, std::true_type{});
+        else launch(std::integral_constant<int, V>{}, std::true_type{}, std::false_type{});
+    } else {
+        if (p.sigmoid) launch(std::integral_constant<int, V>{}, std::false_type{}, std::true_type{});
+        else launch(std::integral_constant<int, V>{}, std::false_type{}, std::false_type{});
+    }
+    return hipGetLastError();
+}
+
+template <class F>
+hipError_t with_width(const BalanceArgs& p, F&& launch) {
+    if (p.experts <= 64) return with_types<1>(p, launch);
+    if (p.experts <= 128) return with_types<2>(p, launch);
+    if (p.experts <= 256) return with_types<4>(p, launch);
+    if (p.experts <= 512) return with_types<8>(p, launch);
+    return with_types<16>(p, launch);
+}
+
+}  // namespace
+
+hipError_t launch_dispatch(const DispatchArgs& p, hipStream_t stream) {
+    const dim3 block(kThreads);
+    int64_t parts = ceil_div(p.routes, kThreads);
+    if (parts > kDispatchParts) parts = kDispatchParts;
+    // one workgroup does it all while its waves stay within 8 rounds of 64
+    // routes: a second launch costs more
+    if (p.routes <= 8 * kThreads) {
+        const int64_t per_part = ceil_div(p.routes > 0 ? p.routes : 1, kThreads) * kThreads;
+        hipLaunchKernelGGL((dispatch_place_kernel<true>), dim3(1), block, 0, stream, p, per_part, 1);
+        return hipGetLastError();
+    }
+    const int64_t per_part = ceil_div(ceil_div(p.routes, parts), kThreads) * kThreads;
+    parts = ceil_div(p.routes, per_part);
+    hipLaunchKernelGGL(dispatch_count_kernel, dim3((unsigned)parts), block, 0, stream, p, per_part);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((dispatch_place_kernel<false>), dim3((unsigned)parts), block, 0, stream, p, per_part, (int)parts);
+    return hipGetLastError();
+}
+
+int64_t balance_workspace_bytes(int64_t tokens, int64_t experts, int64_t seqs) {
+    return plan_of(tokens, experts, seqs, nullptr).bytes;
+}
+
+hipError_t launch_balance(const BalanceArgs& p, hipStream_t stream) {
+    const BalancePlan b = plan_of(p.tokens, p.experts, p.seqs, p.workspace);
+    const hipError_t e = with_width(p, [&](auto v, auto f32, auto sigmoid) {
+        hipLaunchKernelGGL((balance_part_kernel<decltype(v)::value, decltype(f32)::value, decltype(sigmoid)::value>),
+                           dim3((unsigned)b.parts), dim3(kThreads), 0, stream, p, b);
+    });
+    if (e != hipSuccess) return e;
+    const int slices = (int)ceil_div(p.experts, 64);
+    hipLaunchKernelGGL(balance_finish_kernel, dim3((unsigned)(p.seqs * slices)), dim3(kThreads), 0, stream, p, b, slices);
+    return hipGetLastError();
+}
+
+hipError_t launch_balance_backward(const BalanceArgs& p, hipStream_t stream) {
+    const dim3 grid((unsigned)ceil_div(p.tokens, 4 * kTokensAtOnce));
+    return with_width(p, [&](auto v, auto f32, auto sigmoid) {
+        hipLaunchKernelGGL((balance_backward_kernel<decltype(v)::value, decltype(f32)::value, decltype(sigmoid)::value>),
+                           grid, dim3(256), 0, stream, p);
+    });
+}
+
+}  // namespace moe
+}  // namespace fp8q

@@ -547,5 +547,6 @@ int fp8q_last_hip_error(void);
 #endif
 
 #include "fp8q_mx4.h" /* FP4 microscaling quantization and products */
+#include "fp8q_moe.h" /* MoE routing: row layout, balance loss */
 
 #endif /* FP8Q_H */
