@@ -77,8 +77,8 @@ hipError_t launch_quant_scatter(const ScatterArgs& p, hipStream_t stream);
 hipError_t launch_dequant(const DequantArgs& p, hipStream_t stream);
 
 struct GemmArgs {
-    int64_t m, n;
-    int64_t kt;  // K tiles
+    int32_t m, n;
+    int32_t kt;  // K tiles
     const uint8_t* a;
     int64_t ld_a;  // row tiles between K tiles
     const uint32_t* a_scale;

@@ -40,6 +40,7 @@ int check_gemm(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t ld_a, 
                int64_t ld_as, const uint8_t* b, int64_t ld_b, const uint32_t* b_scale, int64_t ld_bs, const void* c,
                int64_t ldc, int out_dtype) {
     if (!c) return FP8Q_ERR_NULL;
+    if (m > FP4Q_MAX_GEMM_ROWS || n > FP4Q_MAX_GEMM_ROWS || k > FP4Q_MAX_GEMM_K) return FP8Q_ERR_SHAPE;
     if (k > 0) {
         int st = check_matrix(a, ld_a, a_scale, ld_as, m, k);
         if (st == FP8Q_OK) st = check_matrix(b, ld_b, b_scale, ld_bs, n, k);
@@ -54,7 +55,7 @@ GemmArgs gemm_args(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t ld
                    int64_t ld_as, const uint8_t* b, int64_t ld_b, const uint32_t* b_scale, int64_t ld_bs, void* c,
                    int64_t ldc, int out_dtype) {
     GemmArgs p = {};
-    p.m = m; p.n = n; p.kt = tiles_of(k, kTileK);
+    p.m = (int32_t)m; p.n = (int32_t)n; p.kt = (int32_t)tiles_of(k, kTileK);
     p.a = a; p.ld_a = ld_a; p.a_scale = a_scale; p.ld_as = ld_as;
     p.b = b; p.ld_b = ld_b; p.b_scale = b_scale; p.ld_bs = ld_bs;
     p.c = c; p.ldc = ldc; p.out_f32 = out_dtype == FP8Q_OUT_F32;
@@ -162,7 +163,7 @@ int fp4_grouped_gemm_mx(int32_t groups, const int32_t* group_offsets, const int3
     if (!group_offsets) return FP8Q_ERR_NULL;
     const int st = check_gemm(m_total, n, k, a, ld_a, a_scale, ld_as, b, ld_b, b_scale, ld_bs, c, ldc, out_dtype);
     if (st != FP8Q_OK) return st;
-    if (m_total % kTileRows != 0 || m_total > 0x7FFFFFFFLL || stride_b < 0 || stride_bs < 0) return FP8Q_ERR_SHAPE;
+    if (m_total % kTileRows != 0 || stride_b < 0 || stride_bs < 0) return FP8Q_ERR_SHAPE;
     if (mul_limit(groups, stride_b, kMaxBytes) < 0 || mul_limit(groups, stride_bs, kMaxBytes / 4) < 0)
         return FP8Q_ERR_SHAPE;
     if (!is_aligned(group_offsets, 4) || !is_aligned(group_rows, 4) || stride_b % 16 != 0) return FP8Q_ERR_ALIGN;

@@ -11,6 +11,8 @@
 
 #include "fp8q_device.h"
 
+#include <type_traits>
+
 namespace fp8q {
 namespace mx4 {
 namespace {
@@ -39,8 +41,10 @@ __device__ __forceinline__ int lane_scale_word(int lane) { return 4 * (lane & 15
 
 // The rows of one output tile: [m0, row_hi) are stored, those from real_end
 // on as zeros (padding of an expert's segment).
+// (Row and column numbers are 32-bit: the scalar unit has no 64-bit compare,
+// and a buffer resource must stay in scalar registers.)
 struct Rows {
-    int64_t m0, row_hi, real_end;
+    int m0, row_hi, real_end;
     int expert;
 };
 
@@ -50,42 +54,39 @@ struct Rows {
 // wave: lane l takes segment base + l, a running sum gives the tiles before
 // it. Every lane of the wave must take part.
 template <int BM>
-__device__ __forceinline__ bool grouped_rows(const GemmArgs& p, int64_t slot, Rows& t) {
+__device__ __forceinline__ bool grouped_rows(const GemmArgs& p, int slot, Rows& t) {
     const int lane = threadIdx.x & 63;
     for (int base = 0; base <= p.groups; base += 64) {
         const int e = base + lane;
-        int64_t beg = 0, end = 0;
+        int beg = 0, end = 0;
         if (e <= p.groups) {
             beg = p.group_offsets[e];
             end = e < p.groups ? p.group_offsets[e + 1] : p.m;
         }
-        // offsets that break the contract must not move stores outside C
-        beg = beg < 0 ? 0 : (beg > p.m ? p.m : beg);
-        end = end < beg ? beg : (end > p.m ? p.m : end);
-        const int tiles = (int)((end - beg + BM - 1) / BM);
+        // offsets that break the contract must not move accesses outside A
+        // and C: whole row tiles of [0, m)
+        beg = min(max(beg, 0), p.m) & ~15;
+        end = min(max(end, beg), p.m);
+        const int tiles = (end - beg + BM - 1) / BM;
         int incl = tiles;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int u = __shfl_up(incl, d);
             if (lane >= d) incl += u;
         }
-        const int chunk = __builtin_amdgcn_readfirstlane(__shfl(incl, 63));
+        const int chunk = __builtin_amdgcn_readlane(incl, 63);
         if (slot < chunk) {
             const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(incl > slot)) - 1);
-            const int before = __shfl(incl - tiles, l);
-            const int64_t seg = __shfl((int)beg, l), seg_end = __shfl((int)end, l);
-            t.expert = __builtin_amdgcn_readfirstlane(base + l);
+            const int before = __builtin_amdgcn_readlane(incl - tiles, l);
+            const int seg = __builtin_amdgcn_readlane(beg, l), seg_end = __builtin_amdgcn_readlane(end, l);
+            t.expert = base + l;
             t.m0 = seg + (slot - before) * BM;
             t.row_hi = min(seg_end, t.m0 + BM);
-            int64_t real = seg;  // no expert: nothing is real
+            t.real_end = seg;  // no expert: nothing is real
             if (t.expert < p.groups) {
-                real = seg_end;
-                if (p.group_rows) {
-                    const int64_t rows = max(p.group_rows[t.expert], 0);
-                    real = min(seg + rows, seg_end);
-                }
+                t.real_end = seg_end;
+                if (p.group_rows) t.real_end = seg + min(max(p.group_rows[t.expert], 0), seg_end - seg);
             }
-            t.real_end = real;
             return true;
         }
         slot -= chunk;
@@ -94,9 +95,9 @@ __device__ __forceinline__ bool grouped_rows(const GemmArgs& p, int64_t slot, Ro
 }
 
 template <bool F32>
-__device__ __forceinline__ void store4(const GemmArgs& p, int64_t m, int64_t n, v4f v) {
+__device__ __forceinline__ void store4(const GemmArgs& p, int m, int n, v4f v) {
     if constexpr (F32) {
-        float* const c = static_cast<float*>(p.c) + m * p.ldc + n;
+        float* const c = static_cast<float*>(p.c) + (int64_t)m * p.ldc + n;
         if (p.c_vec && n + 4 <= p.n) {
             *reinterpret_cast<v4f*>(c) = v;
         } else {
@@ -105,7 +106,7 @@ __device__ __forceinline__ void store4(const GemmArgs& p, int64_t m, int64_t n, 
                 if (n + r < p.n) c[r] = v[r];
         }
     } else {
-        uint16_t* const c = static_cast<uint16_t*>(p.c) + m * p.ldc + n;
+        uint16_t* const c = static_cast<uint16_t*>(p.c) + (int64_t)m * p.ldc + n;
         const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
         if (p.c_vec && n + 4 <= p.n) {
             *reinterpret_cast<uint2*>(c) = make_uint2(lo, hi);
@@ -127,10 +128,10 @@ __device__ __forceinline__ void store4(const GemmArgs& p, int64_t m, int64_t n, 
 constexpr int kMaxWaves = 16;
 
 template <int MS, bool F32, bool GROUPED>
-__global__ __launch_bounds__(64 * kMaxWaves) void gemm_rows_kernel(GemmArgs p, int64_t tiles_n) {
+__global__ __launch_bounds__(64 * kMaxWaves) void gemm_rows_kernel(GemmArgs p, int tiles_n) {
     extern __shared__ v4f partial[];  // [waves][MS][64]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int64_t tn = (int64_t)blockIdx.x % tiles_n, tm = (int64_t)blockIdx.x / tiles_n;
+    const int tn = blockIdx.x % tiles_n, tm = blockIdx.x / tiles_n;
     Rows t;
     if constexpr (GROUPED) {
         if (!grouped_rows<16 * MS>(p, tm, t)) return;
@@ -144,14 +145,16 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemm_rows_kernel(GemmArgs p, i
     if (t.m0 < t.real_end) {
         const uint8_t* const qa = p.a + lane_code_offset(lane);
         const uint32_t* const sa = p.a_scale + lane_scale_word(lane);
-        const uint8_t* const qb = p.b + (GROUPED ? t.expert * p.stride_b : 0) + tn * kTileBytes + lane_code_offset(lane);
+        const uint8_t* const qb = p.b + (GROUPED ? t.expert * p.stride_b : 0) + (int64_t)tn * kTileBytes + lane_code_offset(lane);
         const uint32_t* const sb =
-            p.b_scale + (GROUPED ? t.expert * p.stride_bs : 0) + tn * kScaleWords + lane_scale_word(lane);
+            p.b_scale + (GROUPED ? t.expert * p.stride_bs : 0) + (int64_t)tn * kScaleWords + lane_scale_word(lane);
+        const int kt_end = p.kt;
         // row tiles past the last real row are loaded from it and not stored
-        int64_t rt[MS];
+        int rt[MS];
 #pragma unroll
         for (int s = 0; s < MS; ++s) rt[s] = min(t.m0 / 16 + s, (t.real_end - 1) / 16);
-        for (int64_t g = wave; g * kGroupTiles < p.kt; g += waves) {
+        for (int64_t g = wave; g * kGroupTiles < kt_end; g += waves) {
+            const int left = kt_end - (int)g * kGroupTiles;  // K tiles from here on
             const uint32_t swb = sb[g * p.ld_bs * kScaleWords];
             uint32_t swa[MS];
 #pragma unroll
@@ -160,7 +163,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemm_rows_kernel(GemmArgs p, i
 #pragma unroll
             for (int i = 0; i < kGroupTiles; ++i) {
                 // past the last K tile the products are skipped below
-                const int64_t kt = min(g * kGroupTiles + i, p.kt - 1);
+                const int64_t kt = g * kGroupTiles + min(i, left - 1);
                 fb[i] = *reinterpret_cast<const v4i*>(qb + kt * p.ld_b * kTileBytes);
 #pragma unroll
                 for (int s = 0; s < MS; ++s)
@@ -168,15 +171,15 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemm_rows_kernel(GemmArgs p, i
             }
 #pragma unroll
             for (int s = 0; s < MS; ++s) acc[s] = mfma_tile<0>(fb[0], fa[0][s], acc[s], swb, swa[s]);
-            if (g * kGroupTiles + 1 < p.kt) {
+            if (left > 1) {
 #pragma unroll
                 for (int s = 0; s < MS; ++s) acc[s] = mfma_tile<1>(fb[1], fa[1][s], acc[s], swb, swa[s]);
             }
-            if (g * kGroupTiles + 2 < p.kt) {
+            if (left > 2) {
 #pragma unroll
                 for (int s = 0; s < MS; ++s) acc[s] = mfma_tile<2>(fb[2], fa[2][s], acc[s], swb, swa[s]);
             }
-            if (g * kGroupTiles + 3 < p.kt) {
+            if (left > 3) {
 #pragma unroll
                 for (int s = 0; s < MS; ++s) acc[s] = mfma_tile<3>(fb[3], fa[3][s], acc[s], swb, swa[s]);
             }
@@ -189,7 +192,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemm_rows_kernel(GemmArgs p, i
         v4f v = partial[i];
         for (int w = 1; w < waves; ++w) v += partial[w * MS * 64 + i];
         const int l = i & 63;
-        const int64_t m = t.m0 + (i >> 6) * 16 + (l & 15), n = tn * 16 + 4 * (l >> 4);
+        const int m = t.m0 + (i >> 6) * 16 + (l & 15), n = tn * 16 + 4 * (l >> 4);
         if (m >= t.row_hi) continue;
         if (m >= t.real_end) v = v4f{0.f, 0.f, 0.f, 0.f};
         store4<F32>(p, m, n, v);
@@ -198,9 +201,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemm_rows_kernel(GemmArgs p, i
 
 template <int MS, bool GROUPED>
 hipError_t dispatch_rows(const GemmArgs& p, int64_t tiles_m, hipStream_t stream) {
-    const int64_t tiles_n = (p.n + 15) / 16, kg = (p.kt + kGroupTiles - 1) / kGroupTiles;
-    const int64_t rounds = kg > 0 ? (kg + kMaxWaves - 1) / kMaxWaves : 1;
-    const int waves = kg > 0 ? (int)((kg + rounds - 1) / rounds) : 1;
+    const int tiles_n = (p.n + 15) / 16, kg = (p.kt + kGroupTiles - 1) / kGroupTiles;
+    const int rounds = kg > 0 ? (kg + kMaxWaves - 1) / kMaxWaves : 1;
+    const int waves = kg > 0 ? (kg + rounds - 1) / rounds : 1;
     const dim3 grid((unsigned)(tiles_m * tiles_n)), block(64 * waves);
     const size_t lds = (size_t)waves * MS * 64 * sizeof(v4f);
     if (p.out_f32)
@@ -210,12 +213,271 @@ hipError_t dispatch_rows(const GemmArgs& p, int64_t tiles_m, hipStream_t stream)
     return hipGetLastError();
 }
 
+// ------------------------------------------------------------ many rows
+
+// s_waitcnt with vmcnt = N and the other counters left at their maxima
+// (lgkmcnt, bits 11:8, at 0: the wave's own LDS reads are done too).
+constexpr int waitcnt_vm(int n) { return 0x0070 | (n & 15) | ((n >> 4) << 14); }
+
+// LDS-DMA copy of 1 KB by a wave: 16 bytes from each lane's src to dst + 16 *
+// lane (dst is wave-uniform).
+__device__ __forceinline__ void copy_1k(const void* src, void* dst) {
+    __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 16, 0, 0);
+}
+
+// LDS of the tiled kernels: four stages of one K tile (A tiles, then B tiles)
+// and two of scale words, each an array of its own, so that the compiler can
+// tell a stage being filled from the one being read.
+constexpr int kStages = 4;
+constexpr int kMaxStage = 32 * kTileBytes;
+constexpr int kMaxScaleStage = 32 * kScaleWords;
+__shared__ __attribute__((aligned(1024))) uint8_t lds_t0[kMaxStage];
+__shared__ __attribute__((aligned(1024))) uint8_t lds_t1[kMaxStage];
+__shared__ __attribute__((aligned(1024))) uint8_t lds_t2[kMaxStage];
+__shared__ __attribute__((aligned(1024))) uint8_t lds_t3[kMaxStage];
+__shared__ __attribute__((aligned(1024))) uint32_t lds_s0[kMaxScaleStage];
+__shared__ __attribute__((aligned(1024))) uint32_t lds_s1[kMaxScaleStage];
+
+template <int S>
+__device__ __forceinline__ uint8_t* stage_tiles() {
+    if constexpr (S == 0) return lds_t0;
+    else if constexpr (S == 1) return lds_t1;
+    else if constexpr (S == 2) return lds_t2;
+    else return lds_t3;
+}
+template <int S>
+__device__ __forceinline__ uint32_t* stage_scales() {
+    if constexpr (S == 0) return lds_s0;
+    else return lds_s1;
+}
+
+// Output tile `slot` of a dense problem: within an XCD (see below) slots walk
+// bands of four tile rows, so that the tiles resident together share A and B
+// panels in the XCD's L2.
+template <int BM, int BN>
+__device__ __forceinline__ bool dense_slot(const GemmArgs& p, int slot, int& tm, int& tn) {
+    const int tiles_m = (p.m + BM - 1) / BM, tiles_n = (p.n + BN - 1) / BN;
+    if (slot >= tiles_m * tiles_n) return false;
+    constexpr int G = 4;
+    const int band = slot / (G * tiles_n), first = band * G;
+    const int gm = min(tiles_m - first, G), within = slot - band * G * tiles_n;
+    tm = __builtin_amdgcn_readfirstlane(first + within % gm);  // (divisions leave the scalar unit)
+    tn = __builtin_amdgcn_readfirstlane(within / gm);
+    return true;
+}
+
+// A workgroup of 4 waves (2 x 2) owns 32 TM x 32 TN outputs, a wave 16 TM x
+// 16 TN of them: per K tile it reads TM + TN tiles from LDS and issues TM TN
+// MFMAs. While the MFMAs of K tile j run from registers, the fragments of j + 1
+// are read from LDS, and the copies of j + 2 .. j + 4 are in flight (LDS-DMA,
+// 1 KB contiguous per instruction, linear in LDS). One barrier per K tile: it
+// says that everybody's copies of tile j + 1 have landed and that everybody
+// has read tile j, whose stage the copies of tile j + 4 then overwrite.
+template <int TM, int TN, bool F32, bool GROUPED>
+__global__ __launch_bounds__(256, TM * TN > 32 ? 1 : 2) void gemm_tiles_kernel(GemmArgs p) {
+    constexpr int BM = 32 * TM, BN = 32 * TN;
+    constexpr int kATiles = 2 * TM, kBTiles = 2 * TN;
+    constexpr int kCopies = (kATiles + kBTiles) / 4;                 // 1 KB copies per wave and K tile
+    constexpr int kScaleCopies = (kATiles + kBTiles + 15) / 16;      // 1 KB (4 row tiles) per wave and K group
+    static_assert(kATiles % 4 == 0 && kBTiles % 4 == 0 && (kATiles + kBTiles) % 16 == 0,
+                  "every wave makes the same number of copies");
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+
+    // Workgroup b runs on XCD b % 8.
+    Rows t;
+    int tn;
+    const int slot = (int)((blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8);
+    if constexpr (GROUPED) {
+        const int tiles_n = (p.n + BN - 1) / BN;
+        tn = __builtin_amdgcn_readfirstlane(slot % tiles_n);
+        if (!grouped_rows<BM>(p, __builtin_amdgcn_readfirstlane(slot / tiles_n), t)) return;
+    } else {
+        int tm;
+        if (!dense_slot<BM, BN>(p, slot, tm, tn)) return;
+        t = Rows{tm * BM, min(p.m, (tm + 1) * BM), p.m, 0};
+    }
+    const int n0 = tn * BN;
+    const int kt = p.kt;
+
+    v4f acc[TN][TM];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int i = 0; i < TM; ++i) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    if (t.m0 < t.real_end && kt > 0) {
+        // Copies: wave w fills tiles [kATiles / 4 * w, + kATiles / 4) of a
+        // stage's A part and the same of its B part. Row tiles past the last
+        // one (or past the expert's real rows) repeat it: loaded, never
+        // stored. All but lane * 16 is wave-uniform.
+        constexpr int kAW = kATiles / 4, kBW = kBTiles / 4;
+        const int a_last = (min(t.real_end, t.row_hi) - 1) / 16 - t.m0 / 16;
+        const int b_last = (p.n - 1) / 16 - n0 / 16;
+        int off_a[kAW], off_b[kBW];
+#pragma unroll
+        for (int c = 0; c < kAW; ++c) off_a[c] = min(kAW * wave + c, a_last) * kTileBytes;
+#pragma unroll
+        for (int c = 0; c < kBW; ++c) off_b[c] = min(kBW * wave + c, b_last) * kTileBytes;
+        const uint8_t* ga = p.a + (int64_t)(t.m0 / 16) * kTileBytes;
+        const uint8_t* gb = p.b + (GROUPED ? t.expert * p.stride_b : 0) + (int64_t)(n0 / 16) * kTileBytes;
+        const int64_t step_a = p.ld_a * kTileBytes, step_b = p.ld_b * kTileBytes;
+        const uint32_t voff = lane * 16;
+        // copies of the next K tile into `stage`; past the last one they
+        // repeat it (never used), which keeps the count of copies in flight
+        int ahead = 0;
+        auto copy_tiles = [&](auto stage) {
+            uint8_t* const dst = stage_tiles<decltype(stage)::value>();
+#pragma unroll
+            for (int c = 0; c < kAW; ++c) copy_1k(ga + off_a[c] + voff, dst + (kAW * wave + c) * kTileBytes);
+#pragma unroll
+            for (int c = 0; c < kBW; ++c) copy_1k(gb + off_b[c] + voff, dst + (kATiles + kBW * wave + c) * kTileBytes);
+            ++ahead;
+            ga += ahead < kt ? step_a : 0;
+            gb += ahead < kt ? step_b : 0;
+        };
+        // The scale words of a K group: copy c takes row tiles [4 (4 c + wave),
+        // + 4) of the stage, one per 16 lanes, A's first.
+        const int kgs = (kt + kGroupTiles - 1) / kGroupTiles;
+        int s_ahead = 0;
+        const uint32_t* gsa = p.a_scale + (int64_t)(t.m0 / 16) * kScaleWords;
+        const uint32_t* gsb = p.b_scale + (GROUPED ? t.expert * p.stride_bs : 0) + (int64_t)(n0 / 16) * kScaleWords;
+        uint32_t soff[kScaleCopies];
+#pragma unroll
+        for (int c = 0; c < kScaleCopies; ++c) {
+            const int i = 4 * (4 * c + wave) + (lane >> 4);
+            soff[c] = (i < kATiles ? min(i, a_last) : min(i - kATiles, b_last)) * kScaleWords + (lane & 15) * 4;
+        }
+        auto copy_scales = [&](auto stage) {
+            uint32_t* const dst = stage_scales<decltype(stage)::value>();
+#pragma unroll
+            for (int c = 0; c < kScaleCopies; ++c) {
+                const int i = 4 * (4 * c + wave);
+                copy_1k((i < kATiles ? gsa : gsb) + soff[c], dst + i * kScaleWords);
+            }
+            ++s_ahead;
+            gsa += s_ahead < kgs ? p.ld_as * kScaleWords : 0;
+            gsb += s_ahead < kgs ? p.ld_bs * kScaleWords : 0;
+        };
+        const int frag = lane_code_offset(lane), sword = lane_scale_word(lane);
+        auto read_a = [&](auto stage, int i) {
+            return *reinterpret_cast<const v4i*>(stage_tiles<decltype(stage)::value>() + (wm * TM + i) * kTileBytes + frag);
+        };
+        auto read_b = [&](auto stage, int i) {
+            return *reinterpret_cast<const v4i*>(stage_tiles<decltype(stage)::value>() +
+                                                 (kATiles + wn * TN + i) * kTileBytes + frag);
+        };
+        auto read_scales = [&](auto stage, uint32_t (&sa)[TM], uint32_t (&sb)[TN]) {
+            const uint32_t* const s = stage_scales<decltype(stage)::value>() + sword;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) sa[i] = s[(wm * TM + i) * kScaleWords];
+#pragma unroll
+            for (int i = 0; i < TN; ++i) sb[i] = s[(kATiles + wn * TN + i) * kScaleWords];
+        };
+
+        v4i fa[2][TM], fb[2][TN];
+        uint32_t sa[2][TM], sb[2][TN];
+        // The next K tile, j: its MFMAs from register set P % 2; fragments of
+        // j + 1 into the other; copies of j + 4. P = j mod 8 fixes stages and
+        // registers.
+        auto step = [&](auto pos) {
+            constexpr int P = decltype(pos)::value;
+            constexpr int G = P / 4;
+            using Next = std::integral_constant<int, (P + 1) % kStages>;
+            // batches of the two youngest K tiles may still be in flight
+            constexpr int kFlying = 2 * kCopies + (P % 4 == 1 || P % 4 == 2 ? kScaleCopies : 0);
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm(kFlying));
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (P % 4 == 0) copy_scales(std::integral_constant<int, (G + 1) % 2>{});
+            copy_tiles(std::integral_constant<int, P % kStages>{});
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa[(P + 1) % 2][i] = read_a(Next{}, i);
+#pragma unroll
+            for (int i = 0; i < TN; ++i) fb[(P + 1) % 2][i] = read_b(Next{}, i);
+            if constexpr (P % 4 == 3) read_scales(std::integral_constant<int, (G + 1) % 2>{}, sa[(G + 1) % 2], sb[(G + 1) % 2]);
+#pragma unroll
+            for (int n = 0; n < TN; ++n)
+#pragma unroll
+                for (int m = 0; m < TM; ++m)
+                    acc[n][m] = mfma_tile<P % 4>(fb[P % 2][n], fa[P % 2][m], acc[n][m], sb[G][n], sa[G][m]);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        using I0 = std::integral_constant<int, 0>;
+        using I1 = std::integral_constant<int, 1>;
+        using I2 = std::integral_constant<int, 2>;
+        using I3 = std::integral_constant<int, 3>;
+        copy_scales(I0{});
+        copy_tiles(I0{});
+        copy_tiles(I1{});
+        copy_tiles(I2{});
+        copy_tiles(I3{});
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(3 * kCopies));
+        __builtin_amdgcn_s_barrier();
+        read_scales(I0{}, sa[0], sb[0]);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa[0][i] = read_a(I0{}, i);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) fb[0][i] = read_b(I0{}, i);
+        using I4 = std::integral_constant<int, 4>;
+        using I5 = std::integral_constant<int, 5>;
+        using I6 = std::integral_constant<int, 6>;
+        using I7 = std::integral_constant<int, 7>;
+        int j = 0;
+        for (; j + 8 <= kt; j += 8) {
+            step(I0{});
+            step(I1{});
+            step(I2{});
+            step(I3{});
+            step(I4{});
+            step(I5{});
+            step(I6{});
+            step(I7{});
+        }
+        const int rest = kt - j;
+        if (rest > 0) step(I0{});
+        if (rest > 1) step(I1{});
+        if (rest > 2) step(I2{});
+        if (rest > 3) step(I3{});
+        if (rest > 4) step(I4{});
+        if (rest > 5) step(I5{});
+        if (rest > 6) step(I6{});
+        // the last copies land before the LDS can be another workgroup's
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    }
+
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int m = t.m0 + (wm * TM + i) * 16 + (lane & 15);
+        if (m >= t.row_hi) continue;
+        const bool pad = m >= t.real_end;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int n = n0 + (wn * TN + j) * 16 + 4 * (lane >> 4);
+            if (n < p.n) store4<F32>(p, m, n, pad ? v4f{0.f, 0.f, 0.f, 0.f} : acc[j][i]);
+        }
+    }
+}
+
+template <int TM, int TN, bool GROUPED>
+hipError_t dispatch_tiles(const GemmArgs& p, int64_t tiles_m, hipStream_t stream) {
+    const int64_t tiles = tiles_m * ((p.n + 32 * TN - 1) / (32 * TN));
+    const dim3 grid((unsigned)((tiles + 7) / 8 * 8)), block(256);
+    if (p.out_f32)
+        hipLaunchKernelGGL((gemm_tiles_kernel<TM, TN, true, GROUPED>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((gemm_tiles_kernel<TM, TN, false, GROUPED>), grid, block, 0, stream, p);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_gemm(const GemmArgs& p, hipStream_t stream) {
     if (p.m <= 16) return dispatch_rows<1, false>(p, 1, stream);
     if (p.m <= 32) return dispatch_rows<2, false>(p, 1, stream);
-    return dispatch_rows<4, false>(p, (p.m + 63) / 64, stream);
+    if (p.m <= 256) return dispatch_rows<4, false>(p, (p.m + 63) / 64, stream);
+    return dispatch_tiles<8, 8, false>(p, (p.m + 255) / 256, stream);
 }
 
 hipError_t launch_grouped_gemm(const GemmArgs& p, hipStream_t stream) {
@@ -223,7 +485,8 @@ hipError_t launch_grouped_gemm(const GemmArgs& p, hipStream_t stream) {
     const int64_t avg = p.m / p.groups;
     if (avg <= 16) return dispatch_rows<1, true>(p, p.m / 16 + p.groups + 1, stream);
     if (avg <= 32) return dispatch_rows<2, true>(p, p.m / 32 + p.groups + 1, stream);
-    return dispatch_rows<4, true>(p, p.m / 64 + p.groups + 1, stream);
+    if (avg <= 128) return dispatch_rows<4, true>(p, p.m / 64 + p.groups + 1, stream);
+    return dispatch_tiles<8, 8, true>(p, p.m / 256 + p.groups + 1, stream);
 }
 
 }  // namespace mx4

@@ -41,6 +41,14 @@ extern "C" {
 #define FP4Q_TILE_32x1 1 /* blocks along the columns of x: the transposed operand   */
 
 /*
+ * Limits of the products: rows of A, B and C are numbered with 32 bits (a
+ * tile of 256 rows may start at the last one). Codes and scales are addressed
+ * with 64 bits. Larger values return FP8Q_ERR_SHAPE before any launch.
+ */
+#define FP4Q_MAX_GEMM_ROWS 2147483136LL   /* 2^31 - 512: m, n, m_total */
+#define FP4Q_MAX_GEMM_K    137438953472LL /* 2^37                     */
+
+/*
  * fp4_quantize_mx -- bf16 to FP4 codes and scales.
  *
  * x       groups matrices [rows][ld_x], ld_x >= cols, stride_x elements apart
@@ -106,7 +114,7 @@ int fp4_dequantize_mx(const uint8_t *q, int64_t ld_q, const uint32_t *scale, int
  * c           [m][ldc], ldc >= n; out_dtype FP8Q_OUT_BF16 (rounded once, to
  *             nearest even) or FP8Q_OUT_F32. Every element of the m x n window
  *             is written; k == 0 writes zeros (a, b and scales may be NULL).
- * Any m, n, k >= 0 and any ldc. m == 0 or n == 0: returns FP8Q_OK.
+ * Any m, n, k >= 0 within the limits, and any ldc. m == 0 or n == 0: returns FP8Q_OK.
  * Errors: FP8Q_ERR_NULL, FP8Q_ERR_SHAPE, FP8Q_ERR_ALIGN (a, b not 16-byte,
  *         scales not 4-byte, c not element aligned), FP8Q_ERR_ENUM,
  *         FP8Q_ERR_HIP.
@@ -130,7 +138,7 @@ int fp4_gemm_mx(int64_t m, int64_t n, int64_t k, const uint8_t *a, int64_t ld_a,
  *               the rows that it set aside).
  * group_rows    DEVICE int32[groups], 0 <= group_rows[e] <= segment e; NULL:
  *               every row of every segment is real.
- * m_total       rows of A and C, % 16 == 0, < 2^31.
+ * m_total       rows of A and C, % 16 == 0.
  * b, b_scale    expert e's FP4 matrix of n rows at b + e * stride_b (bytes,
  *               % 16 == 0) and b_scale + e * stride_bs (words); strides >= 0.
  * c             [m_total][ldc]; out_dtype as in fp4_gemm_mx.
