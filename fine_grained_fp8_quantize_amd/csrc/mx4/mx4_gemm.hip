@@ -225,6 +225,29 @@ __device__ __forceinline__ void copy_1k(const void* src, void* dst) {
     __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 16, 0, 0);
 }
 
+// acc += (B tile) * (A tile)^T with the accumulator in place in AGPRs. The
+// 256 accumulator registers of a 128 x 128 wave tile are all the AGPRs there
+// are: left to itself, the register allocator gives results other registers
+// than their inputs and copies them back and forth inside the K loop (752
+// copies per 512 MFMAs). The tied operand rules that out. The compiler does
+// not see a matrix instruction here, so it is up to the code that reads
+// accumulators to wait first (mfma_settle).
+template <int T>
+__device__ __forceinline__ void mfma_in_place(v4f& acc, v4i b, v4i a, uint32_t sb, uint32_t sa) {
+#define FP8Q_MFMA(lo, hi)                                                                                         \
+    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" lo "," lo ",0] op_sel_hi:[" hi "," hi \
+                 ",0] cbsz:4 blgp:4"                                                                              \
+                 : "+a"(acc)                                                                                      \
+                 : "v"(b), "v"(a), "v"(sb), "v"(sa))
+    if constexpr (T == 0) FP8Q_MFMA("0", "0");
+    else if constexpr (T == 1) FP8Q_MFMA("1", "0");
+    else if constexpr (T == 2) FP8Q_MFMA("0", "1");
+    else FP8Q_MFMA("1", "1");
+#undef FP8Q_MFMA
+}
+// More wait states than the last MFMA's results take.
+__device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
 // LDS of the tiled kernels: four stages of one K tile (A tiles, then B tiles)
 // and two of scale words, each an array of its own, so that the compiler can
 // tell a stage being filled from the one being read.
@@ -279,6 +302,7 @@ __global__ __launch_bounds__(256, TM * TN > 32 ? 1 : 2) void gemm_tiles_kernel(G
     constexpr int kATiles = 2 * TM, kBTiles = 2 * TN;
     constexpr int kCopies = (kATiles + kBTiles) / 4;                 // 1 KB copies per wave and K tile
     constexpr int kScaleCopies = (kATiles + kBTiles + 15) / 16;      // 1 KB (4 row tiles) per wave and K group
+    static_assert(TM <= TN && kCopies <= TN, "the copies and reads of a K tile fit its rows of MFMAs");
     static_assert(kATiles % 4 == 0 && kBTiles % 4 == 0 && (kATiles + kBTiles) % 16 == 0,
                   "every wave makes the same number of copies");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -326,15 +350,22 @@ __global__ __launch_bounds__(256, TM * TN > 32 ? 1 : 2) void gemm_tiles_kernel(G
         // copies of the next K tile into `stage`; past the last one they
         // repeat it (never used), which keeps the count of copies in flight
         int ahead = 0;
-        auto copy_tiles = [&](auto stage) {
-            uint8_t* const dst = stage_tiles<decltype(stage)::value>();
-#pragma unroll
-            for (int c = 0; c < kAW; ++c) copy_1k(ga + off_a[c] + voff, dst + (kAW * wave + c) * kTileBytes);
-#pragma unroll
-            for (int c = 0; c < kBW; ++c) copy_1k(gb + off_b[c] + voff, dst + (kATiles + kBW * wave + c) * kTileBytes);
+        auto copy_tile = [&](auto stage, int c) {
+            uint8_t* const dst = stage_tiles<decltype(stage)::value>() +
+                                 (c < kAW ? kAW * wave + c : kATiles + kBW * wave + c - kAW) * kTileBytes;
+            const uint8_t* src = c < kAW ? ga + off_a[c] : gb + off_b[c - kAW];
+            asm("" : "+s"(src));  // (keeps the sum with the lane's offset out of vector registers)
+            copy_1k(src + voff, dst);
+        };
+        auto next_tile = [&] {
             ++ahead;
             ga += ahead < kt ? step_a : 0;
             gb += ahead < kt ? step_b : 0;
+        };
+        auto copy_tiles = [&](auto stage) {
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c) copy_tile(stage, c);
+            next_tile();
         };
         // The scale words of a K group: copy c takes row tiles [4 (4 c + wave),
         // + 4) of the stage, one per 16 lanes, A's first.
@@ -391,18 +422,20 @@ __global__ __launch_bounds__(256, TM * TN > 32 ? 1 : 2) void gemm_tiles_kernel(G
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (P % 4 == 0) copy_scales(std::integral_constant<int, (G + 1) % 2>{});
-            copy_tiles(std::integral_constant<int, P % kStages>{});
-#pragma unroll
-            for (int i = 0; i < TM; ++i) fa[(P + 1) % 2][i] = read_a(Next{}, i);
-#pragma unroll
-            for (int i = 0; i < TN; ++i) fb[(P + 1) % 2][i] = read_b(Next{}, i);
             if constexpr (P % 4 == 3) read_scales(std::integral_constant<int, (G + 1) % 2>{}, sa[(G + 1) % 2], sb[(G + 1) % 2]);
+            // one row of MFMAs at a time, with its share of the copies and
+            // fragment reads in front
 #pragma unroll
-            for (int n = 0; n < TN; ++n)
+            for (int n = 0; n < TN; ++n) {
+                if (n < kCopies) copy_tile(std::integral_constant<int, P % kStages>{}, n);
+                fb[(P + 1) % 2][n] = read_b(Next{}, n);
+                if (n < TM) fa[(P + 1) % 2][n] = read_a(Next{}, n);
 #pragma unroll
                 for (int m = 0; m < TM; ++m)
-                    acc[n][m] = mfma_tile<P % 4>(fb[P % 2][n], fa[P % 2][m], acc[n][m], sb[G][n], sa[G][m]);
-            __builtin_amdgcn_sched_barrier(0);
+                    mfma_in_place<P % 4>(acc[n][m], fb[P % 2][n], fa[P % 2][m], sb[G][n], sa[G][m]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            next_tile();
         };
         using I0 = std::integral_constant<int, 0>;
         using I1 = std::integral_constant<int, 1>;
@@ -445,6 +478,7 @@ __global__ __launch_bounds__(256, TM * TN > 32 ? 1 : 2) void gemm_tiles_kernel(G
         if (rest > 6) step(I6{});
         // the last copies land before the LDS can be another workgroup's
         __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        mfma_settle();
     }
 
 #pragma unroll
