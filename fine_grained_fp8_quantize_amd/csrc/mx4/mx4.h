@@ -11,15 +11,16 @@
 // tile 4 kg + t.
 //
 // Why this layout. One tile is exactly what a wave feeds to one operand of
-// v_mfma_scale_f32_16x16x128_f8f6f4 (lane l: 16 bytes, row l % 16, block
-// l / 16), so every copy of it, to LDS or straight to registers, is 1 KB
+// v_mfma_scale_f32_16x16x128_f8f6f4 (a lane: 16 bytes, one block of one
+// row), so every copy of it, to LDS or straight to registers, is 1 KB
 // contiguous: on MI355X such copies run at 47-49 B/clk per CU from L2, where
-// 8 rows x 128 B at a row pitch run at 29-32. The 16 lanes of one block read
-// 16 rows 64 bytes apart; the XOR spreads them over all 64 LDS banks, so a
-// tile read from LDS with ds_read_b128 has no bank conflicts. With K tiles
-// outermost the tiles that a workgroup reads together are one contiguous
-// run, spread over all L2 channels. A lane's scale word serves four K tiles:
-// the MFMA's op_sel picks the byte.
+// 8 rows x 128 B at a row pitch run at 29-32. A row's 64 bytes repeat the LDS
+// banks every four rows; the XOR moves a block of rows four apart to
+// different banks, so that a tile is read from LDS without bank conflicts (in
+// the lane order of mx4_gemm.hip). With K tiles outermost the tiles that a
+// workgroup reads together are one contiguous run, spread over all L2
+// channels. A lane's scale word serves four K tiles: the MFMA's op_sel picks
+// the byte.
 #pragma once
 
 #include <hip/hip_runtime_api.h>

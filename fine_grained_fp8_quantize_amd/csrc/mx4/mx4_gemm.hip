@@ -31,13 +31,25 @@ __device__ __forceinline__ v4f mfma_tile(v4i b, v4i a, v4f acc, uint32_t sb, uin
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bw, aw, acc, kFp4, kFp4, T, (int)sb, T, (int)sa);
 }
 
-// Where lane l's 16 bytes (row l % 16, block l / 16) stand in a tile, and its
-// word among the tile's scale words.
+// Which row of a tile lane l feeds to the MFMA (any order does, as long as
+// the outputs are put back in it). ds_read_b128 serves the lanes 0-3, 12-15,
+// 20-27 of each half wave together, then the other 16: with lanes i = l % 16 of
+// 0-3 and 12-15 on the tile's first eight rows and 4-11 on the last eight,
+// both sets touch all 64 banks once (measured: 4 cycles per read; with rows in
+// lane order the layout's XOR leaves a two-way conflict, 8 cycles).
+__device__ __forceinline__ int lane_row(int i) { return i < 4 ? i : (i < 12 ? i + 4 : i - 8); }
+
+// Where lane l's 16 bytes (row lane_row(l % 16), block l / 16) stand in a
+// tile, and its word among the tile's scale words.
 __device__ __forceinline__ int lane_code_offset(int lane) {
-    const int r = lane & 15;
+    const int r = lane_row(lane & 15);
     return r * 64 + ((lane >> 4) ^ (r >> 2)) * 16;
 }
-__device__ __forceinline__ int lane_scale_word(int lane) { return 4 * (lane & 15) + (lane >> 4); }
+__device__ __forceinline__ int lane_scale_word(int lane) { return 4 * lane_row(lane & 15) + (lane >> 4); }
+// The m of lane l's results inside a 16 x 16 output tile, and the first of
+// its four consecutive n.
+__device__ __forceinline__ int lane_m(int lane) { return lane_row(lane & 15); }
+__device__ __forceinline__ int lane_n(int lane) { return lane_row(4 * (lane >> 4)); }
 
 // The rows of one output tile: [m0, row_hi) are stored, those from real_end
 // on as zeros (padding of an expert's segment).
@@ -192,7 +204,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemm_rows_kernel(GemmArgs p, i
         v4f v = partial[i];
         for (int w = 1; w < waves; ++w) v += partial[w * MS * 64 + i];
         const int l = i & 63;
-        const int m = t.m0 + (i >> 6) * 16 + (l & 15), n = tn * 16 + 4 * (l >> 4);
+        const int m = t.m0 + (i >> 6) * 16 + lane_m(l), n = tn * 16 + lane_n(l);
         if (m >= t.row_hi) continue;
         if (m >= t.real_end) v = v4f{0.f, 0.f, 0.f, 0.f};
         store4<F32>(p, m, n, v);
@@ -483,12 +495,12 @@ __global__ __launch_bounds__(256, TM * TN > 32 ? 1 : 2) void gemm_tiles_kernel(G
 
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        const int m = t.m0 + (wm * TM + i) * 16 + (lane & 15);
+        const int m = t.m0 + (wm * TM + i) * 16 + lane_m(lane);
         if (m >= t.row_hi) continue;
         const bool pad = m >= t.real_end;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            const int n = n0 + (wn * TN + j) * 16 + 4 * (lane >> 4);
+            const int n = n0 + (wn * TN + j) * 16 + lane_n(lane);
             if (n < p.n) store4<F32>(p, m, n, pad ? v4f{0.f, 0.f, 0.f, 0.f} : acc[j][i]);
         }
     }
