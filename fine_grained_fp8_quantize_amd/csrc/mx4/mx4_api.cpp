@@ -60,6 +60,7 @@ GemmArgs gemm_args(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t ld
     p.b = b; p.ld_b = ld_b; p.b_scale = b_scale; p.ld_bs = ld_bs;
     p.c = c; p.ldc = ldc; p.out_f32 = out_dtype == FP8Q_OUT_F32;
     p.c_vec = ldc % 4 == 0 && is_aligned(c, p.out_f32 ? 16 : 8);
+    p.c_vec16 = ldc % (p.out_f32 ? 4 : 8) == 0 && is_aligned(c, 16);
     return p;
 }
 

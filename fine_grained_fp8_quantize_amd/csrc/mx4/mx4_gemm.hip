@@ -12,6 +12,7 @@
 #include "fp8q_device.h"
 
 #include <type_traits>
+#include <utility>
 
 namespace fp8q {
 namespace mx4 {
@@ -20,6 +21,10 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+
+// Lambdas of the kernels: one that is not inlined would put the register
+// arrays that it captures into memory.
+#define FP8Q_INLINE __attribute__((always_inline))
 
 constexpr int kFp4 = 4;  // the MFMA's operand format code of E2M1
 
@@ -231,10 +236,18 @@ hipError_t dispatch_rows(const GemmArgs& p, int64_t tiles_m, hipStream_t stream)
 // (lgkmcnt, bits 11:8, at 0: the wave's own LDS reads are done too).
 constexpr int waitcnt_vm(int n) { return 0x0070 | (n & 15) | ((n >> 4) << 14); }
 
-// LDS-DMA copy of 1 KB by a wave: 16 bytes from each lane's src to dst + 16 *
-// lane (dst is wave-uniform).
-__device__ __forceinline__ void copy_1k(const void* src, void* dst) {
-    __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 16, 0, 0);
+// LDS-DMA copy of 1 KB by a wave: 16 bytes from src + voff (lane * 16) + OFF
+// to dst + OFF + 16 * lane. src and dst are wave-uniform; the instruction's
+// own offset applies to both, so neighbouring copies need no new addresses.
+template <int OFF>
+__device__ __forceinline__ void copy_1k(const void* src, uint32_t voff, void* dst) {
+    asm("" : "+v"(voff));  // (its zero extension is then seen here: scalar base + 32-bit lane offset)
+    __builtin_amdgcn_global_load_lds(static_cast<const uint8_t*>(src) + voff, (lds_void*)dst, 16, OFF, 0);
+}
+
+template <int... Is, class F>
+__device__ __forceinline__ void unroll(std::integer_sequence<int, Is...>, F&& f) {
+    (f(std::integral_constant<int, Is>{}), ...);
 }
 
 // acc += (B tile) * (A tile)^T with the accumulator in place in AGPRs. The
@@ -260,9 +273,9 @@ __device__ __forceinline__ void mfma_in_place(v4f& acc, v4i b, v4i a, uint32_t s
 // More wait states than the last MFMA's results take.
 __device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
-// LDS of the tiled kernels: four stages of one K tile (A tiles, then B tiles)
-// and two of scale words, each an array of its own, so that the compiler can
-// tell a stage being filled from the one being read.
+// LDS of the tiled kernels: four stages of one K tile (A tiles, then B
+// tiles), each an array of its own, so that the compiler can tell a stage being
+// filled from the one being read, and one of scale words.
 constexpr int kStages = 4;
 constexpr int kMaxStage = 32 * kTileBytes;
 constexpr int kMaxScaleStage = 32 * kScaleWords;
@@ -270,8 +283,7 @@ __shared__ __attribute__((aligned(1024))) uint8_t lds_t0[kMaxStage];
 __shared__ __attribute__((aligned(1024))) uint8_t lds_t1[kMaxStage];
 __shared__ __attribute__((aligned(1024))) uint8_t lds_t2[kMaxStage];
 __shared__ __attribute__((aligned(1024))) uint8_t lds_t3[kMaxStage];
-__shared__ __attribute__((aligned(1024))) uint32_t lds_s0[kMaxScaleStage];
-__shared__ __attribute__((aligned(1024))) uint32_t lds_s1[kMaxScaleStage];
+__shared__ __attribute__((aligned(1024))) uint32_t lds_scales[kMaxScaleStage];
 
 template <int S>
 __device__ __forceinline__ uint8_t* stage_tiles() {
@@ -280,12 +292,6 @@ __device__ __forceinline__ uint8_t* stage_tiles() {
     else if constexpr (S == 2) return lds_t2;
     else return lds_t3;
 }
-template <int S>
-__device__ __forceinline__ uint32_t* stage_scales() {
-    if constexpr (S == 0) return lds_s0;
-    else return lds_s1;
-}
-
 // Output tile `slot` of a dense problem: within an XCD (see below) slots walk
 // bands of four tile rows, so that the tiles resident together share A and B
 // panels in the XCD's L2.
@@ -344,40 +350,37 @@ __global__ __launch_bounds__(256, TM * TN > 32 ? 1 : 2) void gemm_tiles_kernel(G
 
     if (t.m0 < t.real_end && kt > 0) {
         // Copies: wave w fills tiles [kATiles / 4 * w, + kATiles / 4) of a
-        // stage's A part and the same of its B part. Row tiles past the last
-        // one (or past the expert's real rows) repeat it: loaded, never
-        // stored. All but lane * 16 is wave-uniform.
+        // stage's A part and the same of its B part. At the edge of the matrix
+        // (or of an expert's real rows) row tiles past the last one repeat it:
+        // loaded, never stored. What differs between the wave's copies is in
+        // the lanes' offsets, so a K tile costs one address per operand.
         constexpr int kAW = kATiles / 4, kBW = kBTiles / 4;
+        constexpr int kBack = (kAW > kBW ? kAW : kBW) * kTileBytes;  // keeps the offsets positive
         const int a_last = (min(t.real_end, t.row_hi) - 1) / 16 - t.m0 / 16;
         const int b_last = (p.n - 1) / 16 - n0 / 16;
-        int off_a[kAW], off_b[kBW];
-#pragma unroll
-        for (int c = 0; c < kAW; ++c) off_a[c] = min(kAW * wave + c, a_last) * kTileBytes;
-#pragma unroll
-        for (int c = 0; c < kBW; ++c) off_b[c] = min(kBW * wave + c, b_last) * kTileBytes;
-        const uint8_t* ga = p.a + (int64_t)(t.m0 / 16) * kTileBytes;
-        const uint8_t* gb = p.b + (GROUPED ? t.expert * p.stride_b : 0) + (int64_t)(n0 / 16) * kTileBytes;
+        const uint8_t* ga = p.a + (int64_t)(t.m0 / 16) * kTileBytes - kBack;
+        const uint8_t* gb = p.b + (GROUPED ? t.expert * p.stride_b : 0) + (int64_t)(n0 / 16) * kTileBytes - kBack;
         const int64_t step_a = p.ld_a * kTileBytes, step_b = p.ld_b * kTileBytes;
-        const uint32_t voff = lane * 16;
-        // copies of the next K tile into `stage`; past the last one they
+        uint32_t voff[kCopies];
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) {
+            const int i = c < kAW ? c : c - kAW;
+            const int tile = c < kAW ? min(kAW * wave + i, a_last) : min(kBW * wave + i, b_last);
+            voff[c] = (tile - i) * kTileBytes + kBack + lane * 16;
+        }
+        // copy c of the next K tile into `stage`; past the last K tile they
         // repeat it (never used), which keeps the count of copies in flight
         int ahead = 0;
-        auto copy_tile = [&](auto stage, int c) {
-            uint8_t* const dst = stage_tiles<decltype(stage)::value>() +
-                                 (c < kAW ? kAW * wave + c : kATiles + kBW * wave + c - kAW) * kTileBytes;
-            const uint8_t* src = c < kAW ? ga + off_a[c] : gb + off_b[c - kAW];
-            asm("" : "+s"(src));  // (keeps the sum with the lane's offset out of vector registers)
-            copy_1k(src + voff, dst);
+        auto copy_tile = [&](auto stage, auto copy) FP8Q_INLINE {
+            constexpr int C = decltype(copy)::value;
+            constexpr bool kA = C < kAW;
+            uint8_t* const dst = stage_tiles<decltype(stage)::value>() + (kA ? kAW * wave : kATiles + kBW * wave) * kTileBytes;
+            copy_1k<(kA ? C : C - kAW) * kTileBytes>(kA ? ga : gb, voff[C], dst);
         };
-        auto next_tile = [&] {
+        auto next_tile = [&]() FP8Q_INLINE {
             ++ahead;
             ga += ahead < kt ? step_a : 0;
             gb += ahead < kt ? step_b : 0;
-        };
-        auto copy_tiles = [&](auto stage) {
-#pragma unroll
-            for (int c = 0; c < kCopies; ++c) copy_tile(stage, c);
-            next_tile();
         };
         // The scale words of a K group: copy c takes row tiles [4 (4 c + wave),
         // + 4) of the stage, one per 16 lanes, A's first.
@@ -389,110 +392,130 @@ __global__ __launch_bounds__(256, TM * TN > 32 ? 1 : 2) void gemm_tiles_kernel(G
 #pragma unroll
         for (int c = 0; c < kScaleCopies; ++c) {
             const int i = 4 * (4 * c + wave) + (lane >> 4);
-            soff[c] = (i < kATiles ? min(i, a_last) : min(i - kATiles, b_last)) * kScaleWords + (lane & 15) * 4;
+            soff[c] = (i < kATiles ? min(i, a_last) : min(i - kATiles, b_last)) * 4 * kScaleWords + (lane & 15) * 16;
         }
-        auto copy_scales = [&](auto stage) {
-            uint32_t* const dst = stage_scales<decltype(stage)::value>();
+        auto copy_scales = [&]() FP8Q_INLINE {
 #pragma unroll
             for (int c = 0; c < kScaleCopies; ++c) {
                 const int i = 4 * (4 * c + wave);
-                copy_1k((i < kATiles ? gsa : gsb) + soff[c], dst + i * kScaleWords);
+                copy_1k<0>(i < kATiles ? gsa : gsb, soff[c], lds_scales + i * kScaleWords);
             }
             ++s_ahead;
             gsa += s_ahead < kgs ? p.ld_as * kScaleWords : 0;
             gsb += s_ahead < kgs ? p.ld_bs * kScaleWords : 0;
         };
         const int frag = lane_code_offset(lane), sword = lane_scale_word(lane);
-        auto read_a = [&](auto stage, int i) {
+        auto read_a = [&](auto stage, int i) FP8Q_INLINE {
             return *reinterpret_cast<const v4i*>(stage_tiles<decltype(stage)::value>() + (wm * TM + i) * kTileBytes + frag);
         };
-        auto read_b = [&](auto stage, int i) {
+        auto read_b = [&](auto stage, int i) FP8Q_INLINE {
             return *reinterpret_cast<const v4i*>(stage_tiles<decltype(stage)::value>() +
                                                  (kATiles + wn * TN + i) * kTileBytes + frag);
         };
-        auto read_scales = [&](auto stage, uint32_t (&sa)[TM], uint32_t (&sb)[TN]) {
-            const uint32_t* const s = stage_scales<decltype(stage)::value>() + sword;
-#pragma unroll
-            for (int i = 0; i < TM; ++i) sa[i] = s[(wm * TM + i) * kScaleWords];
-#pragma unroll
-            for (int i = 0; i < TN; ++i) sb[i] = s[(kATiles + wn * TN + i) * kScaleWords];
-        };
-
         v4i fa[2][TM], fb[2][TN];
-        uint32_t sa[2][TM], sb[2][TN];
+        uint32_t sa[2][TM], sb[2][TN];  // this K group's scale words, the next one's
         // The next K tile, j: its MFMAs from register set P % 2; fragments of
-        // j + 1 into the other; copies of j + 4. P = j mod 8 fixes stages and
-        // registers.
-        auto step = [&](auto pos) {
+        // j + 1 into the other; copies of j + 4. P = j mod 4 fixes stages and
+        // registers. A wave has its SIMD to itself, so whatever it issues
+        // between two MFMAs beyond the 16 cycles of the first leaves the matrix
+        // unit idle: reads and copies go one at a time between MFMAs.
+        auto step = [&](auto pos) FP8Q_INLINE {
             constexpr int P = decltype(pos)::value;
-            constexpr int G = P / 4;
             using Next = std::integral_constant<int, (P + 1) % kStages>;
             // batches of the two youngest K tiles may still be in flight
-            constexpr int kFlying = 2 * kCopies + (P % 4 == 1 || P % 4 == 2 ? kScaleCopies : 0);
+            constexpr int kFlying = 2 * kCopies + (P == 1 || P == 2 ? kScaleCopies : 0);
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(waitcnt_vm(kFlying));
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (P % 4 == 0) copy_scales(std::integral_constant<int, (G + 1) % 2>{});
-            if constexpr (P % 4 == 3) read_scales(std::integral_constant<int, (G + 1) % 2>{}, sa[(G + 1) % 2], sb[(G + 1) % 2]);
-            // one row of MFMAs at a time, with its share of the copies and
-            // fragment reads in front
-#pragma unroll
-            for (int n = 0; n < TN; ++n) {
-                if (n < kCopies) copy_tile(std::integral_constant<int, P % kStages>{}, n);
-                fb[(P + 1) % 2][n] = read_b(Next{}, n);
-                if (n < TM) fa[(P + 1) % 2][n] = read_a(Next{}, n);
-#pragma unroll
-                for (int m = 0; m < TM; ++m)
-                    mfma_in_place<P % 4>(acc[n][m], fb[P % 2][n], fa[P % 2][m], sb[G][n], sa[G][m]);
+            // the next group's scale words: copied in step 0, read in step 3
+            const uint32_t* const s = lds_scales + sword;
+            unroll(std::make_integer_sequence<int, TN * TM>{}, [&](auto at) FP8Q_INLINE {
+                constexpr int N = decltype(at)::value / TM, M = decltype(at)::value % TM;
+                mfma_in_place<P>(acc[N][M], fb[P % 2][N], fa[P % 2][M], sb[0][N], sa[0][M]);
+                if constexpr (M == 0) fb[(P + 1) % 2][N] = read_b(Next{}, N);
+                if constexpr (M == TM / 4 && N < TM) fa[(P + 1) % 2][N] = read_a(Next{}, N);
+                if constexpr (M == TM / 2 && N == 0 && P == 0) copy_scales();
+                if constexpr (M == 3 * TM / 4 && N < kCopies) copy_tile(pos, std::integral_constant<int, N>{});
+                if constexpr (M == TM - 1 && N == TN - 1) next_tile();
+                if constexpr (P == 3 && M == TM - 1) {
+                    if constexpr (N < TM) sa[1][N] = s[(wm * TM + N) * kScaleWords];
+                    sb[1][N] = s[(kATiles + wn * TN + N) * kScaleWords];
+                }
                 __builtin_amdgcn_sched_barrier(0);
+            });
+            if constexpr (P == 3) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i) sa[0][i] = sa[1][i];
+#pragma unroll
+                for (int i = 0; i < TN; ++i) sb[0][i] = sb[1][i];
             }
-            next_tile();
         };
-        using I0 = std::integral_constant<int, 0>;
-        using I1 = std::integral_constant<int, 1>;
-        using I2 = std::integral_constant<int, 2>;
-        using I3 = std::integral_constant<int, 3>;
-        copy_scales(I0{});
-        copy_tiles(I0{});
-        copy_tiles(I1{});
-        copy_tiles(I2{});
-        copy_tiles(I3{});
+        copy_scales();
+        unroll(std::make_integer_sequence<int, kStages>{}, [&](auto stage) FP8Q_INLINE {
+            unroll(std::make_integer_sequence<int, kCopies>{}, [&](auto c) FP8Q_INLINE { copy_tile(stage, c); });
+            next_tile();
+        });
         __builtin_amdgcn_s_waitcnt(waitcnt_vm(3 * kCopies));
         __builtin_amdgcn_s_barrier();
-        read_scales(I0{}, sa[0], sb[0]);
 #pragma unroll
-        for (int i = 0; i < TM; ++i) fa[0][i] = read_a(I0{}, i);
-#pragma unroll
-        for (int i = 0; i < TN; ++i) fb[0][i] = read_b(I0{}, i);
-        using I4 = std::integral_constant<int, 4>;
-        using I5 = std::integral_constant<int, 5>;
-        using I6 = std::integral_constant<int, 6>;
-        using I7 = std::integral_constant<int, 7>;
-        int j = 0;
-        for (; j + 8 <= kt; j += 8) {
-            step(I0{});
-            step(I1{});
-            step(I2{});
-            step(I3{});
-            step(I4{});
-            step(I5{});
-            step(I6{});
-            step(I7{});
+        for (int i = 0; i < TM; ++i) {
+            sa[0][i] = lds_scales[sword + (wm * TM + i) * kScaleWords];
+            fa[0][i] = read_a(std::integral_constant<int, 0>{}, i);
         }
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+            sb[0][i] = lds_scales[sword + (kATiles + wn * TN + i) * kScaleWords];
+            fb[0][i] = read_b(std::integral_constant<int, 0>{}, i);
+        }
+        int j = 0;
+        for (; j + 4 <= kt; j += 4)
+            unroll(std::make_integer_sequence<int, 4>{}, [&](auto pos) FP8Q_INLINE { step(pos); });
         const int rest = kt - j;
-        if (rest > 0) step(I0{});
-        if (rest > 1) step(I1{});
-        if (rest > 2) step(I2{});
-        if (rest > 3) step(I3{});
-        if (rest > 4) step(I4{});
-        if (rest > 5) step(I5{});
-        if (rest > 6) step(I6{});
-        // the last copies land before the LDS can be another workgroup's
+        if (rest > 0) step(std::integral_constant<int, 0>{});
+        if (rest > 1) step(std::integral_constant<int, 1>{});
+        if (rest > 2) step(std::integral_constant<int, 2>{});
+        // the last copies land before the LDS is used again, here or by
+        // another workgroup
         __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
         mfma_settle();
+        __builtin_amdgcn_s_barrier();
     }
 
+    // bf16 rows that need no edge guards go through the wave's own piece of
+    // LDS, 16 rows at a time, and leave as whole runs of 32 TN bytes; straight
+    // from the accumulators a store would write 32-byte pieces of 16 rows.
+    if constexpr (!F32) {
+        if (p.c_vec16 && n0 + BN <= p.n) {
+            constexpr int kRow = 32 * TN + 16;  // bytes of a staged row, padded against bank conflicts
+            static_assert(4 * 16 * kRow <= kMaxStage, "the four waves' rows fit a stage");
+            constexpr int kLanes = 2 * TN;      // lanes per row when it is read back, 16 bytes each
+            unroll(std::make_integer_sequence<int, TM>{}, [&](auto at) FP8Q_INLINE {
+                constexpr int I = decltype(at)::value;
+                uint8_t* const rows = stage_tiles<I % 2>() + wave * 16 * kRow;
+                const int m16 = t.m0 + (wm * TM + I) * 16;
+                if (m16 >= t.row_hi) return;
+                const bool pad = m16 + lane_m(lane) >= t.real_end;
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const v4f v = pad ? v4f{0.f, 0.f, 0.f, 0.f} : acc[j][I];
+                    *reinterpret_cast<uint2*>(rows + lane_m(lane) * kRow + (j * 16 + lane_n(lane)) * 2) =
+                        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int q = 0; q < 16 * kLanes / 64; ++q) {
+                    const int r = q * (64 / kLanes) + lane / kLanes, at16 = lane % kLanes;
+                    const uint4 v = *reinterpret_cast<const uint4*>(rows + r * kRow + at16 * 16);
+                    if (m16 + r < t.row_hi)
+                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.c) + (int64_t)(m16 + r) * p.ldc + n0 +
+                                                  wn * 16 * TN + at16 * 8) = v;
+                }
+            });
+            return;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int m = t.m0 + (wm * TM + i) * 16 + lane_m(lane);
