@@ -65,13 +65,14 @@ struct Rows {
     int expert;
 };
 
-// Tile `slot` of the grouped order: expert by expert, tiles of BM rows inside
-// each segment [off[e], off[e+1]), then tiles of the rows past the last
-// segment (no expert, all padding). The experts are found by a scan over the
-// wave: lane l takes segment base + l, a running sum gives the tiles before
-// it. Every lane of the wave must take part.
+// Tile `slot` of the grouped order: expert by expert, inside an expert column
+// tile by column tile and then tiles of BM rows of its segment [off[e],
+// off[e+1]), so that the tiles that share a panel of weights are neighbours;
+// last, the rows past the last segment (no expert, all padding). The experts
+// are found by a scan over the wave: lane l takes segment base + l, a running
+// sum gives the tiles before it. Every lane of the wave must take part.
 template <int BM>
-__device__ __forceinline__ bool grouped_rows(const GemmArgs& p, int slot, Rows& t) {
+__device__ __forceinline__ bool grouped_tile(const GemmArgs& p, int slot, int tiles_n, Rows& t, int& tn) {
     const int lane = threadIdx.x & 63;
     for (int base = 0; base <= p.groups; base += 64) {
         const int e = base + lane;
@@ -84,7 +85,7 @@ __device__ __forceinline__ bool grouped_rows(const GemmArgs& p, int slot, Rows& 
         // and C: whole row tiles of [0, m)
         beg = min(max(beg, 0), p.m) & ~15;
         end = min(max(end, beg), p.m);
-        const int tiles = (end - beg + BM - 1) / BM;
+        const int tiles_m = (end - beg + BM - 1) / BM, tiles = tiles_m * tiles_n;
         int incl = tiles;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -94,10 +95,13 @@ __device__ __forceinline__ bool grouped_rows(const GemmArgs& p, int slot, Rows& 
         const int chunk = __builtin_amdgcn_readlane(incl, 63);
         if (slot < chunk) {
             const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(incl > slot)) - 1);
-            const int before = __builtin_amdgcn_readlane(incl - tiles, l);
             const int seg = __builtin_amdgcn_readlane(beg, l), seg_end = __builtin_amdgcn_readlane(end, l);
+            const int seg_tiles = __builtin_amdgcn_readlane(tiles_m, l);
+            const int within = slot - __builtin_amdgcn_readlane(incl - tiles, l);
+            // (divisions leave the scalar unit)
+            tn = __builtin_amdgcn_readfirstlane(within / seg_tiles);
             t.expert = base + l;
-            t.m0 = seg + (slot - before) * BM;
+            t.m0 = seg + __builtin_amdgcn_readfirstlane(within % seg_tiles) * BM;
             t.row_hi = min(seg_end, t.m0 + BM);
             t.real_end = seg;  // no expert: nothing is real
             if (t.expert < p.groups) {
@@ -109,6 +113,15 @@ __device__ __forceinline__ bool grouped_rows(const GemmArgs& p, int slot, Rows& 
         slot -= chunk;
     }
     return false;
+}
+
+// Workgroup b runs on XCD b % 8: round r of an XCD's 32 CUs takes the 32
+// consecutive slots 256 r + 32 (b % 8) + [0, 32), so that neighbours share an
+// L2 and every round is spread evenly over the XCDs. A bijection for grids of
+// whole multiples of 256.
+__device__ __forceinline__ int round_slot() {
+    const int q = (int)(blockIdx.x >> 3);
+    return ((q >> 5) << 8) + ((int)(blockIdx.x & 7) << 5) + (q & 31);
 }
 
 template <bool F32>
@@ -148,11 +161,13 @@ template <int MS, bool F32, bool GROUPED>
 __global__ __launch_bounds__(64 * kMaxWaves) void gemm_rows_kernel(GemmArgs p, int tiles_n) {
     extern __shared__ v4f partial[];  // [waves][MS][64]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int tn = blockIdx.x % tiles_n, tm = blockIdx.x / tiles_n;
     Rows t;
+    int tn;
     if constexpr (GROUPED) {
-        if (!grouped_rows<16 * MS>(p, tm, t)) return;
+        if (!grouped_tile<16 * MS>(p, round_slot(), tiles_n, t, tn)) return;
     } else {
+        const int tm = blockIdx.x / tiles_n;
+        tn = blockIdx.x % tiles_n;
         t = Rows{tm * 16 * MS, min(p.m, (tm + 1) * 16 * MS), p.m, 0};
     }
     v4f acc[MS];
@@ -221,7 +236,8 @@ hipError_t dispatch_rows(const GemmArgs& p, int64_t tiles_m, hipStream_t stream)
     const int tiles_n = (p.n + 15) / 16, kg = (p.kt + kGroupTiles - 1) / kGroupTiles;
     const int rounds = kg > 0 ? (kg + kMaxWaves - 1) / kMaxWaves : 1;
     const int waves = kg > 0 ? (kg + rounds - 1) / rounds : 1;
-    const dim3 grid((unsigned)(tiles_m * tiles_n)), block(64 * waves);
+    const int64_t tiles = tiles_m * tiles_n;
+    const dim3 grid((unsigned)(GROUPED ? (tiles + 255) / 256 * 256 : tiles)), block(64 * waves);
     const size_t lds = (size_t)waves * MS * 64 * sizeof(v4f);
     if (p.out_f32)
         hipLaunchKernelGGL((gemm_rows_kernel<MS, true, GROUPED>), grid, block, lds, stream, p, tiles_n);
@@ -326,15 +342,13 @@ __global__ __launch_bounds__(256, TM * TN > 32 ? 1 : 2) void gemm_tiles_kernel(G
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
 
-    // Workgroup b runs on XCD b % 8.
     Rows t;
     int tn;
-    const int slot = (int)((blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8);
     if constexpr (GROUPED) {
-        const int tiles_n = (p.n + BN - 1) / BN;
-        tn = __builtin_amdgcn_readfirstlane(slot % tiles_n);
-        if (!grouped_rows<BM>(p, __builtin_amdgcn_readfirstlane(slot / tiles_n), t)) return;
+        if (!grouped_tile<BM>(p, round_slot(), (p.n + BN - 1) / BN, t, tn)) return;
     } else {
+        // Workgroup b runs on XCD b % 8, which takes one run of slots.
+        const int slot = (int)((blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8);
         int tm;
         if (!dense_slot<BM, BN>(p, slot, tm, tn)) return;
         t = Rows{tm * BM, min(p.m, (tm + 1) * BM), p.m, 0};
@@ -532,7 +546,8 @@ __global__ __launch_bounds__(256, TM * TN > 32 ? 1 : 2) void gemm_tiles_kernel(G
 template <int TM, int TN, bool GROUPED>
 hipError_t dispatch_tiles(const GemmArgs& p, int64_t tiles_m, hipStream_t stream) {
     const int64_t tiles = tiles_m * ((p.n + 32 * TN - 1) / (32 * TN));
-    const dim3 grid((unsigned)((tiles + 7) / 8 * 8)), block(256);
+    const int64_t unit = GROUPED ? 256 : 8;
+    const dim3 grid((unsigned)((tiles + unit - 1) / unit * unit)), block(256);
     if (p.out_f32)
         hipLaunchKernelGGL((gemm_tiles_kernel<TM, TN, true, GROUPED>), grid, block, 0, stream, p);
     else
