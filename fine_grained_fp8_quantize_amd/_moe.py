@@ -6,8 +6,8 @@ import ctypes
 
 import torch
 
-from . import Fp8qError, _check, _check_tensor, _empty, _load, _need_gpu, _ptr, _stream
-from ._mx4 import _same_device
+from . import Fp8qError, _check, _check_tensor, _load
+from ._mx4 import _address, _new, _on_gpu, _raw_stream
 
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
@@ -47,11 +47,20 @@ def _ids(ids: torch.Tensor, tokens=None):
 
 def _workspace(workspace, nbytes: int, device, stream) -> torch.Tensor:
     if workspace is None:
-        return _empty((nbytes,), torch.uint8, device, stream)
-    _need_gpu(workspace)
+        return _new(nbytes, torch.uint8, device, stream)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise Fp8qError("workspace must be a contiguous uint8 tensor")
     return workspace
+
+
+def _array(t, shape, dtype, device, stream, name: str) -> torch.Tensor:
+    """A contiguous output array: new when absent, checked otherwise."""
+    if t is None:
+        return _new(shape, dtype, device, stream)
+    _check_tensor(t, shape, (dtype,), name)
+    if not t.is_contiguous():
+        raise Fp8qError("%s must be contiguous" % name)
+    return t
 
 
 def moe_dispatch(ids: torch.Tensor, experts: int, align: int = 128, first: int = 0,
@@ -68,26 +77,16 @@ def moe_dispatch(ids: torch.Tensor, experts: int, align: int = 128, first: int =
     quantizers and the grouped GEMMs. A layout never takes more than ``tokens *
     topk + experts * (align - 1)`` rows.
     """
-    _need_gpu(ids, group_offsets, group_rows, dst_rows)
-    _same_device(ids, group_offsets, group_rows, dst_rows, workspace)
+    dev = _on_gpu(ids, group_offsets, group_rows, dst_rows, workspace)
     _ids(ids)
     tokens, topk = ids.shape
-    dev = ids.device
-    if group_offsets is None:
-        group_offsets = _empty((experts + 1,), torch.int32, dev, stream)
-    if group_rows is None:
-        group_rows = _empty((experts,), torch.int32, dev, stream)
-    if dst_rows is None:
-        dst_rows = _empty((tokens, topk), torch.int32, dev, stream)
-    _check_tensor(group_offsets, (experts + 1,), (torch.int32,), "group_offsets")
-    _check_tensor(group_rows, (experts,), (torch.int32,), "group_rows")
-    _check_tensor(dst_rows, (tokens, topk), (torch.int32,), "dst_rows")
-    if not dst_rows.is_contiguous():
-        raise Fp8qError("dst_rows must be contiguous [tokens][topk]")
+    group_offsets = _array(group_offsets, (experts + 1,), torch.int32, dev, stream, "group_offsets")
+    group_rows = _array(group_rows, (experts,), torch.int32, dev, stream, "group_rows")
+    dst_rows = _array(dst_rows, (tokens, topk), torch.int32, dev, stream, "dst_rows")
     workspace = _workspace(workspace, MOE_DISPATCH_WORKSPACE_BYTES, dev, stream)
-    st = _library().moe_dispatch(_ptr(ids), tokens, topk, first, experts, align, _ptr(group_offsets),
-                                 _ptr(group_rows), _ptr(dst_rows), _ptr(workspace), workspace.numel(),
-                                 _stream(stream))
+    st = _library().moe_dispatch(ids.data_ptr(), tokens, topk, first, experts, align, group_offsets.data_ptr(),
+                                 group_rows.data_ptr(), dst_rows.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel(), _raw_stream(stream, dev))
     _check(st, "moe_dispatch")
     return group_offsets, group_rows, dst_rows
 
@@ -111,8 +110,8 @@ def _balance_args(logits, ids, seq_offsets, score):
         raise Fp8qError("score must be 'softmax' or 'sigmoid'")
     seqs = 1 if seq_offsets is None else seq_offsets.numel() - 1
     ld = experts if tokens <= 1 else logits.stride(0)
-    return (_ptr(logits), _LOGITS[logits.dtype], tokens, experts, ld, _ptr(ids), ids.shape[1], _ptr(seq_offsets),
-            seqs, _SCORES[score])
+    return (logits.data_ptr(), _LOGITS[logits.dtype], tokens, experts, ld, ids.data_ptr(), ids.shape[1],
+            _address(seq_offsets), seqs, _SCORES[score])
 
 
 def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, seq_offsets: torch.Tensor | None = None,
@@ -131,26 +130,16 @@ def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, seq_offsets: torch
     one. Returns ``(loss[1], counts[S][experts], coef[S][experts])``; pass
     ``coef`` to :func:`moe_balance_loss_backward`.
     """
-    _need_gpu(logits, ids, seq_offsets, loss, counts, coef)
-    _same_device(logits, ids, seq_offsets, loss, counts, coef, workspace)
+    dev = _on_gpu(logits, ids, seq_offsets, loss, counts, coef, workspace)
     args = _balance_args(logits, ids, seq_offsets, score)
     tokens, experts, seqs = args[2], args[3], args[8]
-    dev = logits.device
-    if loss is None:
-        loss = _empty((1,), torch.float32, dev, stream)
-    if counts is None:
-        counts = _empty((seqs, experts), torch.int32, dev, stream)
-    if coef is None:
-        coef = _empty((seqs, experts), torch.float32, dev, stream)
-    _check_tensor(loss, (1,), (torch.float32,), "loss")
-    for t, dt, name in ((counts, torch.int32, "counts"), (coef, torch.float32, "coef")):
-        _check_tensor(t, (seqs, experts), (dt,), name)
-        if not t.is_contiguous():
-            raise Fp8qError("%s must be contiguous" % name)
+    loss = _array(loss, (1,), torch.float32, dev, stream, "loss")
+    counts = _array(counts, (seqs, experts), torch.int32, dev, stream, "counts")
+    coef = _array(coef, (seqs, experts), torch.float32, dev, stream, "coef")
     lib = _library()
     workspace = _workspace(workspace, lib.moe_balance_workspace_bytes(tokens, experts, seqs), dev, stream)
-    st = lib.moe_balance_loss(*args, float(alpha), _ptr(loss), _ptr(counts), _ptr(coef), _ptr(workspace),
-                              workspace.numel(), _stream(stream))
+    st = lib.moe_balance_loss(*args, float(alpha), loss.data_ptr(), counts.data_ptr(), coef.data_ptr(),
+                              workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     _check(st, "moe_balance_loss")
     return loss, counts, coef
 
@@ -162,19 +151,16 @@ def moe_balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, coef: tor
     logits' dtype. ``coef`` is what the forward call returned; ``grad``: the
     loss's own gradient (one fp32 element; None: 1). ``out`` may be ``logits``.
     """
-    _need_gpu(logits, ids, coef, grad, seq_offsets, out)
-    _same_device(logits, ids, coef, grad, seq_offsets, out)
+    dev = _on_gpu(logits, ids, coef, grad, seq_offsets, out)
     args = _balance_args(logits, ids, seq_offsets, score)
     tokens, experts, seqs = args[2], args[3], args[8]
-    _check_tensor(coef, (seqs, experts), (torch.float32,), "coef")
-    if not coef.is_contiguous():
-        raise Fp8qError("coef must be contiguous")
+    _array(coef, (seqs, experts), torch.float32, dev, stream, "coef")
     if grad is not None and (grad.dtype != torch.float32 or grad.numel() != 1):
         raise Fp8qError("grad must hold one float32 element")
     if out is None:
-        out = _empty((tokens, experts), logits.dtype, logits.device, stream)
+        out = _new((tokens, experts), logits.dtype, dev, stream)
     _check_tensor(out, (tokens, experts), (logits.dtype,), "out")
-    st = _library().moe_balance_loss_backward(*args, _ptr(coef), _ptr(grad), _ptr(out),
-                                              experts if tokens <= 1 else out.stride(0), _stream(stream))
+    st = _library().moe_balance_loss_backward(*args, coef.data_ptr(), _address(grad), out.data_ptr(),
+                                              experts if tokens <= 1 else out.stride(0), _raw_stream(stream, dev))
     _check(st, "moe_balance_loss_backward")
     return out

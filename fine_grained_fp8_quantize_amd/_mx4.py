@@ -6,7 +6,7 @@ import ctypes
 
 import torch
 
-from . import (Fp8qError, _check, _check_tensor, _empty, _load, _need_gpu, _out_code, _ptr, _rowmajor, _stream)
+from . import Fp8qError, _check, _check_tensor, _load, _out_code, _rowmajor
 
 FP4_TILE_1x32 = 0
 FP4_TILE_32x1 = 1
@@ -36,36 +36,98 @@ def _library():
 def _shapes(rows: int, k: int):
     """Shapes of the code and scale tensors of an FP4 matrix [rows][k]."""
     kt, rt = -(-k // 128), -(-rows // 16)
-    return (kt, rt, 1024), (-(-kt // 4), rt, 64)
+    return (kt, rt, 1024), ((kt + 3) // 4, rt, 64)
+
+
+_WORDS = (torch.int32, torch.uint32)
+
+
+def _on_gpu(*ts: torch.Tensor | None) -> torch.device:
+    """The one GPU that all tensors given live on."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise Fp8qError("fp8q tensors must live on the GPU (got a %s tensor)" % t.device)
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise Fp8qError("all tensors must be on one device (got %s and %s)" % (dev, t.device))
+    return dev
+
+
+def _address(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, dev: torch.device) -> int:
+    """hipStream_t of ``stream``, or of torch's current stream on ``dev``. (A
+    call with few rows takes the GPU a few microseconds, and making a Stream
+    object takes the host as long.)"""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _new(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
+    """A new tensor, its memory taken on ``stream`` (see ``_empty``)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _tiles_ld(t: torch.Tensor, unit: int, lead: int, what: str) -> int:
+    """Row tiles between two K tiles (or K groups) of ``t``, whose row tiles of
+    ``unit`` elements must be contiguous."""
+    shape = t.shape
+    rt = shape[-2]
+    if t.is_contiguous() or t.numel() == 0:
+        return rt
+    st = t.stride()
+    if st[-1] != 1 or (rt > 1 and st[-2] != unit):
+        raise Fp8qError("the row tiles of %s must be contiguous" % what)
+    if min(st) < 0 or st[-3] % unit != 0:
+        raise Fp8qError("%s must have K tiles a whole number of row tiles apart" % what)
+    return rt if shape[-3] <= 1 else st[-3] // unit
 
 
 def _matrix(q: torch.Tensor, scale: torch.Tensor, what: str, lead: int = 0):
     """Checks the two tensors of an FP4 matrix (or of a stack of them, with
-    ``lead`` = 1) against each other: dtypes, shapes, tiles contiguous.
-    Returns (K tiles, row tiles)."""
-    if q.dtype != torch.uint8 or q.dim() != 3 + lead or q.shape[-1] != 1024:
+    ``lead`` = 1) against each other: dtypes, shapes, tiles contiguous. Returns
+    K tiles, row tiles, and the leading dimensions of codes and scales."""
+    qs, ss = q.shape, scale.shape
+    if q.dtype is not torch.uint8 or len(qs) != 3 + lead or qs[-1] != 1024:
         raise Fp8qError("%s must be uint8 %s[k tiles][row tiles][1024]" % (what, "[E]" * lead))
-    kt, rt = q.shape[-3], q.shape[-2]
-    want = (*q.shape[:lead], -(-kt // 4), rt, 64)
-    if scale.dtype not in (torch.int32, torch.uint32) or tuple(scale.shape) != want:
-        raise Fp8qError("%s_scale must be int32 %s, got %s %s" % (what, want, scale.dtype, tuple(scale.shape)))
-    for t, unit in ((q, 1024), (scale, 64)):
-        if t.numel() and (t.stride(-1) != 1 or (rt > 1 and t.stride(-2) != unit)):
-            raise Fp8qError("the row tiles of %s must be contiguous" % what)
-        if t.numel() and (t.stride(-3) < 0 or t.stride(-3) % unit != 0 or any(t.stride(i) < 0 for i in range(lead))):
-            raise Fp8qError("%s must have K tiles a whole number of row tiles apart" % what)
-    return kt, rt
+    kt, rt = qs[-3], qs[-2]
+    if (scale.dtype not in _WORDS or len(ss) != 3 + lead or ss[-1] != 64 or ss[-2] != rt or ss[-3] != (kt + 3) // 4
+            or (lead and ss[0] != qs[0])):
+        raise Fp8qError("%s_scale must be int32 %s, got %s %s" % (
+            what, (*qs[:lead], (kt + 3) // 4, rt, 64), scale.dtype, tuple(ss)))
+    return kt, rt, _tiles_ld(q, 1024, lead, what), _tiles_ld(scale, 64, lead, what + "_scale")
 
 
-def _ld(t: torch.Tensor, unit: int) -> int:
-    """Row tiles between two K tiles (or K groups) of a checked tensor."""
-    return t.shape[-2] if t.shape[-3] <= 1 else t.stride(-3) // unit
+def _output(out, shape, dtype, dev, stream) -> torch.Tensor:
+    """The output: new when absent, otherwise of exactly this dtype and shape
+    with unit column stride."""
+    if out is None:
+        return _new(shape, dtype, dev, stream)
+    _check_tensor(out, shape, (dtype,), "out")
+    return out
 
 
-def _same_device(*ts: torch.Tensor) -> None:
-    for t in ts:
-        if t is not None and t.device != ts[0].device:
-            raise Fp8qError("all tensors must be on one device (got %s and %s)" % (ts[0].device, t.device))
+def _codes_out(q, scale, q_shape, s_shape, dev, stream, lead: int = 0):
+    """Code and scale outputs: new when absent, checked otherwise; with their
+    leading dimensions."""
+    if q is None:
+        q = _new(q_shape, torch.uint8, dev, stream)
+    if scale is None:
+        scale = _new(s_shape, torch.int32, dev, stream)
+    if q.shape != q_shape or scale.shape != s_shape:
+        raise Fp8qError("q and scale have shapes %s and %s, expected %s and %s" % (
+            tuple(q.shape), tuple(scale.shape), q_shape, s_shape))
+    return (q, scale, *_matrix(q, scale, "q", lead)[2:])
 
 
 def fp4_quantize_mx(x: torch.Tensor, tiling: str = "1x32", q: torch.Tensor | None = None,
@@ -82,8 +144,7 @@ def fp4_quantize_mx(x: torch.Tensor, tiling: str = "1x32", q: torch.Tensor | Non
     ``[ceil(k tiles / 4)][row tiles][64]`` (with ``[E]`` in front for a
     stack), K tiles of 128 and row tiles of 16.
     """
-    _need_gpu(x, q, scale)
-    _same_device(x, q, scale)
+    dev = _on_gpu(x, q, scale)
     if x.dtype != torch.bfloat16:
         raise Fp8qError("x must be bfloat16")
     lead = x.dim() - 2
@@ -97,19 +158,13 @@ def fp4_quantize_mx(x: torch.Tensor, tiling: str = "1x32", q: torch.Tensor | Non
     rows, cols = x.shape[-2:]
     out_rows, k = (rows, cols) if t == FP4_TILE_1x32 else (cols, rows)
     q_shape, s_shape = (tuple(x.shape[:lead]) + s for s in _shapes(out_rows, k))
-    if q is None:
-        q = _empty(q_shape, torch.uint8, x.device, stream)
-    if scale is None:
-        scale = _empty(s_shape, torch.int32, x.device, stream)
-    _check_tensor(q, q_shape, (torch.uint8,), "q")
-    _check_tensor(scale, s_shape, (torch.int32, torch.uint32), "scale")
-    _matrix(q, scale, "q", lead)
+    q, scale, ld_q, ld_s = _codes_out(q, scale, q_shape, s_shape, dev, stream, lead)
     groups = x.shape[0] if lead else 1
     ld_x = cols if rows <= 1 else x.stride(-2)
     st = _library().fp4_quantize_mx(
-        groups, _ptr(x), rows, cols, ld_x, x.stride(0) if lead else 0, t,
-        _ptr(q), _ld(q, 1024), q.stride(0) if lead else 0,
-        _ptr(scale), _ld(scale, 64), scale.stride(0) if lead else 0, _stream(stream))
+        groups, x.data_ptr(), rows, cols, ld_x, x.stride(0) if lead else 0, t, q.data_ptr(), ld_q,
+        q.stride(0) if lead else 0, scale.data_ptr(), ld_s, scale.stride(0) if lead else 0,
+        _raw_stream(stream, dev))
     _check(st, "fp4_quantize_mx")
     return q, scale
 
@@ -123,8 +178,7 @@ def fp4_quantize_mx_scatter(x: torch.Tensor, dst_rows: torch.Tensor, m_total: in
     Returns the FP4 matrix ``(q, scale)`` of ``m_total`` rows with K =
     ``cols``; rows no route names (segment padding) are left as they were.
     """
-    _need_gpu(x, dst_rows, q, scale)
-    _same_device(x, dst_rows, q, scale)
+    dev = _on_gpu(x, dst_rows, q, scale)
     _rowmajor(x, "x")
     if x.dtype != torch.bfloat16:
         raise Fp8qError("x must be bfloat16")
@@ -135,17 +189,11 @@ def fp4_quantize_mx_scatter(x: torch.Tensor, dst_rows: torch.Tensor, m_total: in
         raise Fp8qError("dst_rows must be int32 [tokens][topk]")
     if not dst_rows.is_contiguous():
         raise Fp8qError("dst_rows must be contiguous [tokens][topk]")
-    q_shape, s_shape = _shapes(m_total, cols)
-    if q is None:
-        q = _empty(q_shape, torch.uint8, x.device, stream)
-    if scale is None:
-        scale = _empty(s_shape, torch.int32, x.device, stream)
-    _check_tensor(q, q_shape, (torch.uint8,), "q")
-    _check_tensor(scale, s_shape, (torch.int32, torch.uint32), "scale")
-    _matrix(q, scale, "q")
+    q, scale, ld_q, ld_s = _codes_out(q, scale, *_shapes(m_total, cols), dev, stream)
     ld_x = cols if tokens <= 1 else x.stride(0)
-    st = _library().fp4_quantize_mx_scatter(_ptr(x), tokens, cols, ld_x, dst_rows.shape[1], _ptr(dst_rows), m_total,
-                                            _ptr(q), _ld(q, 1024), _ptr(scale), _ld(scale, 64), _stream(stream))
+    st = _library().fp4_quantize_mx_scatter(x.data_ptr(), tokens, cols, ld_x, dst_rows.shape[1], dst_rows.data_ptr(),
+                                            m_total, q.data_ptr(), ld_q, scale.data_ptr(), ld_s,
+                                            _raw_stream(stream, dev))
     _check(st, "fp4_quantize_mx_scatter")
     return q, scale
 
@@ -154,17 +202,14 @@ def fp4_dequantize_mx(q: torch.Tensor, scale: torch.Tensor, rows: int, cols: int
                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values ``[rows][cols]`` (bf16 or fp32, exact in both) that an FP4
     matrix of ``rows`` rows with K = ``cols`` holds."""
-    _need_gpu(q, scale, out)
-    _same_device(q, scale, out)
-    kt, rt = _matrix(q, scale, "q")
+    dev = _on_gpu(q, scale, out)
+    kt, rt, ld_q, ld_s = _matrix(q, scale, "q")
     if (kt, rt) != _shapes(rows, cols)[0][:2]:
         raise Fp8qError("q has %d x %d tiles, which is not a matrix of %d rows with K = %d" % (kt, rt, rows, cols))
     oc = _out_code(out_dtype)
-    if out is None:
-        out = _empty((rows, cols), out_dtype, q.device, stream)
-    _check_tensor(out, (rows, cols), (out_dtype,), "out")
-    st = _library().fp4_dequantize_mx(_ptr(q), _ld(q, 1024), _ptr(scale), _ld(scale, 64), rows, cols, _ptr(out),
-                                      cols if rows <= 1 else out.stride(0), oc, _stream(stream))
+    out = _output(out, (rows, cols), out_dtype, dev, stream)
+    st = _library().fp4_dequantize_mx(q.data_ptr(), ld_q, scale.data_ptr(), ld_s, rows, cols, out.data_ptr(),
+                                      cols if rows <= 1 else out.stride(0), oc, _raw_stream(stream, dev))
     _check(st, "fp4_dequantize_mx")
     return out
 
@@ -185,20 +230,17 @@ def fp4_gemm_mx(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale
     :func:`fp4_quantize_mx` (either tiling): a layer's forward product, and
     both gradients with the transposed operands. ``m`` and ``n`` are the
     operands' row counts (whole tiles of 16 when left out)."""
-    _need_gpu(a, a_scale, b, b_scale, out)
-    _same_device(a, a_scale, b, b_scale, out)
-    kt, rta = _matrix(a, a_scale, "a")
-    ktb, rtb = _matrix(b, b_scale, "b")
+    dev = _on_gpu(a, a_scale, b, b_scale, out)
+    kt, rta, ld_a, ld_as = _matrix(a, a_scale, "a")
+    ktb, rtb, ld_b, ld_bs = _matrix(b, b_scale, "b")
     if kt != ktb:
         raise Fp8qError("a and b disagree on K (%d vs %d tiles of 128)" % (kt, ktb))
     m, n = _rows_of(m, rta, "m"), _rows_of(n, rtb, "n")
     oc = _out_code(out_dtype)
-    if out is None:
-        out = _empty((m, n), out_dtype, a.device, stream)
-    _check_tensor(out, (m, n), (out_dtype,), "out")
-    st = _library().fp4_gemm_mx(m, n, kt * 128, _ptr(a), _ld(a, 1024), _ptr(a_scale), _ld(a_scale, 64),
-                                _ptr(b), _ld(b, 1024), _ptr(b_scale), _ld(b_scale, 64),
-                                _ptr(out), n if m <= 1 else out.stride(0), oc, _stream(stream))
+    out = _output(out, (m, n), out_dtype, dev, stream)
+    st = _library().fp4_gemm_mx(m, n, kt * 128, a.data_ptr(), ld_a, a_scale.data_ptr(), ld_as, b.data_ptr(), ld_b,
+                                b_scale.data_ptr(), ld_bs, out.data_ptr(), n if m <= 1 else out.stride(0), oc,
+                                _raw_stream(stream, dev))
     _check(st, "fp4_gemm_mx")
     return out
 
@@ -215,10 +257,9 @@ def fp4_grouped_gemm_mx(group_offsets: torch.Tensor, group_rows: torch.Tensor | 
     stacked FP4 weights of ``n`` rows each. Returns ``out[m_total][n]`` with
     padding rows, and rows past the last segment, zero.
     """
-    _need_gpu(group_offsets, group_rows, a, a_scale, b, b_scale, out)
-    _same_device(a, a_scale, b, b_scale, out, group_offsets, group_rows)
-    kt, rta = _matrix(a, a_scale, "a")
-    ktb, rtb = _matrix(b, b_scale, "b", 1)
+    dev = _on_gpu(a, a_scale, b, b_scale, group_offsets, group_rows, out)
+    kt, rta, ld_a, ld_as = _matrix(a, a_scale, "a")
+    ktb, rtb, ld_b, ld_bs = _matrix(b, b_scale, "b", 1)
     if kt != ktb:
         raise Fp8qError("a and b disagree on K (%d vs %d tiles of 128)" % (kt, ktb))
     groups = b.shape[0]
@@ -231,12 +272,10 @@ def fp4_grouped_gemm_mx(group_offsets: torch.Tensor, group_rows: torch.Tensor | 
         raise Fp8qError("group_rows needs E contiguous entries")
     m_total, n = rta * 16, _rows_of(n, rtb, "n")
     oc = _out_code(out_dtype)
-    if out is None:
-        out = _empty((m_total, n), out_dtype, a.device, stream)
-    _check_tensor(out, (m_total, n), (out_dtype,), "out")
+    out = _output(out, (m_total, n), out_dtype, dev, stream)
     st = _library().fp4_grouped_gemm_mx(
-        groups, _ptr(group_offsets), _ptr(group_rows), m_total, n, kt * 128, _ptr(a), _ld(a, 1024), _ptr(a_scale),
-        _ld(a_scale, 64), _ptr(b), _ld(b, 1024), b.stride(0), _ptr(b_scale), _ld(b_scale, 64), b_scale.stride(0),
-        _ptr(out), n if m_total <= 1 else out.stride(0), oc, _stream(stream))
+        groups, group_offsets.data_ptr(), _address(group_rows), m_total, n, kt * 128, a.data_ptr(), ld_a,
+        a_scale.data_ptr(), ld_as, b.data_ptr(), ld_b, b.stride(0), b_scale.data_ptr(), ld_bs, b_scale.stride(0),
+        out.data_ptr(), n if m_total <= 1 else out.stride(0), oc, _raw_stream(stream, dev))
     _check(st, "fp4_grouped_gemm_mx")
     return out

@@ -65,52 +65,58 @@ struct Rows {
     int expert;
 };
 
-// Tile `slot` of the grouped order: expert by expert, inside an expert column
-// tile by column tile and then tiles of BM rows of its segment [off[e],
-// off[e+1]), so that the tiles that share a panel of weights are neighbours;
-// last, the rows past the last segment (no expert, all padding). The experts
-// are found by a scan over the wave: lane l takes segment base + l, a running
-// sum gives the tiles before it. Every lane of the wave must take part.
-template <int BM>
+// Tile `slot` of the grouped order. Expert e's segment [off[e], off[e+1]) is
+// cut into tiles of BM rows; the rows past the last segment are one more, with
+// no expert and nothing real. First come the tiles with more than SMALL real
+// rows, expert by expert, inside an expert column tile by column tile and then
+// row tile by row tile, so that the tiles that share a panel of weights are
+// neighbours; then the others in the same order (the short tiles fill the gaps
+// that the long ones leave at the end). The experts are found by a scan over
+// the wave: lane l takes segment base + l, a running sum gives the tiles
+// before it. Every lane of the wave must take part.
+template <int BM, int SMALL>
 __device__ __forceinline__ bool grouped_tile(const GemmArgs& p, int slot, int tiles_n, Rows& t, int& tn) {
     const int lane = threadIdx.x & 63;
-    for (int base = 0; base <= p.groups; base += 64) {
-        const int e = base + lane;
-        int beg = 0, end = 0;
-        if (e <= p.groups) {
-            beg = p.group_offsets[e];
-            end = e < p.groups ? p.group_offsets[e + 1] : p.m;
-        }
-        // offsets that break the contract must not move accesses outside A
-        // and C: whole row tiles of [0, m)
-        beg = min(max(beg, 0), p.m) & ~15;
-        end = min(max(end, beg), p.m);
-        const int tiles_m = (end - beg + BM - 1) / BM, tiles = tiles_m * tiles_n;
-        int incl = tiles;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int u = __shfl_up(incl, d);
-            if (lane >= d) incl += u;
-        }
-        const int chunk = __builtin_amdgcn_readlane(incl, 63);
-        if (slot < chunk) {
-            const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(incl > slot)) - 1);
-            const int seg = __builtin_amdgcn_readlane(beg, l), seg_end = __builtin_amdgcn_readlane(end, l);
-            const int seg_tiles = __builtin_amdgcn_readlane(tiles_m, l);
-            const int within = slot - __builtin_amdgcn_readlane(incl - tiles, l);
-            // (divisions leave the scalar unit)
-            tn = __builtin_amdgcn_readfirstlane(within / seg_tiles);
-            t.expert = base + l;
-            t.m0 = seg + __builtin_amdgcn_readfirstlane(within % seg_tiles) * BM;
-            t.row_hi = min(seg_end, t.m0 + BM);
-            t.real_end = seg;  // no expert: nothing is real
-            if (t.expert < p.groups) {
-                t.real_end = seg_end;
-                if (p.group_rows) t.real_end = seg + min(max(p.group_rows[t.expert], 0), seg_end - seg);
+    for (int pass = SMALL > 0 ? 0 : 1; pass < 2; ++pass) {
+        for (int base = 0; base <= p.groups; base += 64) {
+            const int e = base + lane;
+            int beg = 0, end = 0, real = 0;
+            if (e <= p.groups) {
+                beg = p.group_offsets[e];
+                end = e < p.groups ? p.group_offsets[e + 1] : p.m;
+                if (e < p.groups) real = p.group_rows ? p.group_rows[e] : 0x7FFFFFFF;
             }
-            return true;
+            // offsets that break the contract must not move accesses outside A
+            // and C: whole row tiles of [0, m)
+            beg = min(max(beg, 0), p.m) & ~15;
+            end = min(max(end, beg), p.m);
+            real = min(max(real, 0), end - beg);
+            const int big = SMALL > 0 ? real / BM + (real % BM > SMALL ? 1 : 0) : 0;
+            const int tiles_m = pass == 0 ? big : (end - beg + BM - 1) / BM - big;
+            const int tiles = tiles_m * tiles_n;
+            int incl = tiles;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int u = __shfl_up(incl, d);
+                if (lane >= d) incl += u;
+            }
+            const int chunk = __builtin_amdgcn_readlane(incl, 63);
+            if (slot < chunk) {
+                const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(incl > slot)) - 1);
+                const int seg = __builtin_amdgcn_readlane(beg, l), seg_end = __builtin_amdgcn_readlane(end, l);
+                const int seg_tiles = __builtin_amdgcn_readlane(tiles_m, l);
+                const int first = pass == 0 ? 0 : __builtin_amdgcn_readlane(big, l);
+                const int within = slot - __builtin_amdgcn_readlane(incl - tiles, l);
+                // (divisions leave the scalar unit)
+                tn = __builtin_amdgcn_readfirstlane(within / seg_tiles);
+                t.expert = base + l;
+                t.m0 = seg + (first + __builtin_amdgcn_readfirstlane(within % seg_tiles)) * BM;
+                t.row_hi = min(seg_end, t.m0 + BM);
+                t.real_end = seg + __builtin_amdgcn_readlane(real, l);
+                return true;
+            }
+            slot -= chunk;
         }
-        slot -= chunk;
     }
     return false;
 }
@@ -164,7 +170,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemm_rows_kernel(GemmArgs p, i
     Rows t;
     int tn;
     if constexpr (GROUPED) {
-        if (!grouped_tile<16 * MS>(p, round_slot(), tiles_n, t, tn)) return;
+        if (!grouped_tile<16 * MS, 0>(p, round_slot(), tiles_n, t, tn)) return;
     } else {
         const int tm = blockIdx.x / tiles_n;
         tn = blockIdx.x % tiles_n;
@@ -331,28 +337,18 @@ __device__ __forceinline__ bool dense_slot(const GemmArgs& p, int slot, int& tm,
 // says that everybody's copies of tile j + 1 have landed and that everybody
 // has read tile j, whose stage the copies of tile j + 4 then overwrite.
 template <int TM, int TN, bool F32, bool GROUPED>
-__global__ __launch_bounds__(256, TM * TN > 32 ? 1 : 2) void gemm_tiles_kernel(GemmArgs p) {
-    constexpr int BM = 32 * TM, BN = 32 * TN;
+__device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, int tn) {
+    constexpr int BN = 32 * TN;
     constexpr int kATiles = 2 * TM, kBTiles = 2 * TN;
     constexpr int kCopies = (kATiles + kBTiles) / 4;                 // 1 KB copies per wave and K tile
-    constexpr int kScaleCopies = (kATiles + kBTiles + 15) / 16;      // 1 KB (4 row tiles) per wave and K group
+    // 1 KB (4 row tiles) per wave and K group; past the last row tile (24 of
+    // them) a copy repeats it into the unused end of the scale stage
+    constexpr int kScaleCopies = (kATiles + kBTiles + 15) / 16;
     static_assert(TM <= TN && kCopies <= TN, "the copies and reads of a K tile fit its rows of MFMAs");
-    static_assert(kATiles % 4 == 0 && kBTiles % 4 == 0 && (kATiles + kBTiles) % 16 == 0,
-                  "every wave makes the same number of copies");
+    static_assert(kATiles % 4 == 0 && kBTiles % 4 == 0, "every wave makes the same number of copies");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
 
-    Rows t;
-    int tn;
-    if constexpr (GROUPED) {
-        if (!grouped_tile<BM>(p, round_slot(), (p.n + BN - 1) / BN, t, tn)) return;
-    } else {
-        // Workgroup b runs on XCD b % 8, which takes one run of slots.
-        const int slot = (int)((blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8);
-        int tm;
-        if (!dense_slot<BM, BN>(p, slot, tm, tn)) return;
-        t = Rows{tm * BM, min(p.m, (tm + 1) * BM), p.m, 0};
-    }
     const int n0 = tn * BN;
     const int kt = p.kt;
 
@@ -543,15 +539,63 @@ __global__ __launch_bounds__(256, TM * TN > 32 ? 1 : 2) void gemm_tiles_kernel(G
     }
 }
 
-template <int TM, int TN, bool GROUPED>
-hipError_t dispatch_tiles(const GemmArgs& p, int64_t tiles_m, hipStream_t stream) {
-    const int64_t tiles = tiles_m * ((p.n + 32 * TN - 1) / (32 * TN));
-    const int64_t unit = GROUPED ? 256 : 8;
-    const dim3 grid((unsigned)((tiles + unit - 1) / unit * unit)), block(256);
+// Zeros in the padding rows [from, to) of a column tile.
+template <int BN, bool F32>
+__device__ __forceinline__ void zero_rows(const GemmArgs& p, int from, int to, int tn) {
+    for (int i = threadIdx.x; i < (to - from) * (BN / 4); i += blockDim.x) {
+        const int n = tn * BN + i % (BN / 4) * 4;
+        if (n < p.n) store4<F32>(p, from + i / (BN / 4), n, v4f{0.f, 0.f, 0.f, 0.f});
+    }
+}
+
+template <int TM, int TN, bool F32>
+__global__ __launch_bounds__(256, 1) void gemm_tiles_kernel(GemmArgs p) {
+    constexpr int BM = 32 * TM, BN = 32 * TN;
+    // Workgroup b runs on XCD b % 8, which takes one run of slots.
+    const int slot = (int)((blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8);
+    int tm, tn;
+    if (!dense_slot<BM, BN>(p, slot, tm, tn)) return;
+    tile_product<TM, TN, F32, false>(p, Rows{tm * BM, min(p.m, (tm + 1) * BM), p.m, 0}, tn);
+}
+
+// Tiles of 256 x 256, or half as high where no more than 128 rows are real
+// (an expert's last rows, or all of a small one's): that takes about 0.6 of
+// the time.
+template <bool F32>
+__global__ __launch_bounds__(256, 1) void grouped_tiles_kernel(GemmArgs p) {
+    constexpr int BM = 256, BN = 256;
+    Rows t;
+    int tn;
+    if (!grouped_tile<BM, BM / 2>(p, round_slot(), (p.n + BN - 1) / BN, t, tn)) return;
+    const int real = t.real_end - t.m0;
+    if (real > BM / 2) {
+        tile_product<8, 8, F32, true>(p, t, tn);
+    } else {
+        const int half = min(t.row_hi, t.m0 + BM / 2);
+        if (real > 0) tile_product<4, 8, F32, true>(p, Rows{t.m0, half, t.real_end, t.expert}, tn);
+        zero_rows<BN, F32>(p, real > 0 ? half : t.m0, t.row_hi, tn);
+    }
+}
+
+template <int TM, int TN>
+hipError_t dispatch_tiles(const GemmArgs& p, hipStream_t stream) {
+    const int64_t tiles = (int64_t)((p.m + 32 * TM - 1) / (32 * TM)) * ((p.n + 32 * TN - 1) / (32 * TN));
+    const dim3 grid((unsigned)((tiles + 7) / 8 * 8)), block(256);
     if (p.out_f32)
-        hipLaunchKernelGGL((gemm_tiles_kernel<TM, TN, true, GROUPED>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((gemm_tiles_kernel<TM, TN, true>), grid, block, 0, stream, p);
     else
-        hipLaunchKernelGGL((gemm_tiles_kernel<TM, TN, false, GROUPED>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((gemm_tiles_kernel<TM, TN, false>), grid, block, 0, stream, p);
+    return hipGetLastError();
+}
+
+hipError_t dispatch_grouped_tiles(const GemmArgs& p, hipStream_t stream) {
+    // at most one ragged tile per segment, and one past the last
+    const int64_t tiles = (int64_t)(p.m / 256 + p.groups + 1) * ((p.n + 255) / 256);
+    const dim3 grid((unsigned)((tiles + 255) / 256 * 256)), block(256);
+    if (p.out_f32)
+        hipLaunchKernelGGL((grouped_tiles_kernel<true>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((grouped_tiles_kernel<false>), grid, block, 0, stream, p);
     return hipGetLastError();
 }
 
@@ -561,7 +605,7 @@ hipError_t launch_gemm(const GemmArgs& p, hipStream_t stream) {
     if (p.m <= 16) return dispatch_rows<1, false>(p, 1, stream);
     if (p.m <= 32) return dispatch_rows<2, false>(p, 1, stream);
     if (p.m <= 256) return dispatch_rows<4, false>(p, (p.m + 63) / 64, stream);
-    return dispatch_tiles<8, 8, false>(p, (p.m + 255) / 256, stream);
+    return dispatch_tiles<8, 8>(p, stream);
 }
 
 hipError_t launch_grouped_gemm(const GemmArgs& p, hipStream_t stream) {
@@ -570,7 +614,7 @@ hipError_t launch_grouped_gemm(const GemmArgs& p, hipStream_t stream) {
     if (avg <= 16) return dispatch_rows<1, true>(p, p.m / 16 + p.groups + 1, stream);
     if (avg <= 32) return dispatch_rows<2, true>(p, p.m / 32 + p.groups + 1, stream);
     if (avg <= 128) return dispatch_rows<4, true>(p, p.m / 64 + p.groups + 1, stream);
-    return dispatch_tiles<8, 8, true>(p, p.m / 256 + p.groups + 1, stream);
+    return dispatch_grouped_tiles(p, stream);
 }
 
 }  // namespace mx4

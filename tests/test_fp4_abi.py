@@ -121,11 +121,9 @@ def test_binding_refuses_cpu_tensors():
 
 def test_binding_checks_a_matrix_of_tiles():
     q, s = torch.zeros((5, 3, 1024), dtype=torch.uint8), torch.zeros((2, 3, 64), dtype=torch.int32)
-    assert _mx4._matrix(q, s, "q") == (5, 3)
-    assert _mx4._ld(q, 1024) == 3 and _mx4._ld(s, 64) == 3
-    assert _mx4._matrix(q[:, 1:2], s[:, 1:2], "q") == (5, 1)        # a range of row tiles
-    assert _mx4._ld(q[:, 1:2], 1024) == 3
-    assert _mx4._matrix(torch.stack((q, q)), torch.stack((s, s)), "q", 1) == (5, 3)
+    assert _mx4._matrix(q, s, "q") == (5, 3, 3, 3)
+    assert _mx4._matrix(q[:, 1:2], s[:, 1:2], "q") == (5, 1, 3, 3)        # a range of row tiles
+    assert _mx4._matrix(torch.stack((q, q)), torch.stack((s, s)), "q", 1) == (5, 3, 3, 3)
     for bad_q, bad_s in ((q.to(torch.int8), s), (q, s[:1]), (q[..., :512], s), (q[:, :2], s), (q, s.float()),
                          (q.transpose(1, 2).contiguous().transpose(1, 2), s), (q[0], s)):
         with pytest.raises(fq.Fp8qError):
