@@ -65,58 +65,95 @@ struct Rows {
     int expert;
 };
 
-// Tile `slot` of the grouped order. Expert e's segment [off[e], off[e+1]) is
-// cut into tiles of BM rows; the rows past the last segment are one more, with
-// no expert and nothing real. First come the tiles with more than SMALL real
-// rows, expert by expert, inside an expert column tile by column tile and then
-// row tile by row tile, so that the tiles that share a panel of weights are
-// neighbours; then the others in the same order (the short tiles fill the gaps
-// that the long ones leave at the end). The experts are found by a scan over
-// the wave: lane l takes segment base + l, a running sum gives the tiles
-// before it. Every lane of the wave must take part.
+// Expert e's segment [off[e], off[e+1]) is cut into tiles of BM rows; the
+// rows past the last segment are one more segment, with no expert and nothing
+// real. A tile is of one of three kinds: more than SMALL real rows, some, or
+// none (padding). Row tiles of segment e, by kind; a segment has its tiles in
+// this order.
+struct Segment {
+    int beg, end, real, tiles[3];
+};
+template <int BM, int SMALL>
+__device__ __forceinline__ Segment segment(const GemmArgs& p, int e) {
+    Segment s = {};
+    if (e <= p.groups) {
+        s.beg = p.group_offsets[e];
+        s.end = e < p.groups ? p.group_offsets[e + 1] : p.m;
+        if (e < p.groups) s.real = p.group_rows ? p.group_rows[e] : 0x7FFFFFFF;
+    }
+    // offsets that break the contract must not move accesses outside A and C:
+    // whole row tiles of [0, m)
+    s.beg = min(max(s.beg, 0), p.m) & ~15;
+    s.end = min(max(s.end, s.beg), p.m);
+    s.real = min(max(s.real, 0), s.end - s.beg);
+    const int some = (s.real + BM - 1) / BM;
+    s.tiles[0] = s.real / BM + (s.real % BM > SMALL ? 1 : 0);
+    s.tiles[1] = some - s.tiles[0];
+    s.tiles[2] = (s.end - s.beg + BM - 1) / BM - some;
+    return s;
+}
+
+__device__ __forceinline__ int wave_inclusive_sum(int v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(v, d);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+// Tile `slot` of the grouped order. Inside a kind: expert by expert, inside an
+// expert column tile by column tile and then row tile by row tile, so that the
+// tiles that share a panel of weights are neighbours. The tiles with few real
+// rows come first, then those with many, then the padding: the few-row tiles
+// read their weights from HBM for little work, and behind them the others
+// start at different times, so that not everybody waits for HBM at once (8192
+// rows over 32 experts of uneven sizes, in turn on one card: 177 us; many first
+// 188, the two mixed evenly 189). The experts are found by a scan over the
+// wave, lane l taking segment base + l. Every lane of the wave must take part.
 template <int BM, int SMALL>
 __device__ __forceinline__ bool grouped_tile(const GemmArgs& p, int slot, int tiles_n, Rows& t, int& tn) {
     const int lane = threadIdx.x & 63;
-    for (int pass = SMALL > 0 ? 0 : 1; pass < 2; ++pass) {
+    const Segment first64 = segment<BM, SMALL>(p, lane);  // (up to 63 experts: the arrays are read once)
+    int kind = 1;
+    if constexpr (SMALL > 0) {
+        int many = 0, few = 0;
         for (int base = 0; base <= p.groups; base += 64) {
-            const int e = base + lane;
-            int beg = 0, end = 0, real = 0;
-            if (e <= p.groups) {
-                beg = p.group_offsets[e];
-                end = e < p.groups ? p.group_offsets[e + 1] : p.m;
-                if (e < p.groups) real = p.group_rows ? p.group_rows[e] : 0x7FFFFFFF;
-            }
-            // offsets that break the contract must not move accesses outside A
-            // and C: whole row tiles of [0, m)
-            beg = min(max(beg, 0), p.m) & ~15;
-            end = min(max(end, beg), p.m);
-            real = min(max(real, 0), end - beg);
-            const int big = SMALL > 0 ? real / BM + (real % BM > SMALL ? 1 : 0) : 0;
-            const int tiles_m = pass == 0 ? big : (end - beg + BM - 1) / BM - big;
-            const int tiles = tiles_m * tiles_n;
-            int incl = tiles;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int u = __shfl_up(incl, d);
-                if (lane >= d) incl += u;
-            }
-            const int chunk = __builtin_amdgcn_readlane(incl, 63);
-            if (slot < chunk) {
-                const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(incl > slot)) - 1);
-                const int seg = __builtin_amdgcn_readlane(beg, l), seg_end = __builtin_amdgcn_readlane(end, l);
-                const int seg_tiles = __builtin_amdgcn_readlane(tiles_m, l);
-                const int first = pass == 0 ? 0 : __builtin_amdgcn_readlane(big, l);
-                const int within = slot - __builtin_amdgcn_readlane(incl - tiles, l);
-                // (divisions leave the scalar unit)
-                tn = __builtin_amdgcn_readfirstlane(within / seg_tiles);
-                t.expert = base + l;
-                t.m0 = seg + (first + __builtin_amdgcn_readfirstlane(within % seg_tiles)) * BM;
-                t.row_hi = min(seg_end, t.m0 + BM);
-                t.real_end = seg + __builtin_amdgcn_readlane(real, l);
-                return true;
-            }
-            slot -= chunk;
+            const Segment s = base == 0 ? first64 : segment<BM, SMALL>(p, base + lane);
+            many += __builtin_amdgcn_readlane(wave_inclusive_sum(s.tiles[0]), 63);
+            few += __builtin_amdgcn_readlane(wave_inclusive_sum(s.tiles[1]), 63);
         }
+        many *= tiles_n;
+        few *= tiles_n;
+        kind = slot < few ? 1 : (slot < few + many ? 0 : 2);
+        slot -= kind == 1 ? 0 : (kind == 0 ? few : few + many);
+        kind = __builtin_amdgcn_readfirstlane(kind);
+        slot = __builtin_amdgcn_readfirstlane(slot);
+    }
+    for (int base = 0; base <= p.groups; base += 64) {
+        const Segment s = base == 0 ? first64 : segment<BM, SMALL>(p, base + lane);
+        const int tiles_m = SMALL == 0   ? s.tiles[0] + s.tiles[1] + s.tiles[2]
+                            : kind == 0 ? s.tiles[0]
+                            : kind == 1 ? s.tiles[1]
+                                        : s.tiles[2];
+        const int first = SMALL == 0 || kind == 0 ? 0 : (kind == 1 ? s.tiles[0] : s.tiles[0] + s.tiles[1]);
+        const int tiles = tiles_m * tiles_n, incl = wave_inclusive_sum(tiles);
+        const int chunk = __builtin_amdgcn_readlane(incl, 63);
+        if (slot < chunk) {
+            const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(incl > slot)) - 1);
+            const int seg = __builtin_amdgcn_readlane(s.beg, l), seg_end = __builtin_amdgcn_readlane(s.end, l);
+            const int seg_tiles = __builtin_amdgcn_readlane(tiles_m, l);
+            const int within = slot - __builtin_amdgcn_readlane(incl - tiles, l);
+            // (divisions leave the scalar unit)
+            tn = __builtin_amdgcn_readfirstlane(within / seg_tiles);
+            t.expert = base + l;
+            t.m0 = seg + (__builtin_amdgcn_readlane(first, l) + __builtin_amdgcn_readfirstlane(within % seg_tiles)) * BM;
+            t.row_hi = min(seg_end, t.m0 + BM);
+            t.real_end = seg + __builtin_amdgcn_readlane(s.real, l);
+            return true;
+        }
+        slot -= chunk;
     }
     return false;
 }
@@ -261,10 +298,10 @@ constexpr int waitcnt_vm(int n) { return 0x0070 | (n & 15) | ((n >> 4) << 14); }
 // LDS-DMA copy of 1 KB by a wave: 16 bytes from src + voff (lane * 16) + OFF
 // to dst + OFF + 16 * lane. src and dst are wave-uniform; the instruction's
 // own offset applies to both, so neighbouring copies need no new addresses.
-template <int OFF>
+template <int OFF, int POLICY = 0>
 __device__ __forceinline__ void copy_1k(const void* src, uint32_t voff, void* dst) {
     asm("" : "+v"(voff));  // (its zero extension is then seen here: scalar base + 32-bit lane offset)
-    __builtin_amdgcn_global_load_lds(static_cast<const uint8_t*>(src) + voff, (lds_void*)dst, 16, OFF, 0);
+    __builtin_amdgcn_global_load_lds(static_cast<const uint8_t*>(src) + voff, (lds_void*)dst, 16, OFF, POLICY);
 }
 
 template <int... Is, class F>
@@ -385,7 +422,7 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, i
             constexpr int C = decltype(copy)::value;
             constexpr bool kA = C < kAW;
             uint8_t* const dst = stage_tiles<decltype(stage)::value>() + (kA ? kAW * wave : kATiles + kBW * wave) * kTileBytes;
-            copy_1k<(kA ? C : C - kAW) * kTileBytes>(kA ? ga : gb, voff[C], dst);
+            copy_1k<(kA ? C : C - kAW) * kTileBytes, GROUPED && !kA ? 2 : 0>(kA ? ga : gb, voff[C], dst);
         };
         auto next_tile = [&]() FP8Q_INLINE {
             ++ahead;
@@ -539,12 +576,25 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, i
     }
 }
 
-// Zeros in the padding rows [from, to) of a column tile.
+// Zeros in the padding rows [from, to) of a column tile, 16 bytes per store
+// where rows allow it.
 template <int BN, bool F32>
 __device__ __forceinline__ void zero_rows(const GemmArgs& p, int from, int to, int tn) {
-    for (int i = threadIdx.x; i < (to - from) * (BN / 4); i += blockDim.x) {
-        const int n = tn * BN + i % (BN / 4) * 4;
-        if (n < p.n) store4<F32>(p, from + i / (BN / 4), n, v4f{0.f, 0.f, 0.f, 0.f});
+    constexpr int kElems = F32 ? 4 : 8, kPerRow = BN / kElems;
+    constexpr int kBytes = F32 ? 4 : 2;
+    const int n = tn * BN + (int)threadIdx.x % kPerRow * kElems;
+    char* const c = static_cast<char*>(p.c) + (int64_t)n * kBytes;
+    for (int m = from + (int)threadIdx.x / kPerRow; m < to; m += (int)blockDim.x / kPerRow) {
+        char* const row = c + (int64_t)m * p.ldc * kBytes;
+        if (p.c_vec16 && n + kElems <= p.n) {
+            *reinterpret_cast<uint4*>(row) = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int i = 0; i < kElems; ++i) {
+                if (n + i >= p.n) break;
+                if constexpr (F32) reinterpret_cast<float*>(row)[i] = 0.0f;
+                else reinterpret_cast<uint16_t*>(row)[i] = 0;
+            }
+        }
     }
 }
 
@@ -613,7 +663,6 @@ hipError_t launch_grouped_gemm(const GemmArgs& p, hipStream_t stream) {
     const int64_t avg = p.m / p.groups;
     if (avg <= 16) return dispatch_rows<1, true>(p, p.m / 16 + p.groups + 1, stream);
     if (avg <= 32) return dispatch_rows<2, true>(p, p.m / 32 + p.groups + 1, stream);
-    if (avg <= 128) return dispatch_rows<4, true>(p, p.m / 64 + p.groups + 1, stream);
     return dispatch_grouped_tiles(p, stream);
 }
 
