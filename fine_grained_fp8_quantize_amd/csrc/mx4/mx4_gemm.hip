@@ -192,101 +192,152 @@ __device__ __forceinline__ void store4(const GemmArgs& p, int m, int n, v4f v) {
     }
 }
 
+// Zeros in the padding rows [from, to) of a column tile, 16 bytes per store
+// where rows allow it.
+template <int BN, bool F32>
+__device__ __forceinline__ void zero_rows(const GemmArgs& p, int from, int to, int tn) {
+    constexpr int kElems = F32 ? 4 : 8, kPerRow = BN / kElems;
+    constexpr int kBytes = F32 ? 4 : 2;
+    const int n = tn * BN + (int)threadIdx.x % kPerRow * kElems;
+    char* const c = static_cast<char*>(p.c) + (int64_t)n * kBytes;
+    for (int m = from + (int)threadIdx.x / kPerRow; m < to; m += (int)blockDim.x / kPerRow) {
+        char* const row = c + (int64_t)m * p.ldc * kBytes;
+        if (p.c_vec16 && n + kElems <= p.n) {
+            *reinterpret_cast<uint4*>(row) = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int i = 0; i < kElems; ++i) {
+                if (n + i >= p.n) break;
+                if constexpr (F32) reinterpret_cast<float*>(row)[i] = 0.0f;
+                else reinterpret_cast<uint16_t*>(row)[i] = 0;
+            }
+        }
+    }
+}
+
+// 16 bytes of weights, read once (non-temporal).
+__device__ __forceinline__ v4i load_weights(const uint8_t* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const v4i*>(p));
+}
+
 // ------------------------------------------------------------ few rows
 
 // Few rows of A: the weights are streamed from HBM straight to registers. A
-// workgroup owns 16 MS x 16 outputs; its waves take K groups in turn (wave w
-// the groups w, w + waves, ...) and their FP32 partials are added in wave
-// order through LDS, so the result does not depend on timing.
+// workgroup owns 16 MS x 16 NT outputs; wave w takes the K groups w, w + waves,
+// ... : it loads its A tiles of a group once and multiplies them with the
+// group's tiles of all NT column tiles, whose loads (4 NT KB per wave) are in
+// flight together. The waves' FP32 partials are added in wave order through
+// LDS, so the result does not depend on timing.
 constexpr int kMaxWaves = 16;
 
-template <int MS, bool F32, bool GROUPED>
+template <int MS, int NT, bool F32, bool GROUPED>
 __global__ __launch_bounds__(64 * kMaxWaves) void gemm_rows_kernel(GemmArgs p, int tiles_n) {
-    extern __shared__ v4f partial[];  // [waves][MS][64]
+    extern __shared__ v4f partial[];  // [waves][NT][MS][64]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     Rows t;
     int tn;
     if constexpr (GROUPED) {
         if (!grouped_tile<16 * MS, 0>(p, round_slot(), tiles_n, t, tn)) return;
+        if (t.m0 >= t.real_end) {
+            zero_rows<16 * NT, F32>(p, t.m0, t.row_hi, tn);
+            return;
+        }
     } else {
         const int tm = blockIdx.x / tiles_n;
         tn = blockIdx.x % tiles_n;
         t = Rows{tm * 16 * MS, min(p.m, (tm + 1) * 16 * MS), p.m, 0};
     }
-    v4f acc[MS];
+    v4f acc[NT][MS];
 #pragma unroll
-    for (int s = 0; s < MS; ++s) acc[s] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int s = 0; s < MS; ++s) acc[j][s] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    if (t.m0 < t.real_end) {
-        const uint8_t* const qa = p.a + lane_code_offset(lane);
-        const uint32_t* const sa = p.a_scale + lane_scale_word(lane);
-        const uint8_t* const qb = p.b + (GROUPED ? t.expert * p.stride_b : 0) + (int64_t)tn * kTileBytes + lane_code_offset(lane);
-        const uint32_t* const sb =
-            p.b_scale + (GROUPED ? t.expert * p.stride_bs : 0) + (int64_t)tn * kScaleWords + lane_scale_word(lane);
-        const int kt_end = p.kt;
-        // row tiles past the last real row are loaded from it and not stored
-        int rt[MS];
+    // row and column tiles past the last one repeat it: loaded, not stored
+    int rt[MS], ct[NT];
 #pragma unroll
-        for (int s = 0; s < MS; ++s) rt[s] = min(t.m0 / 16 + s, (t.real_end - 1) / 16);
-        for (int64_t g = wave; g * kGroupTiles < kt_end; g += waves) {
-            const int left = kt_end - (int)g * kGroupTiles;  // K tiles from here on
-            const uint32_t swb = sb[g * p.ld_bs * kScaleWords];
-            uint32_t swa[MS];
+    for (int s = 0; s < MS; ++s) rt[s] = min(t.m0 / 16 + s, (t.real_end - 1) / 16);
 #pragma unroll
-            for (int s = 0; s < MS; ++s) swa[s] = sa[(g * p.ld_as + rt[s]) * kScaleWords];
-            v4i fb[kGroupTiles], fa[kGroupTiles][MS];
+    for (int j = 0; j < NT; ++j) ct[j] = min(tn * NT + j, (p.n - 1) / 16);
+    const uint8_t* const qa = p.a + lane_code_offset(lane);
+    const uint32_t* const sa = p.a_scale + lane_scale_word(lane);
+    const uint8_t* const qb = p.b + (GROUPED ? t.expert * p.stride_b : 0) + lane_code_offset(lane);
+    const uint32_t* const sb = p.b_scale + (GROUPED ? t.expert * p.stride_bs : 0) + lane_scale_word(lane);
+    for (int64_t g = wave; g * kGroupTiles < p.kt; g += waves) {
+        const int left = p.kt - (int)g * kGroupTiles;  // K tiles from here on
+        v4i fb[kGroupTiles][NT], fa[kGroupTiles][MS];
+        uint32_t wb[NT], wa[MS];
 #pragma unroll
-            for (int i = 0; i < kGroupTiles; ++i) {
-                // past the last K tile the products are skipped below
-                const int64_t kt = g * kGroupTiles + min(i, left - 1);
-                fb[i] = *reinterpret_cast<const v4i*>(qb + kt * p.ld_b * kTileBytes);
+        for (int i = 0; i < kGroupTiles; ++i) {
+            // past the last K tile the products are skipped below
+            const int64_t kt = g * kGroupTiles + min(i, left - 1);
 #pragma unroll
-                for (int s = 0; s < MS; ++s)
-                    fa[i][s] = *reinterpret_cast<const v4i*>(qa + (kt * p.ld_a + rt[s]) * kTileBytes);
-            }
-#pragma unroll
-            for (int s = 0; s < MS; ++s) acc[s] = mfma_tile<0>(fb[0], fa[0][s], acc[s], swb, swa[s]);
-            if (left > 1) {
-#pragma unroll
-                for (int s = 0; s < MS; ++s) acc[s] = mfma_tile<1>(fb[1], fa[1][s], acc[s], swb, swa[s]);
-            }
-            if (left > 2) {
-#pragma unroll
-                for (int s = 0; s < MS; ++s) acc[s] = mfma_tile<2>(fb[2], fa[2][s], acc[s], swb, swa[s]);
-            }
-            if (left > 3) {
-#pragma unroll
-                for (int s = 0; s < MS; ++s) acc[s] = mfma_tile<3>(fb[3], fa[3][s], acc[s], swb, swa[s]);
-            }
+            for (int j = 0; j < NT; ++j) fb[i][j] = load_weights(qb + (kt * p.ld_b + ct[j]) * kTileBytes);
         }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) wb[j] = sb[(g * p.ld_bs + ct[j]) * kScaleWords];
+#pragma unroll
+        for (int i = 0; i < kGroupTiles; ++i) {
+            const int64_t kt = g * kGroupTiles + min(i, left - 1);
+#pragma unroll
+            for (int s = 0; s < MS; ++s)
+                fa[i][s] = *reinterpret_cast<const v4i*>(qa + (kt * p.ld_a + rt[s]) * kTileBytes);
+        }
+#pragma unroll
+        for (int s = 0; s < MS; ++s) wa[s] = sa[(g * p.ld_as + rt[s]) * kScaleWords];
+        auto multiply = [&](auto tile) FP8Q_INLINE {
+            constexpr int T = decltype(tile)::value;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int s = 0; s < MS; ++s) acc[j][s] = mfma_tile<T>(fb[T][j], fa[T][s], acc[j][s], wb[j], wa[s]);
+        };
+        multiply(std::integral_constant<int, 0>{});
+        if (left > 1) multiply(std::integral_constant<int, 1>{});
+        if (left > 2) multiply(std::integral_constant<int, 2>{});
+        if (left > 3) multiply(std::integral_constant<int, 3>{});
     }
 #pragma unroll
-    for (int s = 0; s < MS; ++s) partial[(wave * MS + s) * 64 + lane] = acc[s];
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int s = 0; s < MS; ++s) partial[((wave * NT + j) * MS + s) * 64 + lane] = acc[j][s];
     __syncthreads();
-    for (int i = threadIdx.x; i < MS * 64; i += blockDim.x) {
+    for (int i = threadIdx.x; i < NT * MS * 64; i += blockDim.x) {
+        const int l = i & 63, s = (i >> 6) % MS, j = (i >> 6) / MS;
+        const int m = t.m0 + s * 16 + lane_m(l), n = (tn * NT + j) * 16 + lane_n(l);
+        if (m >= t.row_hi || n >= p.n) continue;
         v4f v = partial[i];
-        for (int w = 1; w < waves; ++w) v += partial[w * MS * 64 + i];
-        const int l = i & 63;
-        const int m = t.m0 + (i >> 6) * 16 + lane_m(l), n = tn * 16 + lane_n(l);
-        if (m >= t.row_hi) continue;
+        for (int w = 1; w < waves; ++w) v += partial[w * NT * MS * 64 + i];
         if (m >= t.real_end) v = v4f{0.f, 0.f, 0.f, 0.f};
         store4<F32>(p, m, n, v);
     }
 }
 
-template <int MS, bool GROUPED>
-hipError_t dispatch_rows(const GemmArgs& p, int64_t tiles_m, hipStream_t stream) {
-    const int tiles_n = (p.n + 15) / 16, kg = (p.kt + kGroupTiles - 1) / kGroupTiles;
+template <int MS, int NT, bool GROUPED>
+hipError_t dispatch_rows_wide(const GemmArgs& p, int64_t tiles_m, hipStream_t stream) {
+    const int tiles_n = (p.n + 16 * NT - 1) / (16 * NT), kg = (p.kt + kGroupTiles - 1) / kGroupTiles;
+    // every wave the same number of K groups, as far as they divide
     const int rounds = kg > 0 ? (kg + kMaxWaves - 1) / kMaxWaves : 1;
     const int waves = kg > 0 ? (kg + rounds - 1) / rounds : 1;
     const int64_t tiles = tiles_m * tiles_n;
     const dim3 grid((unsigned)(GROUPED ? (tiles + 255) / 256 * 256 : tiles)), block(64 * waves);
-    const size_t lds = (size_t)waves * MS * 64 * sizeof(v4f);
+    const size_t lds = (size_t)waves * NT * MS * 64 * sizeof(v4f);
     if (p.out_f32)
-        hipLaunchKernelGGL((gemm_rows_kernel<MS, true, GROUPED>), grid, block, lds, stream, p, tiles_n);
+        hipLaunchKernelGGL((gemm_rows_kernel<MS, NT, true, GROUPED>), grid, block, lds, stream, p, tiles_n);
     else
-        hipLaunchKernelGGL((gemm_rows_kernel<MS, false, GROUPED>), grid, block, lds, stream, p, tiles_n);
+        hipLaunchKernelGGL((gemm_rows_kernel<MS, NT, false, GROUPED>), grid, block, lds, stream, p, tiles_n);
     return hipGetLastError();
+}
+
+// Column tiles per workgroup: as many as leave two workgroups for every CU.
+// `busy`: row tiles that are likely to have work.
+template <int MS, bool GROUPED>
+hipError_t dispatch_rows(const GemmArgs& p, int64_t tiles_m, int64_t busy, hipStream_t stream) {
+    const int64_t tiles = busy * ((p.n + 15) / 16);
+    if constexpr (MS <= 2) {
+        if (tiles >= 4 * 512) return dispatch_rows_wide<MS, 4, GROUPED>(p, tiles_m, stream);
+    }
+    if (tiles >= 2 * 512) return dispatch_rows_wide<MS, 2, GROUPED>(p, tiles_m, stream);
+    return dispatch_rows_wide<MS, 1, GROUPED>(p, tiles_m, stream);
 }
 
 // ------------------------------------------------------------ many rows
@@ -576,28 +627,6 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, i
     }
 }
 
-// Zeros in the padding rows [from, to) of a column tile, 16 bytes per store
-// where rows allow it.
-template <int BN, bool F32>
-__device__ __forceinline__ void zero_rows(const GemmArgs& p, int from, int to, int tn) {
-    constexpr int kElems = F32 ? 4 : 8, kPerRow = BN / kElems;
-    constexpr int kBytes = F32 ? 4 : 2;
-    const int n = tn * BN + (int)threadIdx.x % kPerRow * kElems;
-    char* const c = static_cast<char*>(p.c) + (int64_t)n * kBytes;
-    for (int m = from + (int)threadIdx.x / kPerRow; m < to; m += (int)blockDim.x / kPerRow) {
-        char* const row = c + (int64_t)m * p.ldc * kBytes;
-        if (p.c_vec16 && n + kElems <= p.n) {
-            *reinterpret_cast<uint4*>(row) = make_uint4(0, 0, 0, 0);
-        } else {
-            for (int i = 0; i < kElems; ++i) {
-                if (n + i >= p.n) break;
-                if constexpr (F32) reinterpret_cast<float*>(row)[i] = 0.0f;
-                else reinterpret_cast<uint16_t*>(row)[i] = 0;
-            }
-        }
-    }
-}
-
 template <int TM, int TN, bool F32>
 __global__ __launch_bounds__(256, 1) void gemm_tiles_kernel(GemmArgs p) {
     constexpr int BM = 32 * TM, BN = 32 * TN;
@@ -652,17 +681,17 @@ hipError_t dispatch_grouped_tiles(const GemmArgs& p, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_gemm(const GemmArgs& p, hipStream_t stream) {
-    if (p.m <= 16) return dispatch_rows<1, false>(p, 1, stream);
-    if (p.m <= 32) return dispatch_rows<2, false>(p, 1, stream);
-    if (p.m <= 256) return dispatch_rows<4, false>(p, (p.m + 63) / 64, stream);
+    if (p.m <= 16) return dispatch_rows<1, false>(p, 1, 1, stream);
+    if (p.m <= 32) return dispatch_rows<2, false>(p, 1, 1, stream);
+    if (p.m <= 256) return dispatch_rows<4, false>(p, (p.m + 63) / 64, (p.m + 63) / 64, stream);
     return dispatch_tiles<8, 8>(p, stream);
 }
 
 hipError_t launch_grouped_gemm(const GemmArgs& p, hipStream_t stream) {
     // at most one ragged tile per segment, and one past the last
     const int64_t avg = p.m / p.groups;
-    if (avg <= 16) return dispatch_rows<1, true>(p, p.m / 16 + p.groups + 1, stream);
-    if (avg <= 32) return dispatch_rows<2, true>(p, p.m / 32 + p.groups + 1, stream);
+    if (avg <= 16) return dispatch_rows<1, true>(p, p.m / 16 + p.groups + 1, p.groups, stream);
+    if (avg <= 32) return dispatch_rows<2, true>(p, p.m / 32 + p.groups + 1, p.groups, stream);
     return dispatch_grouped_tiles(p, stream);
 }
 
