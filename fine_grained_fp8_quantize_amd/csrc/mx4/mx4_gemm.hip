@@ -227,10 +227,12 @@ __device__ __forceinline__ v4i load_weights(const uint8_t* p) {
 // group's tiles of all NT column tiles, whose loads (4 NT KB per wave) are in
 // flight together. The waves' FP32 partials are added in wave order through
 // LDS, so the result does not depend on timing.
-constexpr int kMaxWaves = 16;
+// With four row tiles a wave needs up to 200 registers: eight waves.
+template <int MS>
+constexpr int kMaxWaves = MS >= 4 ? 8 : 16;
 
 template <int MS, int NT, bool F32, bool GROUPED>
-__global__ __launch_bounds__(64 * kMaxWaves) void gemm_rows_kernel(GemmArgs p, int tiles_n) {
+__global__ __launch_bounds__(64 * kMaxWaves<MS>) void gemm_rows_kernel(GemmArgs p, int tiles_n) {
     extern __shared__ v4f partial[];  // [waves][NT][MS][64]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     Rows t;
@@ -316,7 +318,7 @@ template <int MS, int NT, bool GROUPED>
 hipError_t dispatch_rows_wide(const GemmArgs& p, int64_t tiles_m, hipStream_t stream) {
     const int tiles_n = (p.n + 16 * NT - 1) / (16 * NT), kg = (p.kt + kGroupTiles - 1) / kGroupTiles;
     // every wave the same number of K groups, as far as they divide
-    const int rounds = kg > 0 ? (kg + kMaxWaves - 1) / kMaxWaves : 1;
+    const int rounds = kg > 0 ? (kg + kMaxWaves<MS> - 1) / kMaxWaves<MS> : 1;
     const int waves = kg > 0 ? (kg + rounds - 1) / rounds : 1;
     const int64_t tiles = tiles_m * tiles_n;
     const dim3 grid((unsigned)(GROUPED ? (tiles + 255) / 256 * 256 : tiles)), block(64 * waves);
@@ -328,15 +330,15 @@ hipError_t dispatch_rows_wide(const GemmArgs& p, int64_t tiles_m, hipStream_t st
     return hipGetLastError();
 }
 
-// Column tiles per workgroup: as many as leave two workgroups for every CU.
+// Column tiles per workgroup: as many as leave three workgroups for four CUs.
 // `busy`: row tiles that are likely to have work.
 template <int MS, bool GROUPED>
 hipError_t dispatch_rows(const GemmArgs& p, int64_t tiles_m, int64_t busy, hipStream_t stream) {
     const int64_t tiles = busy * ((p.n + 15) / 16);
-    if constexpr (MS <= 2) {
-        if (tiles >= 4 * 512) return dispatch_rows_wide<MS, 4, GROUPED>(p, tiles_m, stream);
+    if constexpr (MS != 2) {  // (two row tiles by four columns do not fit 128 registers)
+        if (tiles >= 4 * 192) return dispatch_rows_wide<MS, 4, GROUPED>(p, tiles_m, stream);
     }
-    if (tiles >= 2 * 512) return dispatch_rows_wide<MS, 2, GROUPED>(p, tiles_m, stream);
+    if (tiles >= 2 * 192) return dispatch_rows_wide<MS, 2, GROUPED>(p, tiles_m, stream);
     return dispatch_rows_wide<MS, 1, GROUPED>(p, tiles_m, stream);
 }
 
@@ -385,23 +387,21 @@ __device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 
 
 // LDS of the tiled kernels: four stages of one K tile (A tiles, then B
 // tiles), each an array of its own, so that the compiler can tell a stage being
-// filled from the one being read, and one of scale words.
+// filled from the one being read, and one of scale words (64 per row tile,
+// rounded up to what the copies fill). TILES: row tiles of A and B together.
 constexpr int kStages = 4;
-constexpr int kMaxStage = 32 * kTileBytes;
-constexpr int kMaxScaleStage = 32 * kScaleWords;
-__shared__ __attribute__((aligned(1024))) uint8_t lds_t0[kMaxStage];
-__shared__ __attribute__((aligned(1024))) uint8_t lds_t1[kMaxStage];
-__shared__ __attribute__((aligned(1024))) uint8_t lds_t2[kMaxStage];
-__shared__ __attribute__((aligned(1024))) uint8_t lds_t3[kMaxStage];
-__shared__ __attribute__((aligned(1024))) uint32_t lds_scales[kMaxScaleStage];
 
-template <int S>
+template <int S, int TILES>
 __device__ __forceinline__ uint8_t* stage_tiles() {
-    if constexpr (S == 0) return lds_t0;
-    else if constexpr (S == 1) return lds_t1;
-    else if constexpr (S == 2) return lds_t2;
-    else return lds_t3;
+    __shared__ __attribute__((aligned(1024))) uint8_t tiles[TILES * kTileBytes];
+    return tiles;
 }
+template <int TILES>
+__device__ __forceinline__ uint32_t* stage_scales() {
+    __shared__ __attribute__((aligned(1024))) uint32_t words[(TILES + 15) / 16 * 16 * kScaleWords];
+    return words;
+}
+
 // Output tile `slot` of a dense problem: within an XCD (see below) slots walk
 // bands of four tile rows, so that the tiles resident together share A and B
 // panels in the XCD's L2.
@@ -424,7 +424,9 @@ __device__ __forceinline__ bool dense_slot(const GemmArgs& p, int slot, int& tm,
 // 1 KB contiguous per instruction, linear in LDS). One barrier per K tile: it
 // says that everybody's copies of tile j + 1 have landed and that everybody
 // has read tile j, whose stage the copies of tile j + 4 then overwrite.
-template <int TM, int TN, bool F32, bool GROUPED>
+// LDS: row tiles that a stage holds (a kernel with tiles of two sizes uses one
+// set of stages for both).
+template <int TM, int TN, int LDS, bool F32, bool GROUPED>
 __device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, int tn) {
     constexpr int BN = 32 * TN;
     constexpr int kATiles = 2 * TM, kBTiles = 2 * TN;
@@ -472,7 +474,7 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, i
         auto copy_tile = [&](auto stage, auto copy) FP8Q_INLINE {
             constexpr int C = decltype(copy)::value;
             constexpr bool kA = C < kAW;
-            uint8_t* const dst = stage_tiles<decltype(stage)::value>() + (kA ? kAW * wave : kATiles + kBW * wave) * kTileBytes;
+            uint8_t* const dst = stage_tiles<decltype(stage)::value, LDS>() + (kA ? kAW * wave : kATiles + kBW * wave) * kTileBytes;
             copy_1k<(kA ? C : C - kAW) * kTileBytes, GROUPED && !kA ? 2 : 0>(kA ? ga : gb, voff[C], dst);
         };
         auto next_tile = [&]() FP8Q_INLINE {
@@ -496,7 +498,7 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, i
 #pragma unroll
             for (int c = 0; c < kScaleCopies; ++c) {
                 const int i = 4 * (4 * c + wave);
-                copy_1k<0>(i < kATiles ? gsa : gsb, soff[c], lds_scales + i * kScaleWords);
+                copy_1k<0>(i < kATiles ? gsa : gsb, soff[c], stage_scales<LDS>() + i * kScaleWords);
             }
             ++s_ahead;
             gsa += s_ahead < kgs ? p.ld_as * kScaleWords : 0;
@@ -504,10 +506,10 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, i
         };
         const int frag = lane_code_offset(lane), sword = lane_scale_word(lane);
         auto read_a = [&](auto stage, int i) FP8Q_INLINE {
-            return *reinterpret_cast<const v4i*>(stage_tiles<decltype(stage)::value>() + (wm * TM + i) * kTileBytes + frag);
+            return *reinterpret_cast<const v4i*>(stage_tiles<decltype(stage)::value, LDS>() + (wm * TM + i) * kTileBytes + frag);
         };
         auto read_b = [&](auto stage, int i) FP8Q_INLINE {
-            return *reinterpret_cast<const v4i*>(stage_tiles<decltype(stage)::value>() +
+            return *reinterpret_cast<const v4i*>(stage_tiles<decltype(stage)::value, LDS>() +
                                                  (kATiles + wn * TN + i) * kTileBytes + frag);
         };
         v4i fa[2][TM], fb[2][TN];
@@ -527,7 +529,7 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, i
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
             // the next group's scale words: copied in step 0, read in step 3
-            const uint32_t* const s = lds_scales + sword;
+            const uint32_t* const s = stage_scales<LDS>() + sword;
             unroll(std::make_integer_sequence<int, TN * TM>{}, [&](auto at) FP8Q_INLINE {
                 constexpr int N = decltype(at)::value / TM, M = decltype(at)::value % TM;
                 mfma_in_place<P>(acc[N][M], fb[P % 2][N], fa[P % 2][M], sb[0][N], sa[0][M]);
@@ -558,12 +560,12 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, i
         __builtin_amdgcn_s_barrier();
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            sa[0][i] = lds_scales[sword + (wm * TM + i) * kScaleWords];
+            sa[0][i] = stage_scales<LDS>()[sword + (wm * TM + i) * kScaleWords];
             fa[0][i] = read_a(std::integral_constant<int, 0>{}, i);
         }
 #pragma unroll
         for (int i = 0; i < TN; ++i) {
-            sb[0][i] = lds_scales[sword + (kATiles + wn * TN + i) * kScaleWords];
+            sb[0][i] = stage_scales<LDS>()[sword + (kATiles + wn * TN + i) * kScaleWords];
             fb[0][i] = read_b(std::integral_constant<int, 0>{}, i);
         }
         int j = 0;
@@ -586,11 +588,11 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, i
     if constexpr (!F32) {
         if (p.c_vec16 && n0 + BN <= p.n) {
             constexpr int kRow = 32 * TN + 16;  // bytes of a staged row, padded against bank conflicts
-            static_assert(4 * 16 * kRow <= kMaxStage, "the four waves' rows fit a stage");
+            static_assert(4 * 16 * kRow <= LDS * kTileBytes, "the four waves' rows fit a stage");
             constexpr int kLanes = 2 * TN;      // lanes per row when it is read back, 16 bytes each
             unroll(std::make_integer_sequence<int, TM>{}, [&](auto at) FP8Q_INLINE {
                 constexpr int I = decltype(at)::value;
-                uint8_t* const rows = stage_tiles<I % 2>() + wave * 16 * kRow;
+                uint8_t* const rows = stage_tiles<I % 2, LDS>() + wave * 16 * kRow;
                 const int m16 = t.m0 + (wm * TM + I) * 16;
                 if (m16 >= t.row_hi) return;
                 const bool pad = m16 + lane_m(lane) >= t.real_end;
@@ -628,13 +630,13 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, i
 }
 
 template <int TM, int TN, bool F32>
-__global__ __launch_bounds__(256, 1) void gemm_tiles_kernel(GemmArgs p) {
+__global__ __launch_bounds__(256, TM * TN > 16 ? 1 : 2) void gemm_tiles_kernel(GemmArgs p) {
     constexpr int BM = 32 * TM, BN = 32 * TN;
     // Workgroup b runs on XCD b % 8, which takes one run of slots.
     const int slot = (int)((blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8);
     int tm, tn;
     if (!dense_slot<BM, BN>(p, slot, tm, tn)) return;
-    tile_product<TM, TN, F32, false>(p, Rows{tm * BM, min(p.m, (tm + 1) * BM), p.m, 0}, tn);
+    tile_product<TM, TN, 2 * (TM + TN), F32, false>(p, Rows{tm * BM, min(p.m, (tm + 1) * BM), p.m, 0}, tn);
 }
 
 // Tiles of 256 x 256, or half as high where no more than 128 rows are real
@@ -648,10 +650,10 @@ __global__ __launch_bounds__(256, 1) void grouped_tiles_kernel(GemmArgs p) {
     if (!grouped_tile<BM, BM / 2>(p, round_slot(), (p.n + BN - 1) / BN, t, tn)) return;
     const int real = t.real_end - t.m0;
     if (real > BM / 2) {
-        tile_product<8, 8, F32, true>(p, t, tn);
+        tile_product<8, 8, 32, F32, true>(p, t, tn);
     } else {
         const int half = min(t.row_hi, t.m0 + BM / 2);
-        if (real > 0) tile_product<4, 8, F32, true>(p, Rows{t.m0, half, t.real_end, t.expert}, tn);
+        if (real > 0) tile_product<4, 8, 32, F32, true>(p, Rows{t.m0, half, t.real_end, t.expert}, tn);
         zero_rows<BN, F32>(p, real > 0 ? half : t.m0, t.row_hi, tn);
     }
 }
@@ -678,20 +680,43 @@ hipError_t dispatch_grouped_tiles(const GemmArgs& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Rounds of the 256 CUs that tiles of size x size take.
+int64_t rounds_of(const GemmArgs& p, int size) {
+    const int64_t tiles = (int64_t)((p.m + size - 1) / size) * ((p.n + size - 1) / size);
+    return (tiles + 255) / 256;
+}
+
 }  // namespace
 
 hipError_t launch_gemm(const GemmArgs& p, hipStream_t stream) {
     if (p.m <= 16) return dispatch_rows<1, false>(p, 1, 1, stream);
     if (p.m <= 32) return dispatch_rows<2, false>(p, 1, 1, stream);
-    if (p.m <= 256) return dispatch_rows<4, false>(p, (p.m + 63) / 64, (p.m + 63) / 64, stream);
-    return dispatch_tiles<8, 8>(p, stream);
+    // Pieces of 64 x 64 with K split over a workgroup's waves, while they are
+    // less than one round of the CUs: a whole K sum per wave is the longer way
+    // (64 x 4096 x 7168: 10.3 against 14.7 us with 128 x 128 tiles; 256 x 4096 x
+    // 7168, 256 pieces: 17.0 against 15.0).
+    const int64_t rows64 = (p.m + 63) / 64;
+    if (rows64 * ((p.n + 63) / 64) <= 192) return dispatch_rows<4, false>(p, rows64, rows64, stream);
+    // 256 x 256 tiles or 128 x 128 ones, by the time of a round of the 256 CUs:
+    // a tile of the first kind takes about as long as 3.2 of the second one
+    // after the other on a CU (two share it). (4096 x 4096 x 7168: 59 against
+    // 69 us; 2048 x 4096 x 7168: 42 against 36; 1024 x 4096 x 7168: 40 against 20.)
+    const int64_t big = rounds_of(p, 256), small = rounds_of(p, 128);
+    return 16 * big <= 5 * small ? dispatch_tiles<8, 8>(p, stream) : dispatch_tiles<4, 4>(p, stream);
 }
 
 hipError_t launch_grouped_gemm(const GemmArgs& p, hipStream_t stream) {
-    // at most one ragged tile per segment, and one past the last
-    const int64_t avg = p.m / p.groups;
-    if (avg <= 16) return dispatch_rows<1, true>(p, p.m / 16 + p.groups + 1, p.groups, stream);
-    if (avg <= 32) return dispatch_rows<2, true>(p, p.m / 32 + p.groups + 1, p.groups, stream);
+    // How many rows an expert has is not known here; p.m bounds their sum.
+    const int64_t avg = p.m / p.groups, columns = (p.n + 255) / 256;
+    // Tiles of 256 columns once the experts alone give three tiles for four CUs
+    // (27 experts with 2 rows, 2048 x 4096, 216 tiles: 27 us, 28 without LDS);
+    // otherwise narrow pieces with K split over the waves.
+    if (p.groups * ((avg + 255) / 256) * columns >= 192) return dispatch_grouped_tiles(p, stream);
+    // row tiles: at most one ragged one per segment, and one past the last
+    if (avg <= 24) return dispatch_rows<1, true>(p, p.m / 16 + p.groups + 1, p.groups, stream);
+    if (avg <= 48) return dispatch_rows<2, true>(p, p.m / 32 + p.groups + 1, p.groups, stream);
+    const int64_t rows64 = p.m / 64 + p.groups + 1;
+    if (rows64 * ((p.n + 63) / 64) <= 512) return dispatch_rows<4, true>(p, rows64, rows64, stream);
     return dispatch_grouped_tiles(p, stream);
 }
 
