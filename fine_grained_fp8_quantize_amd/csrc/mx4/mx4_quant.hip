@@ -74,6 +74,12 @@ __device__ __forceinline__ uint32_t quant_quad(uint4 v, uint32_t& byte) {
     return byte == 255u ? 0u : c;
 }
 
+__device__ __forceinline__ void store_nt16(void* p, uint4 v) {
+    typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+    __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(p));
+}
+
+constexpr int kMaxTopk = 8;
 constexpr int kQuantWaves = 4;
 // One wave's staging: four tiles, 16 words apart so that the four tiles'
 // equal places fall into different banks.
@@ -113,8 +119,8 @@ __global__ __launch_bounds__(64 * kQuantWaves) void quant_rows_kernel(QuantArgs 
     for (int i = 0; i < kGroupTiles; ++i) {
         const int64_t kt = g * kGroupTiles + i;
         if (kt < kts)
-            *reinterpret_cast<uint4*>(p.q + e * p.stride_q + (kt * p.ld_q + tile) * kTileBytes + lane * 16) =
-                *reinterpret_cast<const uint4*>(&codes[wave][i * kStageTile + lane * 4]);
+            store_nt16(p.q + e * p.stride_q + (kt * p.ld_q + tile) * kTileBytes + lane * 16,
+                       *reinterpret_cast<const uint4*>(&codes[wave][i * kStageTile + lane * 4]));
     }
     p.scale[e * p.stride_s + (g * p.ld_s + tile) * kScaleWords + lane] =
         reinterpret_cast<const uint32_t*>(bytes[wave])[lane];
@@ -128,11 +134,14 @@ __device__ __forceinline__ uint32_t quad_max_u16x2(uint32_t v) {
 }
 
 // The transposed operand: blocks of 32 consecutive rows of x, one matrix row
-// per column of x. A workgroup takes 512 rows (tokens) x 128 columns
-// (channels); wave w takes 32 tokens (block w % 4 of K tile w / 4), lane l
-// tokens [8 (l % 4), +8) and channels [8 (l / 4), +8): a load instruction
-// reads 256 bytes of each of 4 tokens, and a block's amax is a quad maximum.
-constexpr int kColsThreads = 1024;
+// per column of x. A workgroup takes 256 rows (tokens: two K tiles, half a
+// group) x 128 columns (channels); wave w takes 32 tokens (block w % 4 of K tile
+// w / 4), lane l tokens [8 (l % 4), +8) and channels [8 (l / 4), +8): a load
+// instruction reads 256 bytes of each of 4 tokens, and a block's amax is a quad
+// maximum. (64 channels, 128 bytes of 8 tokens: a tenth slower where rows do
+// not start on 128-byte lines, as each piece then touches two.)
+constexpr int kColsThreads = 512;
+constexpr int kColsKTiles = 2;
 constexpr int kColsChannels = 128;
 // LDS words of a tile and of its upper eight rows: the 16 (tile, half) pairs
 // that one store instruction touches start 4 banks apart.
@@ -140,16 +149,17 @@ constexpr int kColsTile = kTileBytes / 4 + 8;
 constexpr int kColsHalf = kTileBytes / 8 + 4;
 
 template <bool VEC>
-__global__ __launch_bounds__(kColsThreads) void quant_cols_kernel(QuantArgs p, int64_t ct, int64_t kg) {
+__global__ __launch_bounds__(kColsThreads) void quant_cols_kernel(QuantArgs p, int64_t ct, int64_t halves) {
     constexpr int kTiles = kColsChannels / kTileRows;
-    __shared__ __attribute__((aligned(16))) uint32_t codes[kGroupTiles * kTiles * kColsTile];
-    __shared__ __attribute__((aligned(16))) uint8_t bytes[kTiles * kScaleWords * 4];
+    __shared__ __attribute__((aligned(16))) uint32_t codes[kColsKTiles * kTiles * kColsTile];
+    __shared__ __attribute__((aligned(16))) uint8_t bytes[kTiles * kScaleWords * kColsKTiles];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x % ct, g = (int64_t)blockIdx.x / ct % kg, e = (int64_t)blockIdx.x / ct / kg;
+    const int64_t c = (int64_t)blockIdx.x % ct, hf = (int64_t)blockIdx.x / ct % halves, e = (int64_t)blockIdx.x / ct / halves;
+    const int64_t kt0 = hf * kColsKTiles;  // first K tile
     const uint16_t* const x = p.x + e * p.stride_x;
     const int t = wave >> 2, b = wave & 3, j = lane & 3, chunk = lane >> 2;
     const int64_t col = c * kColsChannels + 8 * chunk;
-    const int64_t tok = g * kGroupK + wave * 32 + 8 * j;
+    const int64_t tok = kt0 * kTileK + wave * 32 + 8 * j;
 
     uint4 v[8];
 #pragma unroll
@@ -177,22 +187,25 @@ __global__ __launch_bounds__(kColsThreads) void quant_cols_kernel(QuantArgs p, i
             const int ch = 8 * chunk + 2 * w + h, r = ch & 15;
             codes[(t * kTiles + (ch >> 4)) * kColsTile + (r >> 3) * kColsHalf + (r & 7) * 16 +
                   (b ^ ((r >> 2) & 3)) * 4 + j] = code;
-            if (j == w) bytes[((ch >> 4) * kScaleWords + 4 * r + b) * 4 + t] = (uint8_t)byte;
+            if (j == w) bytes[((ch >> 4) * kScaleWords + 4 * r + b) * kColsKTiles + t] = (uint8_t)byte;
         }
     }
     __syncthreads();
     const int64_t kts = (p.rows + kTileK - 1) / kTileK, rts = (p.cols + kTileRows - 1) / kTileRows;
 #pragma unroll
-    for (int i = 0; i < kGroupTiles * kTiles / (kColsThreads / 64); ++i) {
-        const int at = i * (kColsThreads / 64) + wave;  // tile at / kTiles of the K group, row tile at % kTiles
-        const int64_t kt = g * kGroupTiles + at / kTiles, rt = c * kTiles + at % kTiles;
+    for (int i = 0; i < kColsKTiles * kTiles / (kColsThreads / 64); ++i) {
+        const int at = i * (kColsThreads / 64) + wave;  // K tile at / kTiles, row tile at % kTiles
+        const int64_t kt = kt0 + at / kTiles, rt = c * kTiles + at % kTiles;
         if (kt < kts && rt < rts)
             *reinterpret_cast<uint4*>(p.q + e * p.stride_q + (kt * p.ld_q + rt) * kTileBytes + lane * 16) =
                 *reinterpret_cast<const uint4*>(&codes[at * kColsTile + (lane >> 5) * kColsHalf + (lane & 31) * 4]);
     }
-    if (wave < kTiles && c * kTiles + wave < rts)
-        p.scale[e * p.stride_s + (g * p.ld_s + c * kTiles + wave) * kScaleWords + lane] =
-            reinterpret_cast<const uint32_t*>(bytes)[wave * kScaleWords + lane];
+    // two of the four bytes of each scale word
+    static_assert(kTiles == kColsThreads / 64, "one row tile per wave");
+    if (c * kTiles + wave < rts)
+        reinterpret_cast<uint16_t*>(p.scale + e * p.stride_s +
+                                    (hf / 2 * p.ld_s + c * kTiles + wave) * kScaleWords + lane)[hf & 1] =
+            reinterpret_cast<const uint16_t*>(bytes)[wave * kScaleWords + lane];
 }
 
 // Quantize each token once and store its codes to every row its routes name.
@@ -203,11 +216,19 @@ template <bool VEC>
 __global__ __launch_bounds__(64 * kQuantWaves) void quant_scatter_kernel(ScatterArgs p, int64_t kg, int64_t units) {
     __shared__ __attribute__((aligned(16))) uint32_t codes[kQuantWaves][kGroupTiles * kStageTile];
     __shared__ __attribute__((aligned(16))) uint8_t bytes[kQuantWaves][kScaleWords * 4];
+    __shared__ int32_t routes[kQuantWaves][kTileRows * kMaxTopk];  // of the wave's 16 tokens, -1 for none
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t unit = (int64_t)blockIdx.x * kQuantWaves + wave;
     if (unit >= units) return;  // whole wave; no workgroup barrier below
     const int64_t g = unit % kg, first = unit / kg * kTileRows;
     const int t = lane >> 4, b = (lane >> 2) & 3;
+#pragma unroll
+    for (int i = 0; i < kTileRows * kMaxTopk / 64; ++i) {
+        const int at = i * 64 + lane;
+        int64_t dst = -1;
+        if (at < kTileRows * p.topk && first * p.topk + at < p.tokens * p.topk) dst = p.dst[first * p.topk + at];
+        routes[wave][at] = dst < 0 || dst >= p.m_total ? -1 : (int32_t)dst;
+    }
 
     uint4 v[kTileRows];
 #pragma unroll
@@ -235,19 +256,14 @@ __global__ __launch_bounds__(64 * kQuantWaves) void quant_scatter_kernel(Scatter
     for (int k = 0; k < p.topk; ++k) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t token = first + 4 * i + (lane >> 4);
-            if (token >= p.tokens || kt >= kts) continue;
-            const int64_t dst = p.dst[token * p.topk + k];
-            if (dst < 0 || dst >= p.m_total) continue;
-            const int r = (int)(dst & 15);
+            const int dst = routes[wave][(4 * i + (lane >> 4)) * p.topk + k];
+            if (dst < 0 || kt >= kts) continue;
+            const int r = dst & 15;
             *reinterpret_cast<uint4*>(p.q + (kt * p.ld_q + (dst >> 4)) * kTileBytes + r * 64 +
                                       (blk ^ ((r >> 2) & 3)) * 16) = w[i];
         }
-        const int64_t token = first + (lane >> 2);
-        if (token >= p.tokens) continue;
-        const int64_t dst = p.dst[token * p.topk + k];
-        if (dst < 0 || dst >= p.m_total) continue;
-        p.scale[(g * p.ld_s + (dst >> 4)) * kScaleWords + (int)(dst & 15) * 4 + (lane & 3)] = word;
+        const int dst = routes[wave][(lane >> 2) * p.topk + k];
+        if (dst >= 0) p.scale[(g * p.ld_s + (dst >> 4)) * kScaleWords + (dst & 15) * 4 + (lane & 3)] = word;
     }
 }
 
@@ -326,12 +342,13 @@ hipError_t launch_quant_rows(const QuantArgs& p, hipStream_t stream) {
 }
 
 hipError_t launch_quant_cols(const QuantArgs& p, hipStream_t stream) {
-    const int64_t ct = ceil_div(p.cols, kColsChannels), kg = ceil_div(p.rows, kGroupK);
-    const dim3 grid((unsigned)(p.groups * ct * kg)), block(kColsThreads);
+    // both halves of the last K group, whose scale bytes must all be written
+    const int64_t ct = ceil_div(p.cols, kColsChannels), halves = 2 * ceil_div(p.rows, kGroupK);
+    const dim3 grid((unsigned)(p.groups * ct * halves)), block(kColsThreads);
     if (p.vec)
-        hipLaunchKernelGGL((quant_cols_kernel<true>), grid, block, 0, stream, p, ct, kg);
+        hipLaunchKernelGGL((quant_cols_kernel<true>), grid, block, 0, stream, p, ct, halves);
     else
-        hipLaunchKernelGGL((quant_cols_kernel<false>), grid, block, 0, stream, p, ct, kg);
+        hipLaunchKernelGGL((quant_cols_kernel<false>), grid, block, 0, stream, p, ct, halves);
     return hipGetLastError();
 }
 
