@@ -31,29 +31,38 @@ __device__ __forceinline__ int wave_inclusive_sum(int v) {
     return v;
 }
 
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+// Lane exchange inside the vector unit (DPP); lanes that receive nothing get
+// `none`.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float dpp(float v, float none) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)__float_as_uint(none), (int)__float_as_uint(v),
+                                                                 CTRL, ROWS, 0xF, false));
 }
 
+// Reductions over the wave, the result in every lane: four steps inside the
+// rows of 16 lanes, then row 15's value to the next row and row 31's to the
+// upper half, which leaves the whole in lane 63. No LDS permutes: their
+// latency, six in a row per reduction, is what a row's scores would wait for.
+__device__ __forceinline__ float lane63(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-    v += dpp<0xB1>(v);
-    v += dpp<0x4E>(v);
-    v += dpp<0x141>(v);
-    v += dpp<0x140>(v);
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-    return v;
+    v += dpp<0xB1>(v, 0.f);
+    v += dpp<0x4E>(v, 0.f);
+    v += dpp<0x141>(v, 0.f);
+    v += dpp<0x140>(v, 0.f);
+    v += dpp<0x142, 0xA>(v, 0.f);
+    v += dpp<0x143, 0xC>(v, 0.f);
+    return lane63(v);
 }
-
 __device__ __forceinline__ float wave_fmax(float v) {
-    v = fmaxf(v, dpp<0xB1>(v));
-    v = fmaxf(v, dpp<0x4E>(v));
-    v = fmaxf(v, dpp<0x141>(v));
-    v = fmaxf(v, dpp<0x140>(v));
-    v = fmaxf(v, __shfl_xor(v, 16));
-    v = fmaxf(v, __shfl_xor(v, 32));
-    return v;
+    v = fmaxf(v, dpp<0xB1>(v, -INFINITY));
+    v = fmaxf(v, dpp<0x4E>(v, -INFINITY));
+    v = fmaxf(v, dpp<0x141>(v, -INFINITY));
+    v = fmaxf(v, dpp<0x140>(v, -INFINITY));
+    v = fmaxf(v, dpp<0x142, 0xA>(v, -INFINITY));
+    v = fmaxf(v, dpp<0x143, 0xC>(v, -INFINITY));
+    return lane63(v);
 }
 
 // ---------------------------------------------------------------- dispatch
@@ -84,6 +93,7 @@ template <bool SINGLE>
 __global__ __launch_bounds__(kThreads) void dispatch_place_kernel(DispatchArgs p, int64_t per_part, int parts) {
     __shared__ int next[kWaves][kMaxExperts];
     __shared__ int wave_total[kWaves];
+    __shared__ int part_sums[2][kThreads];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int experts = p.experts;
     for (int i = lane; i < experts; i += 64) next[wave][i] = 0;
@@ -96,11 +106,28 @@ __global__ __launch_bounds__(kThreads) void dispatch_place_kernel(DispatchArgs p
         if (e >= 0 && e < experts) atomicAdd(&next[wave][e], 1);
     }
     int total = 0, before = 0;
-    if (!SINGLE && tid < experts) {
-        for (int c = 0; c < parts; ++c) {
-            const int v = p.counts[(int64_t)c * experts + tid];
-            total += v;
-            before += c < (int)blockIdx.x ? v : 0;
+    if constexpr (!SINGLE) {
+        // all parts' counts: `shares` threads per expert take every shares-th
+        // part each, so that few loads follow each other
+        const int width = 64 << (32 - __clz((experts - 1) >> 6)), shares = kThreads / width;
+        const int e = tid & (width - 1);
+        if (e < experts) {
+#pragma unroll 8
+            for (int c = tid / width; c < parts; c += shares) {
+                const int v = p.counts[(int64_t)c * experts + e];
+                total += v;
+                before += c < (int)blockIdx.x ? v : 0;
+            }
+        }
+        part_sums[0][tid] = total;
+        part_sums[1][tid] = before;
+        __syncthreads();
+        total = before = 0;
+        if (tid < experts) {
+            for (int i = tid; i < kThreads; i += width) {
+                total += part_sums[0][i];
+                before += part_sums[1][i];
+            }
         }
     }
     __syncthreads();
@@ -221,12 +248,11 @@ __device__ __forceinline__ bool find_part(const BalanceArgs& p, int64_t chunk, i
         const int incl = wave_inclusive_sum(parts);
         const int all = __builtin_amdgcn_readfirstlane(__shfl(incl, 63));
         if (slot < before + all) {
-            const int l = __ffsll((unsigned long long)__ballot(before + incl > slot)) - 1;
-            seq = __builtin_amdgcn_readfirstlane(base + l);
-            first = before + __builtin_amdgcn_readfirstlane(__shfl(incl - parts, l));
-            sequence_span(p, seq, b, e);
-            beg = b + (slot - first) * chunk;
-            end = min(e, beg + chunk);
+            const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(before + incl > slot)) - 1);
+            seq = base + l;
+            first = before + __builtin_amdgcn_readlane(incl - parts, l);
+            beg = __builtin_amdgcn_readlane((int)b, l) + (slot - first) * chunk;
+            end = min((int64_t)__builtin_amdgcn_readlane((int)e, l), beg + chunk);
             return true;
         }
         before += all;
@@ -323,15 +349,16 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(BalanceArgs p, B
         }
 #pragma unroll
         for (int u = 0; u < kTokensAtOnce; ++u) {
+            // (rows that are not counted go through the same steps, so that the
+            // four rows' reductions overlap)
             const unsigned long long valid = __ballot(id[u] >= 0);
-            if (valid == 0) continue;
             if (id[u] >= 0) atomicAdd(&hist[id[u]], 1);
-            tokens += 1;
+            tokens += valid != 0;
             routes += __popcll(valid);
             float s[V];
             row_scores<V, SIGMOID>(x[u], s);
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] += s[i];
+            for (int i = 0; i < V; ++i) acc[i] += valid != 0 ? s[i] : 0.0f;
         }
     }
 #pragma unroll
@@ -363,23 +390,20 @@ __global__ __launch_bounds__(kThreads) void balance_finish_kernel(BalanceArgs p,
     const int s = (int)(blockIdx.x / slices), e = (int)(blockIdx.x % slices) * 64 + lane;
     if (tid == 0) live = seq_first = seq_parts = seq_tokens = seq_routes = 0;
     __syncthreads();
-    // every sequence's totals, from its first part on
+    // this sequence's totals, and how many sequences have a counted token: a
+    // sequence counts where its first part with one is met
     for (int64_t i = tid; i < b.parts; i += kThreads) {
         const Part a = b.info[i];
-        if (a.seq < 0 || a.first != i) continue;
-        int tokens = 0, routes = 0, n = 0;
-        for (int64_t j = i; j < b.parts; ++j, ++n) {
-            const Part q = b.info[j];
-            if (q.seq != a.seq) break;
-            tokens += q.tokens;
-            routes += q.routes;
-        }
-        if (tokens > 0) atomicAdd(&live, 1);
         if (a.seq == s) {
-            seq_first = (int)i;
-            seq_parts = n;
-            seq_tokens = tokens;
-            seq_routes = routes;
+            if (a.first == i) seq_first = (int)i;
+            atomicAdd(&seq_parts, 1);
+            atomicAdd(&seq_tokens, a.tokens);
+            atomicAdd(&seq_routes, a.routes);
+        }
+        if (a.tokens > 0) {
+            int64_t j = a.first;
+            while (j < i && b.info[j].tokens == 0) ++j;
+            if (j == i) atomicAdd(&live, 1);
         }
     }
     __syncthreads();
@@ -458,29 +482,26 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs p) {
         if (t >= p.tokens) break;
         if (p.seq_offsets)
             while (seq + 1 < p.seqs && p.seq_offsets[seq + 1] <= t) ++seq;
-        float d[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = 0.0f;
-        if (__ballot(id[u] >= 0) != 0) {
-            if (have != seq) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int e = lane + 64 * i;
-                    w[i] = e < p.experts ? p.coef[(int64_t)seq * p.experts + e] : 0.0f;
-                }
-                have = seq;
-            }
-            float s[V];
-            row_scores<V, SIGMOID>(x[u], s);
-            float dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) dot += s[i] * w[i];
-            dot = wave_sum(dot);
+        if (have != seq) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                d[i] = g * s[i] * (w[i] - dot);
-                if (SIGMOID) d[i] *= 1.0f / (1.0f + fast_exp(x[u][i]));
+                const int e = lane + 64 * i;
+                w[i] = e < p.experts ? p.coef[(int64_t)seq * p.experts + e] : 0.0f;
             }
+            have = seq;
+        }
+        const bool counted = __ballot(id[u] >= 0) != 0;
+        float s[V], d[V];
+        row_scores<V, SIGMOID>(x[u], s);
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) dot += s[i] * w[i];
+        dot = wave_sum(dot);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            d[i] = g * s[i] * (w[i] - dot);
+            if (SIGMOID) d[i] *= 1.0f / (1.0f + fast_exp(x[u][i]));
+            d[i] = counted ? d[i] : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
