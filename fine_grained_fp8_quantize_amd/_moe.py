@@ -57,6 +57,8 @@ def _array(t, shape, dtype, device, stream, name: str) -> torch.Tensor:
     """A contiguous output array: new when absent, checked otherwise."""
     if t is None:
         return _new(shape, dtype, device, stream)
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t
     _check_tensor(t, shape, (dtype,), name)
     if not t.is_contiguous():
         raise Fp8qError("%s must be contiguous" % name)
@@ -159,7 +161,8 @@ def moe_balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, coef: tor
         raise Fp8qError("grad must hold one float32 element")
     if out is None:
         out = _new((tokens, experts), logits.dtype, dev, stream)
-    _check_tensor(out, (tokens, experts), (logits.dtype,), "out")
+    else:
+        _check_tensor(out, (tokens, experts), (logits.dtype,), "out")
     st = _library().moe_balance_loss_backward(*args, coef.data_ptr(), _address(grad), out.data_ptr(),
                                               experts if tokens <= 1 else out.stride(0), _raw_stream(stream, dev))
     _check(st, "moe_balance_loss_backward")

@@ -42,18 +42,19 @@ def _shapes(rows: int, k: int):
 _WORDS = (torch.int32, torch.uint32)
 
 
-def _on_gpu(*ts: torch.Tensor | None) -> torch.device:
-    """The one GPU that all tensors given live on."""
+def _on_gpu(*ts: torch.Tensor | None) -> int:
+    """The index of the one GPU that all tensors given live on."""
     dev = None
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise Fp8qError("fp8q tensors must live on the GPU (got a %s tensor)" % t.device)
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise Fp8qError("all tensors must be on one device (got %s and %s)" % (dev, t.device))
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise Fp8qError("fp8q tensors must live on the GPU (got a %s tensor)" % t.device)
+            if dev is not None:
+                raise Fp8qError("all tensors must be on one device (got cuda:%d and cuda:%d)" % (dev, d))
+            dev = d
     return dev
 
 
@@ -61,21 +62,31 @@ def _address(t: torch.Tensor | None) -> int:
     return 0 if t is None else t.data_ptr()
 
 
-def _raw_stream(stream, dev: torch.device) -> int:
+def _raw_stream(stream, dev: int) -> int:
     """hipStream_t of ``stream``, or of torch's current stream on ``dev``. (A
     call with few rows takes the GPU a few microseconds, and making a Stream
     object takes the host as long.)"""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _new(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
+def _new(shape, dtype, dev: int, stream) -> torch.Tensor:
     """A new tensor, its memory taken on ``stream`` (see ``_empty``)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=_device(dev))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=_device(dev))
+
+
+_devices: dict = {}
+
+
+def _device(dev: int) -> torch.device:
+    got = _devices.get(dev)
+    if got is None:
+        got = _devices[dev] = torch.device("cuda", dev)
+    return got
 
 
 def _tiles_ld(t: torch.Tensor, unit: int, lead: int, what: str) -> int:
@@ -98,6 +109,11 @@ def _matrix(q: torch.Tensor, scale: torch.Tensor, what: str, lead: int = 0):
     ``lead`` = 1) against each other: dtypes, shapes, tiles contiguous. Returns
     K tiles, row tiles, and the leading dimensions of codes and scales."""
     qs, ss = q.shape, scale.shape
+    if (lead == 0 and q.dtype is torch.uint8 and scale.dtype is torch.int32 and q.is_contiguous()
+            and scale.is_contiguous() and len(qs) == 3 and qs[2] == 1024):
+        kt, rt, _ = qs  # the usual case, in few steps
+        if ss == ((kt + 3) // 4, rt, 64):
+            return kt, rt, rt, rt
     if q.dtype is not torch.uint8 or len(qs) != 3 + lead or qs[-1] != 1024:
         raise Fp8qError("%s must be uint8 %s[k tiles][row tiles][1024]" % (what, "[E]" * lead))
     kt, rt = qs[-3], qs[-2]
