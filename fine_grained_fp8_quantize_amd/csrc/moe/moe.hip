@@ -244,7 +244,7 @@ __device__ __forceinline__ bool find_part(const BalanceArgs& p, int64_t chunk, i
     for (int base = 0; base < p.seqs; base += 64) {
         int64_t b = 0, e = 0;
         if (base + lane < p.seqs) sequence_span(p, base + lane, b, e);
-        const int parts = (int)((e - b + chunk - 1) / chunk);
+        const int parts = (int)((uint32_t)(e - b + chunk - 1) / (uint32_t)chunk);  // (32-bit: tokens < 2^31)
         const int incl = wave_inclusive_sum(parts);
         const int all = __builtin_amdgcn_readfirstlane(__shfl(incl, 63));
         if (slot < before + all) {
@@ -260,10 +260,71 @@ __device__ __forceinline__ bool find_part(const BalanceArgs& p, int64_t chunk, i
     return false;
 }
 
-template <bool F32>
-__device__ __forceinline__ float load_logit(const void* base, int64_t at) {
-    if constexpr (F32) return static_cast<const float*>(base)[at];
-    return __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[at] << 16);
+// A lane's share of a row: experts [V lane, V lane + V), -inf past the last.
+// VEC: rows start on boundaries of the lane's share (16 bytes at most), so that
+// a share is one load, or two to four for many experts.
+template <int V, bool F32, bool VEC>
+__device__ __forceinline__ void load_row(const void* base, int64_t row, int experts, float (&x)[V]) {
+    const int e0 = V * (threadIdx.x & 63);
+    if (VEC && e0 + V <= experts) {
+        if constexpr (F32) {
+            const float* const p = static_cast<const float*>(base) + row + e0;
+            if constexpr (V % 4 == 0) {
+#pragma unroll
+                for (int i = 0; i < V; i += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(p + i);
+                    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[i] = p[i];
+            }
+        } else {
+            const uint16_t* const p = static_cast<const uint16_t*>(base) + row + e0;
+            if constexpr (V % 4 == 0) {
+#pragma unroll
+                for (int i = 0; i < V; i += 4) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(p + i);
+                    x[i] = bf16_lo(v.x), x[i + 1] = bf16_hi(v.x), x[i + 2] = bf16_lo(v.y), x[i + 3] = bf16_hi(v.y);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[i] = __uint_as_float((uint32_t)p[i] << 16);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        x[i] = -INFINITY;
+        if (e0 + i < experts) {
+            if constexpr (F32) x[i] = static_cast<const float*>(base)[row + e0 + i];
+            else x[i] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[row + e0 + i] << 16);
+        }
+    }
+}
+
+template <int V, bool F32, bool VEC>
+__device__ __forceinline__ void store_row(void* base, int64_t row, int experts, const float (&x)[V]) {
+    const int e0 = V * (threadIdx.x & 63);
+    if (VEC && V % 4 == 0 && e0 + V <= experts) {
+#pragma unroll
+        for (int i = 0; i + 3 < V; i += 4) {
+            if constexpr (F32)
+                *reinterpret_cast<float4*>(static_cast<float*>(base) + row + e0 + i) =
+                    make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            else
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + row + e0 + i) =
+                    make_uint2(pack_bf16x2(x[i], x[i + 1]), pack_bf16x2(x[i + 2], x[i + 3]));
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (e0 + i >= experts) continue;
+        if constexpr (F32) static_cast<float*>(base)[row + e0 + i] = x[i];
+        else static_cast<uint16_t*>(base)[row + e0 + i] = (uint16_t)pack_bf16x2(x[i], 0.0f);
+    }
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -276,8 +337,8 @@ __device__ __forceinline__ float log_sigmoid(float x) {
     return fminf(x, 0.0f) - kLn2 * __builtin_amdgcn_logf(1.0f + fast_exp(-fabsf(x)));
 }
 
-// Scores of one row, lane l holding experts l + 64 i; x past the last expert
-// must be -inf. A row without a finite score gets zeros, a NaN reaches every
+// Scores of one row, lane l holding experts [V l, V l + V); x past the last
+// expert must be -inf. A row without a finite score gets zeros, a NaN reaches every
 // score of its row.
 template <int V, bool SIGMOID>
 __device__ __forceinline__ void row_scores(const float (&x)[V], float (&s)[V]) {
@@ -311,7 +372,7 @@ __device__ __forceinline__ int valid_route(const BalanceArgs& p, int64_t token) 
     return id >= 0 && id < p.experts ? id : -1;
 }
 
-template <int V, bool F32, bool SIGMOID>
+template <int V, bool F32, bool SIGMOID, bool VEC>
 __global__ __launch_bounds__(kThreads) void balance_part_kernel(BalanceArgs p, BalancePlan b) {
     __shared__ float sums[kWaves][64 * V];
     __shared__ int hist[64 * V];
@@ -341,11 +402,7 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(BalanceArgs p, B
         for (int u = 0; u < kTokensAtOnce; ++u) {
             const int64_t t = t0 + u;
             id[u] = t < stop ? valid_route(p, t) : -1;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane + 64 * i;
-                x[u][i] = t < stop && e < p.experts ? load_logit<F32>(p.logits, t * p.ld + e) : -INFINITY;
-            }
+            load_row<V, F32, VEC>(p.logits, min(t, stop - 1) * p.ld, p.experts, x[u]);
         }
 #pragma unroll
         for (int u = 0; u < kTokensAtOnce; ++u) {
@@ -362,7 +419,7 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(BalanceArgs p, B
         }
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) sums[wave][lane + 64 * i] = acc[i];
+    for (int i = 0; i < V; ++i) sums[wave][V * lane + i] = acc[i];
     if (lane == 0) {
         atomicAdd(&seen[0], tokens);
         atomicAdd(&seen[1], routes);
@@ -434,8 +491,14 @@ __global__ __launch_bounds__(kThreads) void balance_finish_kernel(BalanceArgs p,
         }
         part = wave_sum(part);
         if (lane == 0) {
+            // The store, the count and the last workgroup's loads are atomics
+            // of the whole device, which meet where all XCDs see them; between
+            // the first two it is enough to wait for the store (an agent-wide
+            // release would write back the L2s).
             __hip_atomic_store(&b.losses[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            last = __hip_atomic_fetch_add(b.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+            __builtin_amdgcn_s_waitcnt(0);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+            last = __hip_atomic_fetch_add(b.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
         }
     }
     __syncthreads();
@@ -447,7 +510,7 @@ __global__ __launch_bounds__(kThreads) void balance_finish_kernel(BalanceArgs p,
     if (lane == 0) *p.loss = v;
 }
 
-template <int V, bool F32, bool SIGMOID>
+template <int V, bool F32, bool SIGMOID, bool VEC>
 __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs p) {
     const int lane = threadIdx.x & 63;
     const int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * kTokensAtOnce;
@@ -458,11 +521,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs p) {
     for (int u = 0; u < kTokensAtOnce; ++u) {
         const int64_t t = t0 + u;
         id[u] = t < p.tokens ? valid_route(p, t) : -1;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 64 * i;
-            x[u][i] = t < p.tokens && e < p.experts ? load_logit<F32>(p.logits, t * p.ld + e) : -INFINITY;
-        }
+        load_row<V, F32, VEC>(p.logits, min(t, p.tokens - 1) * p.ld, p.experts, x[u]);
     }
     const float g = p.grad ? *p.grad : 1.0f;
     // the sequence of the first row: the last one that starts at or before it
@@ -485,7 +544,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs p) {
         if (have != seq) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int e = lane + 64 * i;
+                const int e = V * lane + i;
                 w[i] = e < p.experts ? p.coef[(int64_t)seq * p.experts + e] : 0.0f;
             }
             have = seq;
@@ -503,38 +562,41 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs p) {
             if (SIGMOID) d[i] *= 1.0f / (1.0f + fast_exp(x[u][i]));
             d[i] = counted ? d[i] : 0.0f;
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 64 * i;
-            if (e >= p.experts) continue;
-            if constexpr (F32)
-                static_cast<float*>(p.dlogits)[t * p.ld_d + e] = d[i];
-            else
-                static_cast<uint16_t*>(p.dlogits)[t * p.ld_d + e] = (uint16_t)pack_bf16x2(d[i], 0.0f);
-        }
+        store_row<V, F32, VEC>(p.dlogits, t * p.ld_d, p.experts, d);
     }
 }
 
-// One launch for the values-per-lane, type and score of the arguments.
+// One launch for the values-per-lane, type, score and alignment of the
+// arguments.
 template <int V, class F>
-hipError_t with_types(const BalanceArgs& p, F&& launch) {
+hipError_t with_types(const BalanceArgs& p, bool vec, F&& launch) {
+    using N = std::integral_constant<int, V>;
+    const auto aligned = [&](auto f32, auto sigmoid) {
+        if (vec) launch(N{}, f32, sigmoid, std::true_type{});
+        else launch(N{}, f32, sigmoid, std::false_type{});
+    };
     if (p.f32) {
-        if (p.sigmoid) launch(std::integral_constant<int, V>{}, std::true_type{}, std::true_type{});
-        else launch(std::integral_constant<int, V>{}, std::true_type{}, std::false_type{});
+        if (p.sigmoid) aligned(std::true_type{}, std::true_type{});
+        else aligned(std::true_type{}, std::false_type{});
     } else {
-        if (p.sigmoid) launch(std::integral_constant<int, V>{}, std::false_type{}, std::true_type{});
-        else launch(std::integral_constant<int, V>{}, std::false_type{}, std::false_type{});
+        if (p.sigmoid) aligned(std::false_type{}, std::true_type{});
+        else aligned(std::false_type{}, std::false_type{});
     }
     return hipGetLastError();
 }
 
+// Four logits (16 or 8 bytes) at a time stay aligned in every row.
+bool rows_aligned(const void* p, int64_t ld, bool f32) {
+    return reinterpret_cast<uintptr_t>(p) % (f32 ? 16 : 8) == 0 && ld % 4 == 0;
+}
+
 template <class F>
-hipError_t with_width(const BalanceArgs& p, F&& launch) {
-    if (p.experts <= 64) return with_types<1>(p, launch);
-    if (p.experts <= 128) return with_types<2>(p, launch);
-    if (p.experts <= 256) return with_types<4>(p, launch);
-    if (p.experts <= 512) return with_types<8>(p, launch);
-    return with_types<16>(p, launch);
+hipError_t with_width(const BalanceArgs& p, bool vec, F&& launch) {
+    if (p.experts <= 64) return with_types<1>(p, vec, launch);
+    if (p.experts <= 128) return with_types<2>(p, vec, launch);
+    if (p.experts <= 256) return with_types<4>(p, vec, launch);
+    if (p.experts <= 512) return with_types<8>(p, vec, launch);
+    return with_types<16>(p, vec, launch);
 }
 
 }  // namespace
@@ -565,8 +627,10 @@ int64_t balance_workspace_bytes(int64_t tokens, int64_t experts, int64_t seqs) {
 
 hipError_t launch_balance(const BalanceArgs& p, hipStream_t stream) {
     const BalancePlan b = plan_of(p.tokens, p.experts, p.seqs, p.workspace);
-    const hipError_t e = with_width(p, [&](auto v, auto f32, auto sigmoid) {
-        hipLaunchKernelGGL((balance_part_kernel<decltype(v)::value, decltype(f32)::value, decltype(sigmoid)::value>),
+    const bool vec = rows_aligned(p.logits, p.ld, p.f32);
+    const hipError_t e = with_width(p, vec, [&](auto v, auto f32, auto sigmoid, auto aligned) {
+        hipLaunchKernelGGL((balance_part_kernel<decltype(v)::value, decltype(f32)::value, decltype(sigmoid)::value,
+                                                decltype(aligned)::value>),
                            dim3((unsigned)b.parts), dim3(kThreads), 0, stream, p, b);
     });
     if (e != hipSuccess) return e;
@@ -577,8 +641,10 @@ hipError_t launch_balance(const BalanceArgs& p, hipStream_t stream) {
 
 hipError_t launch_balance_backward(const BalanceArgs& p, hipStream_t stream) {
     const dim3 grid((unsigned)ceil_div(p.tokens, 4 * kTokensAtOnce));
-    return with_width(p, [&](auto v, auto f32, auto sigmoid) {
-        hipLaunchKernelGGL((balance_backward_kernel<decltype(v)::value, decltype(f32)::value, decltype(sigmoid)::value>),
+    const bool vec = rows_aligned(p.logits, p.ld, p.f32) && rows_aligned(p.dlogits, p.ld_d, p.f32);
+    return with_width(p, vec, [&](auto v, auto f32, auto sigmoid, auto aligned) {
+        hipLaunchKernelGGL((balance_backward_kernel<decltype(v)::value, decltype(f32)::value, decltype(sigmoid)::value,
+                                                    decltype(aligned)::value>),
                            grid, dim3(256), 0, stream, p);
     });
 }
