@@ -330,8 +330,11 @@ hipError_t dispatch_rows_wide(const GemmArgs& p, int64_t tiles_m, hipStream_t st
     return hipGetLastError();
 }
 
-// Column tiles per workgroup: as many as leave three workgroups for four CUs.
-// `busy`: row tiles that are likely to have work.
+// Column tiles per workgroup: as many as leave three workgroups for four CUs,
+// since a workgroup with more of them reads A less often but runs longer (one
+// row, K = 7168, 1 / 2 / 4 column tiles: n = 4096: 6.2 / 7.3 / 9.5 us; 8192: 9.5 /
+// 8.5 / 10.7; 16384: 18.7 / 15.3 / 13.6). `busy`: row tiles that are likely to
+// have work.
 template <int MS, bool GROUPED>
 hipError_t dispatch_rows(const GemmArgs& p, int64_t tiles_m, int64_t busy, hipStream_t stream) {
     const int64_t tiles = busy * ((p.n + 15) / 16);
@@ -712,11 +715,16 @@ hipError_t launch_grouped_gemm(const GemmArgs& p, hipStream_t stream) {
     // (27 experts with 2 rows, 2048 x 4096, 216 tiles: 27 us, 28 without LDS);
     // otherwise narrow pieces with K split over the waves.
     if (p.groups * ((avg + 255) / 256) * columns >= 192) return dispatch_grouped_tiles(p, stream);
-    // row tiles: at most one ragged one per segment, and one past the last
-    if (avg <= 24) return dispatch_rows<1, true>(p, p.m / 16 + p.groups + 1, p.groups, stream);
-    if (avg <= 48) return dispatch_rows<2, true>(p, p.m / 32 + p.groups + 1, p.groups, stream);
+    // Row tiles of 16, 32 or 64 rows, or 256 x 256 tiles again when there are
+    // rows for them (8 experts, 2048 x 4096, us for each of the four: 16 rows an
+    // expert: 9.9 / 10.2 / 13.4 / 19.8; 32: 12.7 / 11.2 / 13.6 / 20.7; 48: 16.8 /
+    // 16.2 / 13.8 / 21.5; 64: 20.4 / 17.1 / 14.8 / 22.6; 128: 35.1 / 28.6 / 24.4 /
+    // 25.0; 256: 65.3 / 52.2 / 42.4 / 31.7). At most one ragged row tile per
+    // segment, and one past the last.
+    if (avg <= 20) return dispatch_rows<1, true>(p, p.m / 16 + p.groups + 1, p.groups, stream);
+    if (avg <= 40) return dispatch_rows<2, true>(p, p.m / 32 + p.groups + 1, p.groups, stream);
     const int64_t rows64 = p.m / 64 + p.groups + 1;
-    if (rows64 * ((p.n + 63) / 64) <= 512) return dispatch_rows<4, true>(p, rows64, rows64, stream);
+    if (rows64 * ((p.n + 63) / 64) <= 768) return dispatch_rows<4, true>(p, rows64, rows64, stream);
     return dispatch_grouped_tiles(p, stream);
 }
 
