@@ -261,35 +261,20 @@ __device__ __forceinline__ bool find_part(const BalanceArgs& p, int64_t chunk, i
 }
 
 // A lane's share of a row: experts [V lane, V lane + V), -inf past the last.
-// VEC: rows start on boundaries of the lane's share (16 bytes at most), so that
-// a share is one load, or two to four for many experts.
+// VEC (shares of four and more): rows start on boundaries of four logits, 16
+// or 8 bytes, which are one load.
 template <int V, bool F32, bool VEC>
 __device__ __forceinline__ void load_row(const void* base, int64_t row, int experts, float (&x)[V]) {
     const int e0 = V * (threadIdx.x & 63);
     if (VEC && e0 + V <= experts) {
-        if constexpr (F32) {
-            const float* const p = static_cast<const float*>(base) + row + e0;
-            if constexpr (V % 4 == 0) {
 #pragma unroll
-                for (int i = 0; i < V; i += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(p + i);
-                    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-                }
+        for (int i = 0; i + 3 < V; i += 4) {
+            if constexpr (F32) {
+                const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + row + e0 + i);
+                x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
             } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[i] = p[i];
-            }
-        } else {
-            const uint16_t* const p = static_cast<const uint16_t*>(base) + row + e0;
-            if constexpr (V % 4 == 0) {
-#pragma unroll
-                for (int i = 0; i < V; i += 4) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(p + i);
-                    x[i] = bf16_lo(v.x), x[i + 1] = bf16_hi(v.x), x[i + 2] = bf16_lo(v.y), x[i + 3] = bf16_hi(v.y);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[i] = __uint_as_float((uint32_t)p[i] << 16);
+                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + row + e0 + i);
+                x[i] = bf16_lo(v.x), x[i + 1] = bf16_hi(v.x), x[i + 2] = bf16_lo(v.y), x[i + 3] = bf16_hi(v.y);
             }
         }
         return;
@@ -307,7 +292,7 @@ __device__ __forceinline__ void load_row(const void* base, int64_t row, int expe
 template <int V, bool F32, bool VEC>
 __device__ __forceinline__ void store_row(void* base, int64_t row, int experts, const float (&x)[V]) {
     const int e0 = V * (threadIdx.x & 63);
-    if (VEC && V % 4 == 0 && e0 + V <= experts) {
+    if (VEC && e0 + V <= experts) {
 #pragma unroll
         for (int i = 0; i + 3 < V; i += 4) {
             if constexpr (F32)
@@ -435,38 +420,46 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(BalanceArgs p, B
     if (tid == 0) b.info[blockIdx.x] = Part{seq, (int)first, seen[0], seen[1]};
 }
 
+constexpr int kSeqBits = 32 * kThreads;  // sequences per pass over the records
+
 // Adds up one sequence's parts for 64 experts per workgroup (16 waves share
 // the parts), then writes its counts and coefficients; the last workgroup to
 // finish adds the losses, in their order.
 __global__ __launch_bounds__(kThreads) void balance_finish_kernel(BalanceArgs p, BalancePlan b, int slices) {
     __shared__ float sums[kWaves][64];
     __shared__ int counts[kWaves][64];
+    __shared__ unsigned bits[kSeqBits / 32];
     __shared__ int live, seq_first, seq_parts, seq_tokens, seq_routes;
     __shared__ int last;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int s = (int)(blockIdx.x / slices), e = (int)(blockIdx.x % slices) * 64 + lane;
     if (tid == 0) live = seq_first = seq_parts = seq_tokens = seq_routes = 0;
     __syncthreads();
-    // this sequence's totals, and how many sequences have a counted token: a
-    // sequence counts where its first part with one is met
-    for (int64_t i = tid; i < b.parts; i += kThreads) {
-        const Part a = b.info[i];
-        if (a.seq == s) {
-            if (a.first == i) seq_first = (int)i;
-            atomicAdd(&seq_parts, 1);
-            atomicAdd(&seq_tokens, a.tokens);
-            atomicAdd(&seq_routes, a.routes);
+    // this sequence's totals, and how many sequences have a counted token: one
+    // bit each (a part says what it has, and no load waits for another)
+    for (int base = 0; base < p.seqs; base += kSeqBits) {
+        for (int i = tid; i < kSeqBits / 32; i += kThreads) bits[i] = 0;
+        __syncthreads();
+        for (int64_t i = tid; i < b.parts; i += kThreads) {
+            const Part a = b.info[i];
+            if (base == 0 && a.seq == s) {
+                if (a.first == i) seq_first = (int)i;
+                atomicAdd(&seq_parts, 1);
+                atomicAdd(&seq_tokens, a.tokens);
+                atomicAdd(&seq_routes, a.routes);
+            }
+            const int at = a.seq - base;
+            if (a.tokens > 0 && at >= 0 && at < kSeqBits) atomicOr(&bits[at >> 5], 1u << (at & 31));
         }
-        if (a.tokens > 0) {
-            int64_t j = a.first;
-            while (j < i && b.info[j].tokens == 0) ++j;
-            if (j == i) atomicAdd(&live, 1);
-        }
+        __syncthreads();
+        for (int i = tid; i < kSeqBits / 32; i += kThreads)
+            if (bits[i]) atomicAdd(&live, __popc(bits[i]));
+        __syncthreads();
     }
-    __syncthreads();
     float sum = 0.0f;
     int count = 0;
     if (e < p.experts) {
+#pragma unroll 4
         for (int i = wave; i < seq_parts; i += kWaves) {
             const int64_t at = (int64_t)(seq_first + i) * p.experts + e;
             sum += b.sums[at];
@@ -491,14 +484,8 @@ __global__ __launch_bounds__(kThreads) void balance_finish_kernel(BalanceArgs p,
         }
         part = wave_sum(part);
         if (lane == 0) {
-            // The store, the count and the last workgroup's loads are atomics
-            // of the whole device, which meet where all XCDs see them; between
-            // the first two it is enough to wait for the store (an agent-wide
-            // release would write back the L2s).
-            __hip_atomic_store(&b.losses[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            __builtin_amdgcn_s_waitcnt(0);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
-            last = __hip_atomic_fetch_add(b.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+            b.losses[blockIdx.x] = part;
+            last = __hip_atomic_fetch_add(b.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
         }
     }
     __syncthreads();
@@ -572,8 +559,10 @@ template <int V, class F>
 hipError_t with_types(const BalanceArgs& p, bool vec, F&& launch) {
     using N = std::integral_constant<int, V>;
     const auto aligned = [&](auto f32, auto sigmoid) {
-        if (vec) launch(N{}, f32, sigmoid, std::true_type{});
-        else launch(N{}, f32, sigmoid, std::false_type{});
+        if constexpr (V >= 4) {
+            if (vec) return launch(N{}, f32, sigmoid, std::true_type{});
+        }
+        launch(N{}, f32, sigmoid, std::false_type{});
     };
     if (p.f32) {
         if (p.sigmoid) aligned(std::true_type{}, std::true_type{});
@@ -605,9 +594,10 @@ hipError_t launch_dispatch(const DispatchArgs& p, hipStream_t stream) {
     const dim3 block(kThreads);
     int64_t parts = ceil_div(p.routes, kThreads);
     if (parts > kDispatchParts) parts = kDispatchParts;
-    // one workgroup does it all while its waves stay within 8 rounds of 64
-    // routes: a second launch costs more
-    if (p.routes <= 8 * kThreads) {
+    // One workgroup does it all while its waves stay within 4 rounds of 64
+    // routes: a second launch costs more (2048 routes to 256 experts: 4.9 against
+    // 6.5 us; 4096: 6.8 either way; 8192: 10.8 against 7.2).
+    if (p.routes <= 4 * kThreads) {
         const int64_t per_part = ceil_div(p.routes > 0 ? p.routes : 1, kThreads) * kThreads;
         hipLaunchKernelGGL((dispatch_place_kernel<true>), dim3(1), block, 0, stream, p, per_part, 1);
         return hipGetLastError();
