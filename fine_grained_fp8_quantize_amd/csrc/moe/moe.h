@@ -9,6 +9,7 @@ namespace fp8q {
 namespace moe {
 
 constexpr int kMaxExperts = 1024;
+constexpr int kMaxSeqs = 32768;
 
 struct DispatchArgs {
     const int32_t* ids;

@@ -19,7 +19,7 @@ int check_balance(const void* logits, int logits_dtype, int64_t tokens, int32_t 
     if (logits_dtype != FP8Q_LOGITS_BF16 && logits_dtype != FP8Q_LOGITS_F32) return FP8Q_ERR_ENUM;
     if (score != FP8Q_SCORE_SOFTMAX && score != FP8Q_SCORE_SIGMOID) return FP8Q_ERR_ENUM;
     if (tokens < 0 || tokens > kMaxInt || experts < 1 || experts > kMaxExperts || topk < 1 ||
-        topk > FP8Q_MOE_MAX_TOPK || seqs < 1 || seqs > kMaxInt / kMaxExperts)
+        topk > FP8Q_MOE_MAX_TOPK || seqs < 1 || seqs > kMaxSeqs)
         return FP8Q_ERR_SHAPE;
     if (!seq_offsets && seqs != 1) return FP8Q_ERR_NULL;
     if (!is_aligned(seq_offsets, 4)) return FP8Q_ERR_ALIGN;
@@ -44,6 +44,7 @@ BalanceArgs balance_args(const void* logits, int logits_dtype, int64_t tokens, i
 }  // namespace
 
 static_assert(FP8Q_MOE_MAX_EXPERTS == kMaxExperts, "the limit in fp8q_moe.h");
+static_assert(FP8Q_MOE_MAX_SEQS == kMaxSeqs, "the limit in fp8q_moe.h");
 static_assert(FP8Q_MOE_DISPATCH_WORKSPACE_BYTES == (int64_t)kDispatchParts * kMaxExperts * sizeof(int32_t),
               "the workspace size in fp8q_moe.h holds every part's counts");
 
@@ -71,7 +72,7 @@ int moe_dispatch(const int32_t* ids, int64_t tokens, int32_t topk, int32_t first
 
 int64_t moe_balance_workspace_bytes(int64_t tokens, int32_t experts, int64_t seqs) {
     if (tokens < 0 || tokens > kMaxInt || experts < 1 || experts > kMaxExperts || seqs < 1 ||
-        seqs > kMaxInt / kMaxExperts)
+        seqs > kMaxSeqs)
         return 0;
     return balance_workspace_bytes(tokens, experts, seqs);
 }

@@ -20,6 +20,7 @@ extern "C" {
 
 #define FP8Q_MOE_MAX_EXPERTS 1024
 #define FP8Q_MOE_MAX_TOPK    8
+#define FP8Q_MOE_MAX_SEQS    32768
 
 #define FP8Q_SCORE_SOFTMAX 0 /* s = softmax(logits)                                */
 #define FP8Q_SCORE_SIGMOID 1 /* s = sigmoid(logits) / sum over experts             */
@@ -78,7 +79,8 @@ int moe_dispatch(const int32_t *ids, int64_t tokens, int32_t topk, int32_t first
  * workspace   device scratch, 4-byte aligned, of at least
  *             moe_balance_workspace_bytes(tokens, experts, seqs) bytes.
  * The sums are taken in a fixed order: results repeat bit for bit.
- * Shapes: experts 1..FP8Q_MOE_MAX_EXPERTS, topk 1..8, seqs >= 1, tokens < 2^31.
+ * Shapes: experts 1..FP8Q_MOE_MAX_EXPERTS, topk 1..8, seqs 1..FP8Q_MOE_MAX_SEQS,
+ *         tokens < 2^31.
  *         tokens == 0: loss, counts and coef are written as zeros.
  * seq_offsets is trusted to keep its contract; values that break it give
  * unspecified numbers (no access outside the arrays).

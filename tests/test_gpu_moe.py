@@ -106,6 +106,16 @@ def test_balance_long_batch(score):
     balance_case(x, routes(3, 70000, 2, 16), np.array([0, 100, 65000, 70000], np.int32), score, torch.float32, 2.0 ** -19)
 
 
+def test_balance_many_sequences():
+    """As many sequences as there may be, most of a token or none (a lane adds
+    up to 512 of their losses, one after the other)."""
+    rng = np.random.default_rng(12)
+    x = rng.standard_normal((40000, 8)).astype(np.float32)
+    ids = routes(9, 40000, 2, 8)
+    ids[rng.random(40000) < 0.3] = -1
+    balance_case(x, ids, cuts(rng, 40000, 32768), "softmax", torch.float32, 2.0 ** -14)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_balance_masked_and_extreme_logits(score):
     rng = np.random.default_rng(9)

@@ -61,7 +61,7 @@ def _f(logits=A, dt=1, tokens=10, experts=8, ld=8, ids=B, topk=2, off=C, seqs=3,
 
 BOTH = [(dict(dt=2), ERR_ENUM), (dict(score=2), ERR_ENUM), (dict(tokens=-1), ERR_SHAPE), (dict(experts=0), ERR_SHAPE),
         (dict(experts=1025, ld=1025), ERR_SHAPE), (dict(topk=0), ERR_SHAPE), (dict(topk=9), ERR_SHAPE),
-        (dict(seqs=0), ERR_SHAPE), (dict(ld=7), ERR_SHAPE), (dict(off=0), ERR_NULL), (dict(logits=0), ERR_NULL),
+        (dict(seqs=0), ERR_SHAPE), (dict(seqs=32769), ERR_SHAPE), (dict(ld=7), ERR_SHAPE), (dict(off=0), ERR_NULL), (dict(logits=0), ERR_NULL),
         (dict(ids=0), ERR_NULL), (dict(coef=0), ERR_NULL), (dict(logits=A + 2), ERR_ALIGN), (dict(ids=B + 1), ERR_ALIGN),
         (dict(off=C + 2), ERR_ALIGN), (dict(logits=A + 1, dt=0), ERR_ALIGN)]
 
@@ -86,7 +86,7 @@ def test_balance_backward_refusals(kw, want):
 
 def test_workspace_bytes():
     f = _lib().moe_balance_workspace_bytes
-    assert f(-1, 8, 1) == 0 and f(1, 0, 1) == 0 and f(1, 2000, 1) == 0 and f(1, 8, 0) == 0
+    assert f(-1, 8, 1) == 0 and f(1, 0, 1) == 0 and f(1, 2000, 1) == 0 and f(1, 8, 0) == 0 and f(1, 8, 32769) == 0
     assert 0 < f(0, 8, 1) <= f(100, 8, 1) < f(100, 8, 50) < f(100, 64, 50)
     assert f(1 << 30, 256, 1) < 8 << 20      # long batches are cut into no more parts
 
