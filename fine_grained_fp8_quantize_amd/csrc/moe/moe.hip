@@ -266,31 +266,44 @@ __device__ __forceinline__ bool find_part(const BalanceArgs& p, int64_t chunk, i
     return false;
 }
 
-// A lane's share of a row: experts [V lane, V lane + V), -inf past the last.
-// VEC (shares of four and more): rows start on boundaries of four logits, 16
-// or 8 bytes, which are one load.
+constexpr int kTokensAtOnce = 4;  // rows a wave has in flight
+
+// A lane's share of rows t0, t0 + 1, ... (the last one again past it): experts
+// [V lane, V lane + V), -inf past the last. VEC (shares of four and more): rows
+// start on boundaries of four logits, 16 or 8 bytes, which are one load.
+// Whether a lane reads whole shares is decided once, so that no row's load waits
+// for another's.
 template <int V, bool F32, bool VEC>
-__device__ __forceinline__ void load_row(const void* base, int64_t row, int experts, float (&x)[V]) {
+__device__ __forceinline__ void load_rows(const BalanceArgs& p, int64_t t0, int64_t last, float (&x)[kTokensAtOnce][V]) {
     const int e0 = V * (threadIdx.x & 63);
-    if (VEC && e0 + V <= experts) {
+    if (VEC && e0 + V <= p.experts) {
 #pragma unroll
-        for (int i = 0; i + 3 < V; i += 4) {
-            if constexpr (F32) {
-                const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + row + e0 + i);
-                x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-            } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + row + e0 + i);
-                x[i] = bf16_lo(v.x), x[i + 1] = bf16_hi(v.x), x[i + 2] = bf16_lo(v.y), x[i + 3] = bf16_hi(v.y);
+        for (int u = 0; u < kTokensAtOnce; ++u) {
+            const int64_t at = min(t0 + u, last) * p.ld + e0;
+#pragma unroll
+            for (int i = 0; i + 3 < V; i += 4) {
+                if constexpr (F32) {
+                    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + at + i);
+                    x[u][i] = v.x, x[u][i + 1] = v.y, x[u][i + 2] = v.z, x[u][i + 3] = v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.logits) + at + i);
+                    x[u][i] = bf16_lo(v.x), x[u][i + 1] = bf16_hi(v.x);
+                    x[u][i + 2] = bf16_lo(v.y), x[u][i + 3] = bf16_hi(v.y);
+                }
             }
         }
         return;
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        x[i] = -INFINITY;
-        if (e0 + i < experts) {
-            if constexpr (F32) x[i] = static_cast<const float*>(base)[row + e0 + i];
-            else x[i] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[row + e0 + i] << 16);
+#pragma unroll
+        for (int u = 0; u < kTokensAtOnce; ++u) x[u][i] = -INFINITY;
+        if (e0 + i >= p.experts) continue;
+#pragma unroll
+        for (int u = 0; u < kTokensAtOnce; ++u) {
+            const int64_t at = min(t0 + u, last) * p.ld + e0 + i;
+            if constexpr (F32) x[u][i] = static_cast<const float*>(p.logits)[at];
+            else x[u][i] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.logits)[at] << 16);
         }
     }
 }
@@ -353,8 +366,6 @@ __device__ __forceinline__ void row_scores(const float (&x)[V], float (&s)[V]) {
     for (int i = 0; i < V; ++i) s[i] *= inv;
 }
 
-constexpr int kTokensAtOnce = 4;  // rows a wave has in flight
-
 // Whether a token has a valid route, for the wave (every lane gets it).
 __device__ __forceinline__ int valid_route(const BalanceArgs& p, int64_t token) {
     const int lane = threadIdx.x & 63;
@@ -365,7 +376,7 @@ __device__ __forceinline__ int valid_route(const BalanceArgs& p, int64_t token) 
 
 // One part: every wave takes four rows at a time, loads them together and adds
 // their scores in registers; the waves' sums meet in LDS in wave order. 16384
-// x 256 fp32: 11.3 us, 1.5 TB/s: a round trip for the part's place, one for its
+// x 256 fp32: 10.4 us, 1.6 TB/s: a round trip for the part's place, one for its
 // rows, then about 500 vector instructions for each four rows of a wave.
 template <int V, bool F32, bool SIGMOID, bool VEC>
 __global__ __launch_bounds__(kThreads) void balance_part_kernel(BalanceArgs p, BalancePlan b) {
@@ -397,8 +408,8 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(BalanceArgs p, B
         for (int u = 0; u < kTokensAtOnce; ++u) {
             const int64_t t = t0 + u;
             id[u] = t < stop ? valid_route(p, t) : -1;
-            load_row<V, F32, VEC>(p.logits, min(t, stop - 1) * p.ld, p.experts, x[u]);
         }
+        load_rows<V, F32, VEC>(p, t0, stop - 1, x);
 #pragma unroll
         for (int u = 0; u < kTokensAtOnce; ++u) {
             // (rows that are not counted go through the same steps, so that the
@@ -516,8 +527,8 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs p) {
     for (int u = 0; u < kTokensAtOnce; ++u) {
         const int64_t t = t0 + u;
         id[u] = t < p.tokens ? valid_route(p, t) : -1;
-        load_row<V, F32, VEC>(p.logits, min(t, p.tokens - 1) * p.ld, p.experts, x[u]);
     }
+    load_rows<V, F32, VEC>(p, t0, p.tokens - 1, x);
     const float g = p.grad ? *p.grad : 1.0f;
     // the sequence of the first row: the last one that starts at or before it
     int seq = 0;
