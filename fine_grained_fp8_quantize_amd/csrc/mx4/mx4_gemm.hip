@@ -333,18 +333,19 @@ hipError_t dispatch_rows_wide(const GemmArgs& p, int64_t tiles_m, hipStream_t st
     return hipGetLastError();
 }
 
-// Column tiles per workgroup: as many as leave three workgroups for four CUs,
-// since a workgroup with more of them reads A less often but runs longer (one
-// row, K = 7168, 1 / 2 / 4 column tiles: n = 4096: 6.2 / 7.3 / 9.5 us; 8192: 9.5 /
-// 8.5 / 10.7; 16384: 18.7 / 15.3 / 13.6). `busy`: row tiles that are likely to
-// have work.
+// Column tiles per workgroup: the fewest with which the workgroups are one round
+// of the 256 CUs, and at most four; a workgroup with more of them reads A less
+// often but runs longer (one row, K = 7168, 1 / 2 / 4 column tiles: n = 4096: 6.2 /
+// 7.3 / 9.5 us; 8192: 9.5 / 8.5 / 10.7; 16384: 18.7 / 15.3 / 13.6; 64 rows: n =
+// 8192: 15.5 / 13.3 / 18.0; 48 rows, K = 4096, n = 10000: 13.2 / 14.1 / 11.8).
+// `busy`: row tiles that are likely to have work.
 template <int MS, bool GROUPED>
 hipError_t dispatch_rows(const GemmArgs& p, int64_t tiles_m, int64_t busy, hipStream_t stream) {
     const int64_t tiles = busy * ((p.n + 15) / 16);
     if constexpr (MS != 2) {  // (two row tiles by four columns do not fit 128 registers)
-        if (tiles >= 4 * 192) return dispatch_rows_wide<MS, 4, GROUPED>(p, tiles_m, stream);
+        if (tiles > 512) return dispatch_rows_wide<MS, 4, GROUPED>(p, tiles_m, stream);
     }
-    if (tiles >= 2 * 192) return dispatch_rows_wide<MS, 2, GROUPED>(p, tiles_m, stream);
+    if (tiles > 256) return dispatch_rows_wide<MS, 2, GROUPED>(p, tiles_m, stream);
     return dispatch_rows_wide<MS, 1, GROUPED>(p, tiles_m, stream);
 }
 
