@@ -21,6 +21,8 @@ int check_balance(const void* logits, int logits_dtype, int64_t tokens, int32_t 
     if (tokens < 0 || tokens > kMaxInt || experts < 1 || experts > kMaxExperts || topk < 1 ||
         topk > FP8Q_MOE_MAX_TOPK || seqs < 1 || seqs > kMaxSeqs)
         return FP8Q_ERR_SHAPE;
+    // a sequence may hold every route: its totals and counts are int32
+    if (tokens * topk > kMaxInt) return FP8Q_ERR_SHAPE;
     if (!seq_offsets && seqs != 1) return FP8Q_ERR_NULL;
     if (!is_aligned(seq_offsets, 4)) return FP8Q_ERR_ALIGN;
     if (tokens == 0) return FP8Q_OK;

@@ -80,7 +80,7 @@ int moe_dispatch(const int32_t *ids, int64_t tokens, int32_t topk, int32_t first
  *             moe_balance_workspace_bytes(tokens, experts, seqs) bytes.
  * The sums are taken in a fixed order: results repeat bit for bit.
  * Shapes: experts 1..FP8Q_MOE_MAX_EXPERTS, topk 1..8, seqs 1..FP8Q_MOE_MAX_SEQS,
- *         tokens < 2^31.
+ *         tokens * topk < 2^31 (the counts are int32).
  *         tokens == 0: loss, counts and coef are written as zeros.
  * seq_offsets is trusted to keep its contract; values that break it give
  * unspecified numbers (no access outside the arrays).
