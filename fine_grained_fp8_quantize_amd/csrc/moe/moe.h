@@ -46,6 +46,7 @@ struct BalanceArgs {
     const float* grad;
     void* dlogits;
     int64_t ld_d;
+    int64_t token0;  // the launch's first token
 };
 
 int64_t balance_workspace_bytes(int64_t tokens, int64_t experts, int64_t seqs);

@@ -9,6 +9,7 @@
 #include "moe/moe.h"
 
 #include "fp8q_device.h"
+#include "moe/moe_launch.hpp"
 
 #include <math.h>
 
@@ -517,9 +518,10 @@ __global__ __launch_bounds__(kThreads) void balance_finish_kernel(BalanceArgs p,
 // Four rows per wave, scores computed again rather than read (they would be as
 // many bytes as the logits): 16384 x 256 fp32: 11.7 us, 2.9 TB/s read and written.
 template <int V, bool F32, bool SIGMOID, bool VEC>
-__global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs p) {
+__global__ __launch_bounds__(kBackwardThreads) void balance_backward_kernel(BalanceArgs p) {
+    static_assert(kBackwardRows == kBackwardThreads / 64 * kTokensAtOnce, "every wave takes its rows once");
     const int lane = threadIdx.x & 63;
-    const int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * kTokensAtOnce;
+    const int64_t t0 = p.token0 + ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * kTokensAtOnce;
     if (t0 >= p.tokens) return;
     float x[kTokensAtOnce][V];
     int id[kTokensAtOnce];
@@ -649,13 +651,19 @@ hipError_t launch_balance(const BalanceArgs& p, hipStream_t stream) {
 }
 
 hipError_t launch_balance_backward(const BalanceArgs& p, hipStream_t stream) {
-    const dim3 grid((unsigned)ceil_div(p.tokens, 4 * kTokensAtOnce));
     const bool vec = rows_aligned(p.logits, p.ld, p.f32) && rows_aligned(p.dlogits, p.ld_d, p.f32);
-    return with_width(p, vec, [&](auto v, auto f32, auto sigmoid, auto aligned) {
-        hipLaunchKernelGGL((balance_backward_kernel<decltype(v)::value, decltype(f32)::value, decltype(sigmoid)::value,
-                                                    decltype(aligned)::value>),
-                           grid, dim3(256), 0, stream, p);
-    });
+    for (int64_t t0 = 0; t0 < p.tokens; t0 += kBackwardTokens) {
+        BalanceArgs a = p;
+        a.token0 = t0;
+        const LaunchShape shape = backward_shape(p.tokens - t0 < kBackwardTokens ? p.tokens - t0 : kBackwardTokens);
+        const hipError_t e = with_width(a, vec, [&](auto v, auto f32, auto sigmoid, auto aligned) {
+            hipLaunchKernelGGL((balance_backward_kernel<decltype(v)::value, decltype(f32)::value,
+                                                        decltype(sigmoid)::value, decltype(aligned)::value>),
+                               dim3((unsigned)shape.blocks), dim3(shape.threads), 0, stream, a);
+        });
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace moe
