@@ -26,15 +26,10 @@
 #include <hip/hip_runtime_api.h>
 #include <stdint.h>
 
+#include "mx4/mx4_launch.hpp"
+
 namespace fp8q {
 namespace mx4 {
-
-constexpr int kTileRows = 16;
-constexpr int kTileK = 128;
-constexpr int kTileBytes = 1024;
-constexpr int kGroupTiles = 4;              // K tiles that share scale words
-constexpr int kGroupK = kTileK * kGroupTiles;
-constexpr int kScaleWords = 64;             // per row tile and K group
 
 struct QuantArgs {
     const uint16_t* x;

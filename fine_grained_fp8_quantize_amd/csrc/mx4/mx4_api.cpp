@@ -18,7 +18,14 @@ constexpr int64_t kMaxBytes = 1LL << 60;
 
 bool size_ok(int64_t v) { return v >= 0 && v <= kMaxSize; }
 
-int64_t tiles_of(int64_t v, int64_t per) { return (v + per - 1) / per; }
+int64_t tiles_of(int64_t v, int64_t per) { return ceil_div(v, per); }
+
+// Units of 16 rows x 512 k of `groups` matrices stay below what the launch
+// sizes can be computed from.
+bool units_ok(int64_t groups, int64_t rows, int64_t k) {
+    const int64_t units = mul_limit(tiles_of(rows, kTileRows), tiles_of(k, kGroupK), kMaxSize);
+    return units >= 0 && mul_limit(units, groups, kMaxSize) >= 0;
+}
 
 // ld row tiles between `outer` slabs of `unit` elements hold the matrix and
 // stay addressable.
@@ -90,9 +97,9 @@ int fp4_quantize_mx(int32_t groups, const uint16_t* x, int64_t rows, int64_t col
             return FP8Q_ERR_SHAPE;
     }
     if (!is_aligned(x, 2) || (groups > 1 && stride_q % 16 != 0)) return FP8Q_ERR_ALIGN;
-    // blocks of either kernel: one per 16 x 512 unit at most
-    const int64_t units = mul_limit(tiles_of(out_rows, kTileRows), kg, kMaxSize);
-    if (units < 0 || !blocks_ok(mul_limit(units, groups, kMaxSize))) return FP8Q_ERR_SHAPE;
+    if (!units_ok(groups, out_rows, k)) return FP8Q_ERR_SHAPE;
+    if (!launchable(along_rows ? quant_rows_shape(groups, rows, cols) : quant_cols_shape(groups, rows, cols)))
+        return FP8Q_ERR_SHAPE;
     QuantArgs p = {};
     p.x = x; p.rows = rows; p.cols = cols; p.ld_x = ld_x; p.stride_x = groups > 1 ? stride_x : 0;
     p.q = q; p.ld_q = ld_q; p.stride_q = groups > 1 ? stride_q : 0;
@@ -112,7 +119,7 @@ int fp4_quantize_mx_scatter(const uint16_t* x, int64_t tokens, int64_t cols, int
     if (st != FP8Q_OK) return st;
     if (ld_x < cols || mul_limit(tokens, ld_x, kMaxBytes / 2) < 0) return FP8Q_ERR_SHAPE;
     if (!is_aligned(x, 2) || !is_aligned(dst_rows, 4)) return FP8Q_ERR_ALIGN;
-    if (!blocks_ok(mul_limit(tiles_of(tokens, kTileRows), tiles_of(cols, kGroupK), kMaxSize))) return FP8Q_ERR_SHAPE;
+    if (!units_ok(1, tokens, cols) || !launchable(quant_rows_shape(1, tokens, cols))) return FP8Q_ERR_SHAPE;
     ScatterArgs p = {};
     p.x = x; p.tokens = tokens; p.cols = cols; p.ld_x = ld_x;
     p.topk = topk; p.dst = dst_rows; p.m_total = m_total;
@@ -132,7 +139,7 @@ int fp4_dequantize_mx(const uint8_t* q, int64_t ld_q, const uint32_t* scale, int
     const bool f32 = out_dtype == FP8Q_OUT_F32;
     if (ld_y < cols || mul_limit(rows, ld_y, kMaxBytes / 4) < 0) return FP8Q_ERR_SHAPE;
     if (!is_aligned(y, f32 ? 4 : 2)) return FP8Q_ERR_ALIGN;
-    if (!blocks_ok(mul_limit(tiles_of(rows, kTileRows), tiles_of(cols, kGroupK), kMaxSize))) return FP8Q_ERR_SHAPE;
+    if (!units_ok(1, rows, cols) || !launchable(quant_rows_shape(1, rows, cols))) return FP8Q_ERR_SHAPE;
     DequantArgs p = {};
     p.q = q; p.ld_q = ld_q; p.scale = scale; p.ld_s = ld_s;
     p.rows = rows; p.cols = cols; p.y = y; p.ld_y = ld_y; p.f32 = f32;
@@ -148,10 +155,11 @@ int fp4_gemm_mx(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t ld_a,
     if (m == 0 || n == 0) return FP8Q_OK;
     const int st = check_gemm(m, n, k, a, ld_a, a_scale, ld_as, b, ld_b, b_scale, ld_bs, c, ldc, out_dtype);
     if (st != FP8Q_OK) return st;
-    // the smallest output tile that any kernel gives a block is 16 x 16
+    // the kernels number output tiles, of 16 x 16 at the least, with 32 bits
     if (!blocks_ok(mul_limit(tiles_of(m, 16), tiles_of(n, 16), kMaxSize))) return FP8Q_ERR_SHAPE;
-    return hip_status(launch_gemm(
-        gemm_args(m, n, k, a, ld_a, a_scale, ld_as, b, ld_b, b_scale, ld_bs, c, ldc, out_dtype), stream));
+    const GemmArgs p = gemm_args(m, n, k, a, ld_a, a_scale, ld_as, b, ld_b, b_scale, ld_bs, c, ldc, out_dtype);
+    if (!launchable(gemm_shape(gemm_form(m, n), m, n, p.kt))) return FP8Q_ERR_SHAPE;
+    return hip_status(launch_gemm(p, stream));
 }
 
 int fp4_grouped_gemm_mx(int32_t groups, const int32_t* group_offsets, const int32_t* group_rows, int64_t m_total,
@@ -172,6 +180,7 @@ int fp4_grouped_gemm_mx(int32_t groups, const int32_t* group_offsets, const int3
     GemmArgs p = gemm_args(m_total, n, k, a, ld_a, a_scale, ld_as, b, ld_b, b_scale, ld_bs, c, ldc, out_dtype);
     p.groups = groups; p.group_offsets = group_offsets; p.group_rows = group_rows;
     p.stride_b = stride_b; p.stride_bs = stride_bs;
+    if (!launchable(grouped_shape(grouped_form(m_total, n, groups), m_total, n, p.kt, groups))) return FP8Q_ERR_SHAPE;
     return hip_status(launch_grouped_gemm(p, stream));
 }
 

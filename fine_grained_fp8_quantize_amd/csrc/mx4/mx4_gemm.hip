@@ -230,12 +230,8 @@ __device__ __forceinline__ v4i load_weights(const uint8_t* p) {
 // Bound by the HBM stream of the weights: 1 x 4096 x 7168: 6.0 us, 2.6 TB/s (a
 // launch and two dependent waits are most of it); 1 x 16384 x 7168: 13.6 us, 4.6
 // TB/s.
-// With four row tiles a wave needs up to 200 registers: eight waves.
-template <int MS>
-constexpr int kMaxWaves = MS >= 4 ? 8 : 16;
-
 template <int MS, int NT, bool F32, bool GROUPED>
-__global__ __launch_bounds__(64 * kMaxWaves<MS>) void gemm_rows_kernel(GemmArgs p, int tiles_n) {
+__global__ __launch_bounds__(64 * max_waves(MS)) void gemm_rows_kernel(GemmArgs p, int tiles_n) {
     extern __shared__ v4f partial[];  // [waves][NT][MS][64]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     Rows t;
@@ -318,14 +314,10 @@ __global__ __launch_bounds__(64 * kMaxWaves<MS>) void gemm_rows_kernel(GemmArgs 
 }
 
 template <int MS, int NT, bool GROUPED>
-hipError_t dispatch_rows_wide(const GemmArgs& p, int64_t tiles_m, hipStream_t stream) {
-    const int tiles_n = (p.n + 16 * NT - 1) / (16 * NT), kg = (p.kt + kGroupTiles - 1) / kGroupTiles;
-    // every wave the same number of K groups, as far as they divide
-    const int rounds = kg > 0 ? (kg + kMaxWaves<MS> - 1) / kMaxWaves<MS> : 1;
-    const int waves = kg > 0 ? (kg + rounds - 1) / rounds : 1;
-    const int64_t tiles = tiles_m * tiles_n;
-    const dim3 grid((unsigned)(GROUPED ? (tiles + 255) / 256 * 256 : tiles)), block(64 * waves);
-    const size_t lds = (size_t)waves * NT * MS * 64 * sizeof(v4f);
+hipError_t dispatch_rows(const GemmArgs& p, LaunchShape s, hipStream_t stream) {
+    const int tiles_n = (p.n + 16 * NT - 1) / (16 * NT);
+    const dim3 grid((unsigned)s.blocks), block(s.threads);
+    const size_t lds = (size_t)s.threads * NT * MS * sizeof(v4f);
     if (p.out_f32)
         hipLaunchKernelGGL((gemm_rows_kernel<MS, NT, true, GROUPED>), grid, block, lds, stream, p, tiles_n);
     else
@@ -333,20 +325,20 @@ hipError_t dispatch_rows_wide(const GemmArgs& p, int64_t tiles_m, hipStream_t st
     return hipGetLastError();
 }
 
-// Column tiles per workgroup: the fewest with which the workgroups are one round
-// of the 256 CUs, and at most four; a workgroup with more of them reads A less
-// often but runs longer (one row, K = 7168, 1 / 2 / 4 column tiles: n = 4096: 6.2 /
-// 7.3 / 9.5 us; 8192: 9.5 / 8.5 / 10.7; 16384: 18.7 / 15.3 / 13.6; 64 rows: n =
-// 8192: 15.5 / 13.3 / 18.0; 48 rows, K = 4096, n = 10000: 13.2 / 14.1 / 11.8).
-// `busy`: row tiles that are likely to have work.
-template <int MS, bool GROUPED>
-hipError_t dispatch_rows(const GemmArgs& p, int64_t tiles_m, int64_t busy, hipStream_t stream) {
-    const int64_t tiles = busy * ((p.n + 15) / 16);
-    if constexpr (MS != 2) {  // (two row tiles by four columns do not fit 128 registers)
-        if (tiles > 512) return dispatch_rows_wide<MS, 4, GROUPED>(p, tiles_m, stream);
+template <bool GROUPED>
+hipError_t dispatch_rows(const GemmArgs& p, GemmForm f, LaunchShape s, hipStream_t stream) {
+    if (f.ms == 1) {
+        if (f.nt == 1) return dispatch_rows<1, 1, GROUPED>(p, s, stream);
+        if (f.nt == 2) return dispatch_rows<1, 2, GROUPED>(p, s, stream);
+        return dispatch_rows<1, 4, GROUPED>(p, s, stream);
     }
-    if (tiles > 256) return dispatch_rows_wide<MS, 2, GROUPED>(p, tiles_m, stream);
-    return dispatch_rows_wide<MS, 1, GROUPED>(p, tiles_m, stream);
+    if (f.ms == 2) {
+        if (f.nt == 1) return dispatch_rows<2, 1, GROUPED>(p, s, stream);
+        return dispatch_rows<2, 2, GROUPED>(p, s, stream);
+    }
+    if (f.nt == 1) return dispatch_rows<4, 1, GROUPED>(p, s, stream);
+    if (f.nt == 2) return dispatch_rows<4, 2, GROUPED>(p, s, stream);
+    return dispatch_rows<4, 4, GROUPED>(p, s, stream);
 }
 
 // ------------------------------------------------------------ many rows
@@ -674,9 +666,8 @@ __global__ __launch_bounds__(256, 1) void grouped_tiles_kernel(GemmArgs p) {
 }
 
 template <int TM, int TN>
-hipError_t dispatch_tiles(const GemmArgs& p, hipStream_t stream) {
-    const int64_t tiles = (int64_t)((p.m + 32 * TM - 1) / (32 * TM)) * ((p.n + 32 * TN - 1) / (32 * TN));
-    const dim3 grid((unsigned)((tiles + 7) / 8 * 8)), block(256);
+hipError_t dispatch_tiles(const GemmArgs& p, LaunchShape s, hipStream_t stream) {
+    const dim3 grid((unsigned)s.blocks), block(s.threads);
     if (p.out_f32)
         hipLaunchKernelGGL((gemm_tiles_kernel<TM, TN, true>), grid, block, 0, stream, p);
     else
@@ -684,10 +675,8 @@ hipError_t dispatch_tiles(const GemmArgs& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t dispatch_grouped_tiles(const GemmArgs& p, hipStream_t stream) {
-    // at most one ragged tile per segment, and one past the last
-    const int64_t tiles = (int64_t)(p.m / 256 + p.groups + 1) * ((p.n + 255) / 256);
-    const dim3 grid((unsigned)((tiles + 255) / 256 * 256)), block(256);
+hipError_t dispatch_grouped_tiles(const GemmArgs& p, LaunchShape s, hipStream_t stream) {
+    const dim3 grid((unsigned)s.blocks), block(s.threads);
     if (p.out_f32)
         hipLaunchKernelGGL((grouped_tiles_kernel<true>), grid, block, 0, stream, p);
     else
@@ -695,49 +684,19 @@ hipError_t dispatch_grouped_tiles(const GemmArgs& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Rounds of the 256 CUs that tiles of size x size take.
-int64_t rounds_of(const GemmArgs& p, int size) {
-    const int64_t tiles = (int64_t)((p.m + size - 1) / size) * ((p.n + size - 1) / size);
-    return (tiles + 255) / 256;
-}
-
 }  // namespace
 
 hipError_t launch_gemm(const GemmArgs& p, hipStream_t stream) {
-    if (p.m <= 16) return dispatch_rows<1, false>(p, 1, 1, stream);
-    if (p.m <= 32) return dispatch_rows<2, false>(p, 1, 1, stream);
-    // Pieces of 64 x 64 with K split over a workgroup's waves, while they are
-    // less than one round of the CUs: a whole K sum per wave is the longer way
-    // (64 x 4096 x 7168: 10.3 against 14.7 us with 128 x 128 tiles; 256 x 4096 x
-    // 7168, 256 pieces: 17.0 against 15.0).
-    const int64_t rows64 = (p.m + 63) / 64;
-    if (rows64 * ((p.n + 63) / 64) <= 192) return dispatch_rows<4, false>(p, rows64, rows64, stream);
-    // 256 x 256 tiles or 128 x 128 ones, by the time of a round of the 256 CUs:
-    // a tile of the first kind takes about as long as 3.2 of the second one
-    // after the other on a CU (two share it). (4096 x 4096 x 7168: 59 against
-    // 69 us; 2048 x 4096 x 7168: 42 against 36; 1024 x 4096 x 7168: 40 against 20.)
-    const int64_t big = rounds_of(p, 256), small = rounds_of(p, 128);
-    return 16 * big <= 5 * small ? dispatch_tiles<8, 8>(p, stream) : dispatch_tiles<4, 4>(p, stream);
+    const GemmForm f = gemm_form(p.m, p.n);
+    const LaunchShape s = gemm_shape(f, p.m, p.n, p.kt);
+    if (f.kernel == GemmKernel::kRows) return dispatch_rows<false>(p, f, s, stream);
+    return f.ms == 8 ? dispatch_tiles<8, 8>(p, s, stream) : dispatch_tiles<4, 4>(p, s, stream);
 }
 
 hipError_t launch_grouped_gemm(const GemmArgs& p, hipStream_t stream) {
-    // How many rows an expert has is not known here; p.m bounds their sum.
-    const int64_t avg = p.m / p.groups, columns = (p.n + 255) / 256;
-    // Tiles of 256 columns once the experts alone give three tiles for four CUs
-    // (27 experts with 2 rows, 2048 x 4096, 216 tiles: 27 us, 28 without LDS);
-    // otherwise narrow pieces with K split over the waves.
-    if (p.groups * ((avg + 255) / 256) * columns >= 192) return dispatch_grouped_tiles(p, stream);
-    // Row tiles of 16, 32 or 64 rows, or 256 x 256 tiles again when there are
-    // rows for them (8 experts, 2048 x 4096, us for each of the four: 16 rows an
-    // expert: 9.9 / 10.2 / 13.4 / 19.8; 32: 12.7 / 11.2 / 13.6 / 20.7; 48: 16.8 /
-    // 16.2 / 13.8 / 21.5; 64: 20.4 / 17.1 / 14.8 / 22.6; 128: 35.1 / 28.6 / 24.4 /
-    // 25.0; 256: 65.3 / 52.2 / 42.4 / 31.7). At most one ragged row tile per
-    // segment, and one past the last.
-    if (avg <= 20) return dispatch_rows<1, true>(p, p.m / 16 + p.groups + 1, p.groups, stream);
-    if (avg <= 40) return dispatch_rows<2, true>(p, p.m / 32 + p.groups + 1, p.groups, stream);
-    const int64_t rows64 = p.m / 64 + p.groups + 1;
-    if (rows64 * ((p.n + 63) / 64) <= 768) return dispatch_rows<4, true>(p, rows64, rows64, stream);
-    return dispatch_grouped_tiles(p, stream);
+    const GemmForm f = grouped_form(p.m, p.n, p.groups);
+    const LaunchShape s = grouped_shape(f, p.m, p.n, p.kt, p.groups);
+    return f.kernel == GemmKernel::kRows ? dispatch_rows<true>(p, f, s, stream) : dispatch_grouped_tiles(p, s, stream);
 }
 
 }  // namespace mx4

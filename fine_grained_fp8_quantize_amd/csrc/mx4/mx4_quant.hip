@@ -96,7 +96,6 @@ __device__ __forceinline__ void store_nt16(void* p, uint4 v) {
 }
 
 constexpr int kMaxTopk = 8;
-constexpr int kQuantWaves = 4;
 // One wave's staging: four tiles, 16 words apart so that the four tiles'
 // equal places fall into different banks.
 constexpr int kStageTile = kTileBytes / 4 + 16;
@@ -153,9 +152,6 @@ __device__ __forceinline__ uint32_t quad_max_u16x2(uint32_t v) {
 // maximum. (64 channels, 128 bytes of 8 tokens: a tenth slower where rows do
 // not start on 128-byte lines, as each piece then touches two.) 4096 x 7168: 17.0
 // us, 4.4 TB/s; 8192 x 2040: 11.0 us, 3.9 TB/s.
-constexpr int kColsThreads = 512;
-constexpr int kColsKTiles = 2;
-constexpr int kColsChannels = 128;
 // LDS words of a tile and of its upper eight rows: the 16 (tile, half) pairs
 // that one store instruction touches start 4 banks apart.
 constexpr int kColsTile = kTileBytes / 4 + 8;
@@ -340,13 +336,13 @@ __global__ __launch_bounds__(64 * kQuantWaves) void dequant_kernel(DequantArgs p
     }
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 }  // namespace
 
 hipError_t launch_quant_rows(const QuantArgs& p, hipStream_t stream) {
-    const int64_t rt = ceil_div(p.rows, kTileRows), kg = ceil_div(p.cols, kGroupK), units = p.groups * rt * kg;
-    const dim3 grid((unsigned)ceil_div(units, kQuantWaves)), block(64 * kQuantWaves);
+    const int64_t rt = ceil_div(p.rows, kTileRows), kg = ceil_div(p.cols, kGroupK);
+    const int64_t units = quant_rows_units(p.groups, p.rows, p.cols);
+    const LaunchShape s = quant_rows_shape(p.groups, p.rows, p.cols);
+    const dim3 grid((unsigned)s.blocks), block(s.threads);
     if (p.vec)
         hipLaunchKernelGGL((quant_rows_kernel<true>), grid, block, 0, stream, p, rt, kg, units);
     else
@@ -355,10 +351,10 @@ hipError_t launch_quant_rows(const QuantArgs& p, hipStream_t stream) {
 }
 
 hipError_t launch_quant_cols(const QuantArgs& p, hipStream_t stream) {
-    // both halves of the last K group, whose scale bytes must all be written
-    const int64_t ct = ceil_div(p.cols, kColsChannels), halves = 2 * ceil_div(p.rows, kGroupK);
-    const int64_t units = p.groups * ct * halves;
-    const dim3 grid((unsigned)(ceil_div(units, 8) * 8)), block(kColsThreads);
+    const int64_t ct = ceil_div(p.cols, kColsChannels), halves = quant_cols_halves(p.rows);
+    const int64_t units = quant_cols_units(p.groups, p.rows, p.cols);
+    const LaunchShape s = quant_cols_shape(p.groups, p.rows, p.cols);
+    const dim3 grid((unsigned)s.blocks), block(s.threads);
     if (p.vec)
         hipLaunchKernelGGL((quant_cols_kernel<true>), grid, block, 0, stream, p, ct, halves, units);
     else
@@ -367,8 +363,9 @@ hipError_t launch_quant_cols(const QuantArgs& p, hipStream_t stream) {
 }
 
 hipError_t launch_quant_scatter(const ScatterArgs& p, hipStream_t stream) {
-    const int64_t kg = ceil_div(p.cols, kGroupK), units = ceil_div(p.tokens, kTileRows) * kg;
-    const dim3 grid((unsigned)ceil_div(units, kQuantWaves)), block(64 * kQuantWaves);
+    const int64_t kg = ceil_div(p.cols, kGroupK), units = quant_rows_units(1, p.tokens, p.cols);
+    const LaunchShape s = quant_rows_shape(1, p.tokens, p.cols);
+    const dim3 grid((unsigned)s.blocks), block(s.threads);
     if (p.vec)
         hipLaunchKernelGGL((quant_scatter_kernel<true>), grid, block, 0, stream, p, kg, units);
     else
@@ -377,8 +374,9 @@ hipError_t launch_quant_scatter(const ScatterArgs& p, hipStream_t stream) {
 }
 
 hipError_t launch_dequant(const DequantArgs& p, hipStream_t stream) {
-    const int64_t kg = ceil_div(p.cols, kGroupK), units = ceil_div(p.rows, kTileRows) * kg;
-    const dim3 grid((unsigned)ceil_div(units, kQuantWaves)), block(64 * kQuantWaves);
+    const int64_t kg = ceil_div(p.cols, kGroupK), units = quant_rows_units(1, p.rows, p.cols);
+    const LaunchShape s = quant_rows_shape(1, p.rows, p.cols);
+    const dim3 grid((unsigned)s.blocks), block(s.threads);
     if (p.f32) {
         if (p.vec)
             hipLaunchKernelGGL((dequant_kernel<true, true>), grid, block, 0, stream, p, kg, units);

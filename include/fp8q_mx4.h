@@ -41,6 +41,9 @@ extern "C" {
 #define FP4Q_TILE_32x1 1 /* blocks along the columns of x: the transposed operand   */
 
 /*
+ * Limits of every call: its launch holds fewer than 2^32 work-items, that is
+ * fewer than 2^26 units of 16 rows x 512 k (1x32, scatter, read-back) or 2^23
+ * units of 256 rows x 128 columns of x (32x1), parts of units counted whole.
  * Limits of the products: rows of A, B and C are numbered with 32 bits (a
  * tile of 256 rows may start at the last one). Codes and scales are addressed
  * with 64 bits. Larger values return FP8Q_ERR_SHAPE before any launch.
@@ -62,7 +65,7 @@ extern "C" {
  *         matrices (groups > 1: stride_q >= kt * ld_q * 1024, % 16 == 0).
  * scale   words; ld_s row tiles between K groups, stride_s words between
  *         matrices (groups > 1: stride_s >= ceil(kt / 4) * ld_s * 64).
- * Any rows, cols >= 0 and any ld_x; rows of x that start on 16-byte
+ * Any rows, cols >= 0 within the limits and any ld_x; rows of x that start on 16-byte
  * boundaries (x, ld_x and stride_x so aligned) are read faster.
  * groups, rows or cols == 0: returns FP8Q_OK without launching.
  * Errors: FP8Q_ERR_NULL, FP8Q_ERR_SHAPE, FP8Q_ERR_ALIGN (x not 2-byte
