@@ -88,6 +88,7 @@ struct GemmArgs {
     bool out_f32;
     bool c_vec;    // four adjacent outputs of a row may be stored together
     bool c_vec16;  // rows start on 16-byte boundaries
+    bool scales16;  // all scale arrays start on 16-byte boundaries
     // grouped problems only: expert e owns rows [off[e], off[e+1]) of A and C
     int32_t groups;
     const int32_t* group_offsets;

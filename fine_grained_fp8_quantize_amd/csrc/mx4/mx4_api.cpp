@@ -67,6 +67,7 @@ GemmArgs gemm_args(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t ld
     p.b = b; p.ld_b = ld_b; p.b_scale = b_scale; p.ld_bs = ld_bs;
     p.c = c; p.ldc = ldc; p.out_f32 = out_dtype == FP8Q_OUT_F32;
     p.c_vec = ldc % 4 == 0 && is_aligned(c, p.out_f32 ? 16 : 8);
+    p.scales16 = is_aligned(a_scale, 16) && is_aligned(b_scale, 16);
     p.c_vec16 = ldc % (p.out_f32 ? 4 : 8) == 0 && is_aligned(c, 16);
     return p;
 }
@@ -158,7 +159,7 @@ int fp4_gemm_mx(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t ld_a,
     // the kernels number output tiles, of 16 x 16 at the least, with 32 bits
     if (!blocks_ok(mul_limit(tiles_of(m, 16), tiles_of(n, 16), kMaxSize))) return FP8Q_ERR_SHAPE;
     const GemmArgs p = gemm_args(m, n, k, a, ld_a, a_scale, ld_as, b, ld_b, b_scale, ld_bs, c, ldc, out_dtype);
-    if (!launchable(gemm_shape(gemm_form(m, n), m, n, p.kt))) return FP8Q_ERR_SHAPE;
+    if (!launchable(gemm_shape(gemm_form(m, n, p.scales16), m, n, p.kt))) return FP8Q_ERR_SHAPE;
     return hip_status(launch_gemm(p, stream));
 }
 
@@ -180,7 +181,9 @@ int fp4_grouped_gemm_mx(int32_t groups, const int32_t* group_offsets, const int3
     GemmArgs p = gemm_args(m_total, n, k, a, ld_a, a_scale, ld_as, b, ld_b, b_scale, ld_bs, c, ldc, out_dtype);
     p.groups = groups; p.group_offsets = group_offsets; p.group_rows = group_rows;
     p.stride_b = stride_b; p.stride_bs = stride_bs;
-    if (!launchable(grouped_shape(grouped_form(m_total, n, groups), m_total, n, p.kt, groups))) return FP8Q_ERR_SHAPE;
+    p.scales16 = p.scales16 && (groups == 1 || stride_bs % 4 == 0);
+    if (!launchable(grouped_shape(grouped_form(m_total, n, groups, p.scales16), m_total, n, p.kt, groups)))
+        return FP8Q_ERR_SHAPE;
     return hip_status(launch_grouped_gemm(p, stream));
 }
 

@@ -687,14 +687,14 @@ hipError_t dispatch_grouped_tiles(const GemmArgs& p, LaunchShape s, hipStream_t 
 }  // namespace
 
 hipError_t launch_gemm(const GemmArgs& p, hipStream_t stream) {
-    const GemmForm f = gemm_form(p.m, p.n);
+    const GemmForm f = gemm_form(p.m, p.n, p.scales16);
     const LaunchShape s = gemm_shape(f, p.m, p.n, p.kt);
     if (f.kernel == GemmKernel::kRows) return dispatch_rows<false>(p, f, s, stream);
     return f.ms == 8 ? dispatch_tiles<8, 8>(p, s, stream) : dispatch_tiles<4, 4>(p, s, stream);
 }
 
 hipError_t launch_grouped_gemm(const GemmArgs& p, hipStream_t stream) {
-    const GemmForm f = grouped_form(p.m, p.n, p.groups);
+    const GemmForm f = grouped_form(p.m, p.n, p.groups, p.scales16);
     const LaunchShape s = grouped_shape(f, p.m, p.n, p.kt, p.groups);
     return f.kernel == GemmKernel::kRows ? dispatch_rows<true>(p, f, s, stream) : dispatch_grouped_tiles(p, s, stream);
 }

@@ -78,7 +78,10 @@ inline int64_t rounds_of(int64_t m, int64_t n, int64_t size) {
     return ceil_div(ceil_div(m, size) * ceil_div(n, size), 256);
 }
 
-inline GemmForm gemm_form(int64_t m, int64_t n) {
+// scales16: both scale arrays (every expert's) start on 16-byte boundaries. The
+// tile kernels copy scale words to LDS 16 bytes at a time; scales that are
+// aligned to their 4-byte words only go to the rows kernel, which reads words.
+inline GemmForm gemm_form(int64_t m, int64_t n, bool scales16) {
     if (m <= 16) return rows_form(1, 1, n);
     if (m <= 32) return rows_form(2, 1, n);
     // Pieces of 64 x 64 with K split over a workgroup's waves, while they are
@@ -86,7 +89,7 @@ inline GemmForm gemm_form(int64_t m, int64_t n) {
     // (64 x 4096 x 7168: 10.3 against 14.7 us with 128 x 128 tiles; 256 x 4096 x
     // 7168, 256 pieces: 17.0 against 15.0).
     const int64_t rows64 = ceil_div(m, 64);
-    if (rows64 * ceil_div(n, 64) <= 192) return rows_form(4, rows64, n);
+    if (!scales16 || rows64 * ceil_div(n, 64) <= 192) return rows_form(4, rows64, n);
     // 256 x 256 tiles or 128 x 128 ones, by the time of a round of the 256 CUs:
     // a tile of the first kind takes about as long as 3.2 of the second one
     // after the other on a CU (two share it). (4096 x 4096 x 7168: 59 against
@@ -95,13 +98,13 @@ inline GemmForm gemm_form(int64_t m, int64_t n) {
     return {GemmKernel::kTiles, size, size};
 }
 
-inline GemmForm grouped_form(int64_t m_total, int64_t n, int64_t groups) {
+inline GemmForm grouped_form(int64_t m_total, int64_t n, int64_t groups, bool scales16) {
     // How many rows an expert has is not known here; m_total bounds their sum.
     const int64_t avg = m_total / groups, columns = ceil_div(n, 256);
     // Tiles of 256 columns once the experts alone give three tiles for four CUs
     // (27 experts with 2 rows, 2048 x 4096, 216 tiles: 27 us, 28 without LDS);
     // otherwise narrow pieces with K split over the waves.
-    if (groups * ceil_div(avg, 256) * columns >= 192) return {GemmKernel::kGroupedTiles, 8, 8};
+    if (scales16 && groups * ceil_div(avg, 256) * columns >= 192) return {GemmKernel::kGroupedTiles, 8, 8};
     // Row tiles of 16, 32 or 64 rows, or 256 x 256 tiles again when there are
     // rows for them (8 experts, 2048 x 4096, us for each of the four: 16 rows an
     // expert: 9.9 / 10.2 / 13.4 / 19.8; 32: 12.7 / 11.2 / 13.6 / 20.7; 48: 16.8 /
@@ -110,7 +113,7 @@ inline GemmForm grouped_form(int64_t m_total, int64_t n, int64_t groups) {
     if (avg <= 20) return rows_form(1, groups, n);
     if (avg <= 40) return rows_form(2, groups, n);
     const int64_t rows64 = m_total / 64 + groups + 1;
-    if (rows64 * ceil_div(n, 64) <= 768) return rows_form(4, rows64, n);
+    if (!scales16 || rows64 * ceil_div(n, 64) <= 768) return rows_form(4, rows64, n);
     return {GemmKernel::kGroupedTiles, 8, 8};
 }
 

@@ -24,7 +24,8 @@
  * larger matrix is a matrix with the same ld. Rows and elements past the
  * matrix, up to whole tiles, are written as zero codes; scale bytes of whole
  * blocks past it, up to 16 rows and 512 k, as 0.
- * Alignment: codes 16 bytes, scales 4 bytes.
+ * Alignment: codes 16 bytes, scales 4 bytes. Products of many rows are faster
+ * with scales (and experts' scales) that start on 16-byte boundaries.
  */
 #ifndef FP8Q_MX4_H
 #define FP8Q_MX4_H

@@ -30,3 +30,20 @@ def shape(name: str, *args: int) -> tuple[int, int]:
     blocks, threads = ctypes.c_int64(), ctypes.c_int()
     getattr(lib(), name)(*[ctypes.c_int64(a) for a in args], ctypes.byref(blocks), ctypes.byref(threads))
     return blocks.value, threads.value
+
+
+KERNELS = ("rows", "tiles", "grouped tiles")
+
+
+def gemm_form(m: int, n: int, scales16: bool = True) -> tuple[str, int, int]:
+    """Kernel of a dense FP4 product, and its tile's parameters."""
+    out = (ctypes.c_int * 3)()
+    lib().fp4_gemm_form(ctypes.c_int64(m), ctypes.c_int64(n), int(scales16), out)
+    return KERNELS[out[0]], out[1], out[2]
+
+
+def grouped_form(m_total: int, n: int, groups: int, scales16: bool = True) -> tuple[str, int, int]:
+    """Kernel of a grouped FP4 product, and its tile's parameters."""
+    out = (ctypes.c_int * 3)()
+    lib().fp4_grouped_form(ctypes.c_int64(m_total), ctypes.c_int64(n), ctypes.c_int64(groups), int(scales16), out)
+    return KERNELS[out[0]], out[1], out[2]
