@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libfp8q.so")
 SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "mx4/mx4_api.cpp", "mx4/mx4_quant.hip", "mx4/mx4_gemm.hip",
            "moe/moe_api.cpp", "moe/moe.hip"]
 HEADERS = ["fp8q_device.h", "gemm_common.h", "launch.h", "host_checks.hpp", "launch_shape.hpp", "mx4/mx4.h",
-           "mx4/mx4_launch.hpp", "moe/moe.h", "moe/moe_launch.hpp"]
+           "mx4/mx4_launch.hpp", "mx4/mx4_mfma.h", "moe/moe.h", "moe/moe_launch.hpp"]
 PUBLIC_HEADERS = ["fp8q.h", "fp8q_mx4.h", "fp8q_moe.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -10,6 +10,7 @@
 #include "mx4/mx4.h"
 
 #include "fp8q_device.h"
+#include "mx4/mx4_mfma.h"
 
 #include <type_traits>
 #include <utility>
@@ -18,9 +19,7 @@ namespace fp8q {
 namespace mx4 {
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
 
 // Lambdas of the kernels: one that is not inlined would put the register
 // arrays that it captures into memory.
@@ -361,29 +360,6 @@ __device__ __forceinline__ void unroll(std::integer_sequence<int, Is...>, F&& f)
     (f(std::integral_constant<int, Is>{}), ...);
 }
 
-// acc += (B tile) * (A tile)^T with the accumulator in place in AGPRs. The
-// 256 accumulator registers of a 128 x 128 wave tile are all the AGPRs there
-// are: left to itself, the register allocator gives results other registers
-// than their inputs and copies them back and forth inside the K loop (752
-// copies per 512 MFMAs). The tied operand rules that out. The compiler does
-// not see a matrix instruction here, so it is up to the code that reads
-// accumulators to wait first (mfma_settle).
-template <int T>
-__device__ __forceinline__ void mfma_in_place(v4f& acc, v4i b, v4i a, uint32_t sb, uint32_t sa) {
-#define FP8Q_MFMA(lo, hi)                                                                                         \
-    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" lo "," lo ",0] op_sel_hi:[" hi "," hi \
-                 ",0] cbsz:4 blgp:4"                                                                              \
-                 : "+a"(acc)                                                                                      \
-                 : "v"(b), "v"(a), "v"(sb), "v"(sa))
-    if constexpr (T == 0) FP8Q_MFMA("0", "0");
-    else if constexpr (T == 1) FP8Q_MFMA("1", "0");
-    else if constexpr (T == 2) FP8Q_MFMA("0", "1");
-    else FP8Q_MFMA("1", "1");
-#undef FP8Q_MFMA
-}
-// More wait states than the last MFMA's results take.
-__device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
-
 // LDS of the tiled kernels: four stages of one K tile (A tiles, then B
 // tiles), each an array of its own, so that the compiler can tell a stage being
 // filled from the one being read, and one of scale words (64 per row tile,
@@ -582,7 +558,7 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const Rows& t, i
         // the last copies land before the LDS is used again, here or by
         // another workgroup
         __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-        mfma_settle();
+        mfma_settle(acc);
         __builtin_amdgcn_s_barrier();
     }
 
