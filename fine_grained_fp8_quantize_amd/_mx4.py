@@ -289,6 +289,9 @@ def fp4_grouped_gemm_mx(group_offsets: torch.Tensor, group_rows: torch.Tensor | 
     m_total, n = rta * 16, _rows_of(n, rtb, "n")
     oc = _out_code(out_dtype)
     out = _output(out, (m_total, n), out_dtype, dev, stream)
+    if groups == 0:  # (the C call has nothing to do then)
+        with torch.cuda.stream(stream or torch.cuda.current_stream(dev)):
+            return out.zero_()
     st = _library().fp4_grouped_gemm_mx(
         groups, group_offsets.data_ptr(), _address(group_rows), m_total, n, kt * 128, a.data_ptr(), ld_a,
         a_scale.data_ptr(), ld_as, b.data_ptr(), ld_b, b.stride(0), b_scale.data_ptr(), ld_bs, b_scale.stride(0),
