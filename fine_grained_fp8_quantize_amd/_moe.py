@@ -65,6 +65,14 @@ def _array(t, shape, dtype, device, stream, name: str) -> torch.Tensor:
     return t
 
 
+def _layout_args(experts: int, align: int, first: int) -> None:
+    """The C call takes these as 32 bits, and ctypes would drop the others."""
+    if not 1 <= experts <= MOE_MAX_EXPERTS:
+        raise Fp8qError("experts must be 1..%d, got %d" % (MOE_MAX_EXPERTS, experts))
+    if not 1 <= align <= 0x7FFFFFFF or not 0 <= first <= 0x7FFFFFFF - experts:
+        raise Fp8qError("align = %d or first = %d is out of range" % (align, first))
+
+
 def moe_dispatch(ids: torch.Tensor, experts: int, align: int = 128, first: int = 0,
                  group_offsets: torch.Tensor | None = None, group_rows: torch.Tensor | None = None,
                  dst_rows: torch.Tensor | None = None, stream=None, workspace: torch.Tensor | None = None):
@@ -81,6 +89,7 @@ def moe_dispatch(ids: torch.Tensor, experts: int, align: int = 128, first: int =
     """
     dev = _on_gpu(ids, group_offsets, group_rows, dst_rows, workspace)
     _ids(ids)
+    _layout_args(experts, align, first)
     tokens, topk = ids.shape
     group_offsets = _array(group_offsets, (experts + 1,), torch.int32, dev, stream, "group_offsets")
     group_rows = _array(group_rows, (experts,), torch.int32, dev, stream, "group_rows")
