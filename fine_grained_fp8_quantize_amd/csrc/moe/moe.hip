@@ -508,11 +508,13 @@ __global__ __launch_bounds__(kThreads) void balance_finish_kernel(BalanceArgs p,
     }
     __syncthreads();
     if (!last || wave != 0) return;
-    float v = 0.0f;
+    // a lane adds up to 8192 terms (32768 sequences, 1024 experts) one after the
+    // other, of any sizes: in FP32 small ones behind a large one would be lost
+    double v = 0.0;
     for (unsigned i = lane; i < gridDim.x; i += 64)
-        v += __hip_atomic_load(&b.losses[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    v = wave_sum(v);
-    if (lane == 0) *p.loss = v;
+        v += (double)__hip_atomic_load(&b.losses[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const float loss = wave_sum((float)v);
+    if (lane == 0) *p.loss = loss;
 }
 
 // Four rows per wave, scores computed again rather than read (they would be as
