@@ -103,7 +103,9 @@ inline GemmForm grouped_form(int64_t m_total, int64_t n, int64_t groups, bool sc
     const int64_t avg = m_total / groups, columns = ceil_div(n, 256);
     // Tiles of 256 columns once the experts alone give three tiles for four CUs
     // (27 experts with 2 rows, 2048 x 4096, 216 tiles: 27 us, 28 without LDS);
-    // otherwise narrow pieces with K split over the waves.
+    // otherwise narrow pieces with K split over the waves. Fewer rows than
+    // experts (avg = 0) belong to one expert in 16 at the most, segments being
+    // whole row tiles, and take the narrow pieces.
     if (scales16 && groups * ceil_div(avg, 256) * columns >= 192) return {GemmKernel::kGroupedTiles, 8, 8};
     // Row tiles of 16, 32 or 64 rows, or 256 x 256 tiles again when there are
     // rows for them (8 experts, 2048 x 4096, us for each of the four: 16 rows an
