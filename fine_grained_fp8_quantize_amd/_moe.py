@@ -7,7 +7,7 @@ import ctypes
 import torch
 
 from . import Fp8qError, _check, _check_tensor, _load
-from ._mx4 import _address, _new, _on_gpu, _raw_stream
+from ._mx4 import _address, _call, _new, _on_gpu
 
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
@@ -95,9 +95,9 @@ def moe_dispatch(ids: torch.Tensor, experts: int, align: int = 128, first: int =
     group_rows = _array(group_rows, (experts,), torch.int32, dev, stream, "group_rows")
     dst_rows = _array(dst_rows, (tokens, topk), torch.int32, dev, stream, "dst_rows")
     workspace = _workspace(workspace, MOE_DISPATCH_WORKSPACE_BYTES, dev, stream)
-    st = _library().moe_dispatch(ids.data_ptr(), tokens, topk, first, experts, align, group_offsets.data_ptr(),
-                                 group_rows.data_ptr(), dst_rows.data_ptr(), workspace.data_ptr(),
-                                 workspace.numel(), _raw_stream(stream, dev))
+    st = _call(_library().moe_dispatch, dev, stream, ids.data_ptr(), tokens, topk, first, experts, align,
+               group_offsets.data_ptr(), group_rows.data_ptr(), dst_rows.data_ptr(), workspace.data_ptr(),
+               workspace.numel())
     _check(st, "moe_dispatch")
     return group_offsets, group_rows, dst_rows
 
@@ -149,8 +149,8 @@ def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, seq_offsets: torch
     coef = _array(coef, (seqs, experts), torch.float32, dev, stream, "coef")
     lib = _library()
     workspace = _workspace(workspace, lib.moe_balance_workspace_bytes(tokens, experts, seqs), dev, stream)
-    st = lib.moe_balance_loss(*args, float(alpha), loss.data_ptr(), counts.data_ptr(), coef.data_ptr(),
-                              workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    st = _call(lib.moe_balance_loss, dev, stream, *args, float(alpha), loss.data_ptr(), counts.data_ptr(),
+               coef.data_ptr(), workspace.data_ptr(), workspace.numel())
     _check(st, "moe_balance_loss")
     return loss, counts, coef
 
@@ -172,7 +172,7 @@ def moe_balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, coef: tor
         out = _new((tokens, experts), logits.dtype, dev, stream)
     else:
         _check_tensor(out, (tokens, experts), (logits.dtype,), "out")
-    st = _library().moe_balance_loss_backward(*args, coef.data_ptr(), _address(grad), out.data_ptr(),
-                                              experts if tokens <= 1 else out.stride(0), _raw_stream(stream, dev))
+    st = _call(_library().moe_balance_loss_backward, dev, stream, *args, coef.data_ptr(), _address(grad),
+               out.data_ptr(), experts if tokens <= 1 else out.stride(0))
     _check(st, "moe_balance_loss_backward")
     return out

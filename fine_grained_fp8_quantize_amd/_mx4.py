@@ -71,6 +71,16 @@ def _raw_stream(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _call(fn, dev: int, stream, *args) -> int:
+    """Status of the C call ``fn`` for tensors of GPU ``dev``. The call launches on
+    the current device when the stream is the default one, whose handle is the
+    same on every GPU."""
+    if dev == torch._C._cuda_getDevice():
+        return fn(*args, _raw_stream(stream, dev))
+    with torch.cuda.device(dev):
+        return fn(*args, _raw_stream(stream, dev))
+
+
 def _new(shape, dtype, dev: int, stream) -> torch.Tensor:
     """A new tensor, its memory taken on ``stream`` (see ``_empty``)."""
     if stream is None:
@@ -177,10 +187,9 @@ def fp4_quantize_mx(x: torch.Tensor, tiling: str = "1x32", q: torch.Tensor | Non
     q, scale, ld_q, ld_s = _codes_out(q, scale, q_shape, s_shape, dev, stream, lead)
     groups = x.shape[0] if lead else 1
     ld_x = cols if rows <= 1 else x.stride(-2)
-    st = _library().fp4_quantize_mx(
-        groups, x.data_ptr(), rows, cols, ld_x, x.stride(0) if lead else 0, t, q.data_ptr(), ld_q,
-        q.stride(0) if lead else 0, scale.data_ptr(), ld_s, scale.stride(0) if lead else 0,
-        _raw_stream(stream, dev))
+    st = _call(_library().fp4_quantize_mx, dev, stream, groups, x.data_ptr(), rows, cols, ld_x,
+               x.stride(0) if lead else 0, t, q.data_ptr(), ld_q, q.stride(0) if lead else 0, scale.data_ptr(), ld_s,
+               scale.stride(0) if lead else 0)
     _check(st, "fp4_quantize_mx")
     return q, scale
 
@@ -207,9 +216,8 @@ def fp4_quantize_mx_scatter(x: torch.Tensor, dst_rows: torch.Tensor, m_total: in
         raise Fp8qError("dst_rows must be contiguous [tokens][topk]")
     q, scale, ld_q, ld_s = _codes_out(q, scale, *_shapes(m_total, cols), dev, stream)
     ld_x = cols if tokens <= 1 else x.stride(0)
-    st = _library().fp4_quantize_mx_scatter(x.data_ptr(), tokens, cols, ld_x, dst_rows.shape[1], dst_rows.data_ptr(),
-                                            m_total, q.data_ptr(), ld_q, scale.data_ptr(), ld_s,
-                                            _raw_stream(stream, dev))
+    st = _call(_library().fp4_quantize_mx_scatter, dev, stream, x.data_ptr(), tokens, cols, ld_x, dst_rows.shape[1],
+               dst_rows.data_ptr(), m_total, q.data_ptr(), ld_q, scale.data_ptr(), ld_s)
     _check(st, "fp4_quantize_mx_scatter")
     return q, scale
 
@@ -224,8 +232,8 @@ def fp4_dequantize_mx(q: torch.Tensor, scale: torch.Tensor, rows: int, cols: int
         raise Fp8qError("q has %d x %d tiles, which is not a matrix of %d rows with K = %d" % (kt, rt, rows, cols))
     oc = _out_code(out_dtype)
     out = _output(out, (rows, cols), out_dtype, dev, stream)
-    st = _library().fp4_dequantize_mx(q.data_ptr(), ld_q, scale.data_ptr(), ld_s, rows, cols, out.data_ptr(),
-                                      cols if rows <= 1 else out.stride(0), oc, _raw_stream(stream, dev))
+    st = _call(_library().fp4_dequantize_mx, dev, stream, q.data_ptr(), ld_q, scale.data_ptr(), ld_s, rows, cols,
+               out.data_ptr(), cols if rows <= 1 else out.stride(0), oc)
     _check(st, "fp4_dequantize_mx")
     return out
 
@@ -254,9 +262,8 @@ def fp4_gemm_mx(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale
     m, n = _rows_of(m, rta, "m"), _rows_of(n, rtb, "n")
     oc = _out_code(out_dtype)
     out = _output(out, (m, n), out_dtype, dev, stream)
-    st = _library().fp4_gemm_mx(m, n, kt * 128, a.data_ptr(), ld_a, a_scale.data_ptr(), ld_as, b.data_ptr(), ld_b,
-                                b_scale.data_ptr(), ld_bs, out.data_ptr(), n if m <= 1 else out.stride(0), oc,
-                                _raw_stream(stream, dev))
+    st = _call(_library().fp4_gemm_mx, dev, stream, m, n, kt * 128, a.data_ptr(), ld_a, a_scale.data_ptr(), ld_as,
+               b.data_ptr(), ld_b, b_scale.data_ptr(), ld_bs, out.data_ptr(), n if m <= 1 else out.stride(0), oc)
     _check(st, "fp4_gemm_mx")
     return out
 
@@ -292,9 +299,8 @@ def fp4_grouped_gemm_mx(group_offsets: torch.Tensor, group_rows: torch.Tensor | 
     if groups == 0:  # (the C call has nothing to do then)
         with torch.cuda.stream(stream or torch.cuda.current_stream(dev)):
             return out.zero_()
-    st = _library().fp4_grouped_gemm_mx(
-        groups, group_offsets.data_ptr(), _address(group_rows), m_total, n, kt * 128, a.data_ptr(), ld_a,
-        a_scale.data_ptr(), ld_as, b.data_ptr(), ld_b, b.stride(0), b_scale.data_ptr(), ld_bs, b_scale.stride(0),
-        out.data_ptr(), n if m_total <= 1 else out.stride(0), oc, _raw_stream(stream, dev))
+    st = _call(_library().fp4_grouped_gemm_mx, dev, stream, groups, group_offsets.data_ptr(), _address(group_rows),
+               m_total, n, kt * 128, a.data_ptr(), ld_a, a_scale.data_ptr(), ld_as, b.data_ptr(), ld_b, b.stride(0),
+               b_scale.data_ptr(), ld_bs, b_scale.stride(0), out.data_ptr(), n if m_total <= 1 else out.stride(0), oc)
     _check(st, "fp4_grouped_gemm_mx")
     return out
