@@ -139,7 +139,9 @@ def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, seq_offsets: torch
     ``"sigmoid"`` (normalised over the experts). ``seq_offsets``: int32
     ``[S + 1]`` cuts the tokens into sequences, whose losses are averaged; None:
     one. Returns ``(loss[1], counts[S][experts], coef[S][experts])``; pass
-    ``coef`` to :func:`moe_balance_loss_backward`.
+    ``coef`` to :func:`moe_balance_loss_backward`. As everywhere in this package
+    there is no autograd: the loss has no graph, also where ``logits`` requires a
+    gradient, and adding it to a model's loss trains nothing by itself.
     """
     dev = _on_gpu(logits, ids, seq_offsets, loss, counts, coef, workspace)
     args = _balance_args(logits, ids, seq_offsets, score)

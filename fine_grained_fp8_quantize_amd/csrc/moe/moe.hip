@@ -94,8 +94,11 @@ __global__ __launch_bounds__(kThreads) void dispatch_count_kernel(DispatchArgs p
 // earlier parts + of earlier waves + of earlier lanes and rounds of its own.
 // Lanes with the same expert find each other with one ballot per bit of the
 // expert's number. SINGLE: the part is the whole batch, and the counts are
-// its own. 131072 routes, 256 experts: 6.9 us, most of it the chain of LDS
-// updates from round to round of a wave; 256 routes, SINGLE: 3.3 us.
+// its own. 256 experts, 64 parts, a wave's rounds of 64 routes depending on one
+// another through `next`: 65536 routes (one round) 6.1 us, 131072 (two) 6.8,
+// 262144 8.4, 524288 12.3, 1048576 (16) 20.6. So a round is 0.7 to 1 us, and
+// what comes before, the reads of all parts' counts and the sums between five
+// barriers, 5 us with the launch. 256 routes, SINGLE: 3.0 us.
 template <bool SINGLE>
 __global__ __launch_bounds__(kThreads) void dispatch_place_kernel(DispatchArgs p, int64_t per_part, int parts) {
     __shared__ int next[kWaves][kMaxExperts];
@@ -445,8 +448,11 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(BalanceArgs p, B
 // Adds up one sequence's parts for 64 experts per workgroup (16 waves share
 // the parts), then writes its counts and coefficients; the last workgroup to
 // finish adds the losses, in their order. 260 parts of 256 experts in 4
-// sequences: 9.2 us, five dependent trips to memory (records, sums, the loss's
-// hand-over in two, the losses).
+// sequences: 8.8 us, five dependent trips to memory (records, sums, the loss's
+// hand-over in two, the losses). Every workgroup reads every part's record, so
+// the cost grows with sequences times parts (256 experts, both kernels through
+// the binding: 16384 tokens in 4, 100, 1000 sequences 18, 25, 142 us; 4096
+// sequences of 64 tokens 886 us; 32768 of one token 26.6 ms).
 __global__ __launch_bounds__(kThreads) void balance_finish_kernel(BalanceArgs p, BalancePlan b, int slices) {
     __shared__ float sums[kWaves][64];
     __shared__ int counts[kWaves][64];

@@ -226,9 +226,9 @@ __device__ __forceinline__ v4i load_weights(const uint8_t* p) {
 // group's tiles of all NT column tiles, whose loads (4 NT KB per wave) are in
 // flight together. The waves' FP32 partials are added in wave order through
 // LDS, so the result does not depend on timing.
-// Bound by the HBM stream of the weights: 1 x 4096 x 7168: 6.0 us, 2.6 TB/s (a
-// launch and two dependent waits are most of it); 1 x 16384 x 7168: 13.6 us, 4.6
-// TB/s.
+// Bound by the HBM stream of the weights: 1 x 4096 x 7168: 6.0 us, 2.6 TB/s (each
+// of the 14 waves has one K group: a launch, one wait for its loads and the join
+// through LDS are most of it); 1 x 16384 x 7168: 13.6 us, 4.6 TB/s.
 template <int MS, int NT, bool F32, bool GROUPED>
 __global__ __launch_bounds__(64 * max_waves(MS)) void gemm_rows_kernel(GemmArgs p, int tiles_n) {
     extern __shared__ v4f partial[];  // [waves][NT][MS][64]
@@ -399,9 +399,9 @@ __device__ __forceinline__ bool dense_slot(const GemmArgs& p, int slot, int& tm,
 // 1 KB contiguous per instruction, linear in LDS). One barrier per K tile: it
 // says that everybody's copies of tile j + 1 have landed and that everybody
 // has read tile j, whose stage the copies of tile j + 4 then overwrite.
-// 4096 x 4096 x 7168 with 256 x 256 tiles: 53 us, 4.6 PFLOP/s; the same MFMAs on
-// random operands with nothing else reach 6.4 to 7.3 (the clock falls with the
-// load). A K tile's step takes 0.76 us, its MFMAs alone 0.66, its copies alone
+// 4096 x 4096 x 7168 with 256 x 256 tiles: 53 to 56 us by card, 4.3 to 4.6
+// PFLOP/s; the same MFMAs on random operands with nothing else reach 6.4 to 7.3
+// (the clock falls with the load). A K tile's step takes 0.76 us, its MFMAs alone 0.66, its copies alone
 // 0.59. 256 x 256 because a step copies 32 KB for its 4096 cycles of MFMA: a tile
 // of half the size needs twice the bytes per product from the L2.
 // LDS: row tiles that a stage holds (a kernel with tiles of two sizes uses one
@@ -621,10 +621,10 @@ __global__ __launch_bounds__(256, TM * TN > 16 ? 1 : 2) void gemm_tiles_kernel(G
 
 // Tiles of 256 x 256, or half as high where no more than 128 rows are real
 // (an expert's last rows, or all of a small one's): that takes about 0.6 of
-// the time. 8192 rows over 32 experts of 4096 x 7168: 163 us, of which HBM
-// traffic (the weights once, A, C and its padding: 750 MB) takes 145 at the
-// rate of a large copy; 27 experts with 2 rows each, 2048 x 4096: 25.7 us, 5.2
-// TB/s.
+// the time. 8192 rows over 32 experts of 4096 x 7168, uneven: 163 to 181 us by
+// card, of which HBM traffic (the weights once, A, C and its padding: 752 MB)
+// takes 145 at the rate of a large copy; 64 routes over 32 experts of 2048 x 4096,
+// 27 to 30 of which have rows: 25.6 us, 5.2 TB/s (134 MB moved with 29).
 template <bool F32>
 __global__ __launch_bounds__(256, 1) void grouped_tiles_kernel(GemmArgs p) {
     constexpr int BM = 256, BN = 256;

@@ -151,7 +151,7 @@ __device__ __forceinline__ uint32_t quad_max_u16x2(uint32_t v) {
 // instruction reads 256 bytes of each of 4 tokens, and a block's amax is a quad
 // maximum. (64 channels, 128 bytes of 8 tokens: a tenth slower where rows do
 // not start on 128-byte lines, as each piece then touches two.) 4096 x 7168: 17.0
-// us, 4.4 TB/s; 8192 x 2040: 11.0 us, 3.9 TB/s.
+// us, 4.4 TB/s; 8192 x 2040: 11.2 us, 3.8 TB/s.
 // LDS words of a tile and of its upper eight rows: the 16 (tile, half) pairs
 // that one store instruction touches start 4 banks apart.
 constexpr int kColsTile = kTileBytes / 4 + 8;

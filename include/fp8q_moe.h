@@ -69,7 +69,7 @@ int moe_dispatch(const int32_t *ids, int64_t tokens, int32_t topk, int32_t first
  *   coef[s][e] = alpha f[s][e] / (T_s S')   = d loss / d s_te of its tokens
  * The counts carry no gradient. A row without a finite score (all logits
  * -inf) has scores of zero; -inf logits have scores of zero; a NaN in a
- * counted row makes the loss NaN (uncounted rows are not read).
+ * counted row makes the loss NaN (what uncounted rows hold does not matter).
  *
  * logits      [tokens][ld], bf16 or fp32 by logits_dtype, ld >= experts.
  * seq_offsets device int32 [seqs + 1]: non-decreasing, from 0 to tokens; NULL
