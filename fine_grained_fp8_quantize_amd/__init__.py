@@ -53,6 +53,9 @@ Layouts (row-major, K contiguous for GEMM operands):
   routes: what the scattering quantizers and the grouped GEMMs take.
 * ``moe_balance_loss(logits, ids)`` / ``moe_balance_loss_backward(...)`` -- the
   router's balance loss with per-expert counts, and its gradient.
+* ``adamw_plan(params, exp_avg, exp_avg_sq, ...)`` / ``adamw_step(plan, grads,
+  step, lr)`` -- AdamW over many tensors in one call, states in FP32 or in
+  E4M3 with a scale for each 128 elements.
 
 E4M3 tensors are returned as ``torch.float8_e4m3fn`` (OCP E4M3FN bytes);
 ``uint8`` tensors are accepted wherever codes are inputs.
@@ -89,6 +92,8 @@ __all__ = [
     "moe_dispatch",
     "moe_balance_loss",
     "moe_balance_loss_backward",
+    "adamw_plan",
+    "adamw_step",
     "fp8q_status_string",
     "fp8q_last_hip_error",
     "Fp8qError",
@@ -791,3 +796,4 @@ def fp8_gemm_tensor(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_s
 from ._mx4 import (  # noqa: E402
     fp4_dequantize_mx, fp4_gemm_mx, fp4_grouped_gemm_mx, fp4_quantize_mx, fp4_quantize_mx_scatter)
 from ._moe import moe_balance_loss, moe_balance_loss_backward, moe_dispatch  # noqa: E402
+from ._adamw import AdamwPlan, adamw_plan, adamw_step  # noqa: E402

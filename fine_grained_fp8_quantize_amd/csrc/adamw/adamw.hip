@@ -1,0 +1,355 @@
+// adamw.hip -- AdamW over many tensors for gfx950.
+//
+// The step is a stream: with FP32 parameters, bf16 gradients and a bf16 copy
+// it reads and writes 28 bytes an element with 32-bit states, 16.1 with 8-bit
+// ones, and HBM bounds it. A launch takes up to 56 tensors, whose table is a
+// kernel argument (it is captured with the launch, and nothing has to be copied
+// to the device first); a workgroup takes 4096 elements of one of them. A thread
+// has four consecutive elements of each of four pieces, so that every load and
+// store of a wave is contiguous, and all of its loads are in flight together.
+#include "adamw/adamw.h"
+
+#include <hip/hip_runtime.h>
+
+#include "fp8q_device.h"
+#include "launch_shape.hpp"
+
+// The arithmetic is that of the formula, one rounding per operation: results
+// do not depend on which multiplications the compiler could join with which
+// additions.
+#pragma clang fp contract(off)
+
+namespace fp8q {
+namespace adamw {
+namespace {
+
+// beta^t by squaring, the same on host and device.
+__host__ __device__ inline double int_pow(double x, int64_t t) {
+    double y = 1.0;
+    for (; t > 0; t >>= 1) {
+        if (t & 1) y *= x;
+        x *= x;
+    }
+    return y;
+}
+
+// What the step's options come to, rounded once.
+struct Factors {
+    float decay;      // 1 - lr * weight_decay
+    float step_size;  // lr / (1 - beta1^t)
+    float root;       // 1 / sqrt(1 - beta2^t)
+};
+__host__ __device__ inline Factors factors(double lr, double weight_decay, double beta1, double beta2, int64_t t) {
+    Factors f;
+    f.decay = (float)(1.0 - lr * weight_decay);
+    f.step_size = (float)(lr / (1.0 - int_pow(beta1, t)));
+    f.root = (float)(1.0 / sqrt(1.0 - int_pow(beta2, t)));
+    return f;
+}
+
+constexpr int kVec = 4;                                // consecutive elements of a thread
+constexpr int kPieces = kChunk / (kThreads * kVec);    // pieces of a workgroup's chunk
+constexpr int kBlock = 128;                            // elements that share a scale
+static_assert(kPieces * kThreads * kVec == kChunk && kBlock == 32 * kVec, "a block is half a wave");
+
+struct Table {
+    fp8q_adamw_tensor t[kMaxTensors];
+    int32_t first[kMaxTensors];   // first workgroup of each tensor
+    uint64_t vec;                 // bit i: the arrays of tensor i can be accessed four elements at a time
+    int32_t place;                // place of t[0] in the call
+    int32_t count;
+};
+
+struct Step {
+    double lr, beta1, beta2, weight_decay;
+    const float* lr_dev;
+    const int64_t* step_dev;
+    const float* grad_scale;
+    int64_t step;
+    Factors f;                    // where neither lr_dev nor step_dev is given
+    float b1, c1, b2, c2, eps;    // beta1, 1 - beta1, beta2, 1 - beta2
+    uint32_t seed_lo, seed_hi;
+};
+static_assert(sizeof(Table) + sizeof(Step) <= 4096, "kernel arguments");
+
+// A 32-bit mixing step (odd multipliers: the golden ratio and the root of two).
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+    x = (x ^ (x >> 16)) * 0x9E3779B9u;
+    x = (x ^ (x >> 15)) * 0x6A09E667u;
+    return x ^ (x >> 16);
+}
+
+// The magnitude code of y in [0, 448] (a NaN counts as 448), rounded up where
+// the 16 random bits pass what is cut off. Normal codes: the bits of y, of which
+// the last 20 are cut; below 2^-6: multiples of 2^-9, cut off in units of 2^-29.
+__device__ __forceinline__ uint32_t stochastic_e4m3(float y, uint32_t bits16) {
+    y = __builtin_fminf(y, kE4M3Max);
+    const bool normal = y >= 0x1p-6f;
+    const uint32_t fixed = normal ? __float_as_uint(y) : (uint32_t)(y * 0x1p29f);
+    const uint32_t code = ((fixed + (bits16 << 4)) >> 20) - (normal ? 120u << 3 : 0u);
+    return code < 126u ? code : 126u;  // (448 itself has no code above)
+}
+
+__device__ __forceinline__ float4 decode4(uint32_t codes) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, true);
+    return make_float4(lo[0], lo[1], hi[0], hi[1]);
+}
+
+// Four elements of a tensor, from `at` on, of which `left` exist.
+template <class T>
+struct Four {
+    T x[4];
+};
+template <class T, bool VEC>
+__device__ __forceinline__ Four<T> load4(const T* p, int64_t at, int left) {
+    Four<T> v;
+    if constexpr (VEC) {
+        typedef T vec_t __attribute__((ext_vector_type(4)));
+        const vec_t w = __builtin_nontemporal_load(reinterpret_cast<const vec_t*>(p + at));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.x[i] = w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.x[i] = i < left ? p[at + i] : T(0);
+    }
+    return v;
+}
+template <class T, bool VEC>
+__device__ __forceinline__ void store4(T* p, int64_t at, int left, const Four<T>& v) {
+    if constexpr (VEC) {
+        typedef T vec_t __attribute__((ext_vector_type(4)));
+        vec_t w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = v.x[i];
+        __builtin_nontemporal_store(w, reinterpret_cast<vec_t*>(p + at));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) p[at + i] = v.x[i];
+    }
+}
+
+template <bool F32>
+using Elem = typename std::conditional<F32, float, uint16_t>::type;
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+
+__device__ __forceinline__ Four<uint16_t> to_bf16(const float (&x)[4]) {
+    const uint32_t lo = pack_bf16x2(x[0], x[1]), hi = pack_bf16x2(x[2], x[3]);
+    return {{(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)}};
+}
+
+// Codes of a thread's four elements of a block (half a wave), and its scale.
+template <bool ROOT>
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], const uint32_t (&bits16)[4], float& scale) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = umax32(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    top = row16_max(top);
+    top = umax32(top, (uint32_t)__shfl_xor((int)top, 16));
+    scale = __uint_as_float(top) * (1.0f / kE4M3Max);
+    const float by = scale > 0.0f ? scale : 1.0f;
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t code = stochastic_e4m3(__builtin_fabsf(x[i]) / by, bits16[i]);
+        if (ROOT && code == 0 && x[i] > 0.0f) code = 1;
+        code |= (__float_as_uint(x[i]) >> 24) & 0x80u;
+        word |= code << (8 * i);
+    }
+    return word;
+}
+
+template <bool P32, bool G32, bool BITS8, bool VEC>
+__device__ __forceinline__ void chunk(const fp8q_adamw_tensor& t, int64_t base, const Step& s, const Factors& f,
+                                      float grad_scale, uint32_t key) {
+    using P = Elem<P32>;
+    using G = Elem<G32>;
+    P* const param = static_cast<P*>(t.param);
+    const G* const grad = static_cast<const G*>(t.grad);
+    const int tid = threadIdx.x;
+    // One piece at a time where elements are looked at one by one.
+    constexpr int U = VEC ? kPieces : 1;
+    for (int first = 0; first < kPieces; first += U) {
+        Four<P> p[U];
+        Four<G> g[U];
+        Four<float> m32[U], v32[U];
+        uint32_t m8[U], v8[U];
+        float ms[U], vs[U];
+        int64_t at[U];
+        int left[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            at[u] = base + ((first + u) * kThreads + tid) * kVec;
+            const int64_t rest = t.numel - at[u];
+            left[u] = rest < 0 ? 0 : (rest < kVec ? (int)rest : kVec);
+            p[u] = load4<P, VEC>(param, at[u], left[u]);
+            g[u] = load4<G, VEC>(grad, at[u], left[u]);
+            if constexpr (BITS8) {
+                const Four<uint8_t> a = load4<uint8_t, VEC>(static_cast<const uint8_t*>(t.exp_avg), at[u], left[u]);
+                const Four<uint8_t> b = load4<uint8_t, VEC>(static_cast<const uint8_t*>(t.exp_avg_sq), at[u], left[u]);
+                m8[u] = a.x[0] | a.x[1] << 8 | a.x[2] << 16 | (uint32_t)a.x[3] << 24;
+                v8[u] = b.x[0] | b.x[1] << 8 | b.x[2] << 16 | (uint32_t)b.x[3] << 24;
+                ms[u] = left[u] > 0 ? t.exp_avg_scale[at[u] / kBlock] : 0.0f;
+                vs[u] = left[u] > 0 ? t.exp_avg_sq_scale[at[u] / kBlock] : 0.0f;
+            } else {
+                m32[u] = load4<float, VEC>(static_cast<const float*>(t.exp_avg), at[u], left[u]);
+                v32[u] = load4<float, VEC>(static_cast<const float*>(t.exp_avg_sq), at[u], left[u]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if constexpr (BITS8) {
+                const float4 a = decode4(m8[u]), b = decode4(v8[u]);
+                const float am[4] = {a.x, a.y, a.z, a.w}, bm[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    m32[u].x[i] = am[i] * ms[u];
+                    const float r = bm[i] * vs[u];
+                    v32[u].x[i] = r * r;
+                }
+            }
+            float np[4], root[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float gi = as_float(g[u].x[i]) * grad_scale;
+                const float m = m32[u].x[i] * s.b1 + gi * s.c1;
+                const float v = v32[u].x[i] * s.b2 + (gi * gi) * s.c2;
+                root[i] = sqrtf(v);
+                np[i] = as_float(p[u].x[i]) * f.decay - (m / (root[i] * f.root + s.eps)) * f.step_size;
+                m32[u].x[i] = m;
+                v32[u].x[i] = v;
+            }
+            if constexpr (P32) {
+                Four<float> w;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w.x[i] = np[i];
+                store4<float, VEC>(param, at[u], left[u], w);
+                if (t.copy) store4<uint16_t, VEC>(t.copy, at[u], left[u], to_bf16(np));
+            } else {
+                store4<uint16_t, VEC>(param, at[u], left[u], to_bf16(np));
+            }
+            if constexpr (BITS8) {
+                uint32_t lo[4], hi[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t bits = mix((uint32_t)(at[u] + i) ^ key);
+                    lo[i] = bits & 0xFFFFu;
+                    hi[i] = bits >> 16;
+                    // elements past the tensor must not count in its last block
+                    if (!VEC && i >= left[u]) m32[u].x[i] = root[i] = 0.0f;
+                }
+                float sm, sv;
+                const uint32_t cm = encode4<false>(m32[u].x, lo, sm), cv = encode4<true>(root, hi, sv);
+                auto bytes = [](uint32_t w) {
+                    return Four<uint8_t>{{(uint8_t)w, (uint8_t)(w >> 8), (uint8_t)(w >> 16), (uint8_t)(w >> 24)}};
+                };
+                store4<uint8_t, VEC>(static_cast<uint8_t*>(t.exp_avg), at[u], left[u], bytes(cm));
+                store4<uint8_t, VEC>(static_cast<uint8_t*>(t.exp_avg_sq), at[u], left[u], bytes(cv));
+                if (left[u] > 0 && at[u] % kBlock == 0) {
+                    t.exp_avg_scale[at[u] / kBlock] = sm;
+                    t.exp_avg_sq_scale[at[u] / kBlock] = sv;
+                }
+            } else {
+                store4<float, VEC>(static_cast<float*>(t.exp_avg), at[u], left[u], m32[u]);
+                store4<float, VEC>(static_cast<float*>(t.exp_avg_sq), at[u], left[u], v32[u]);
+            }
+        }
+    }
+}
+
+template <bool P32, bool G32, bool BITS8>
+__global__ __launch_bounds__(kThreads) void step_kernel(Table table, Step s) {
+    const float grad_scale = s.grad_scale ? *s.grad_scale : 1.0f;
+    if (!(__builtin_fabsf(grad_scale) < __builtin_inff())) return;
+    const int lane = threadIdx.x & 63;
+    const int mine = lane < table.count ? table.first[lane] : 0x7FFFFFFF;
+    const int i = __builtin_amdgcn_readfirstlane(__popcll(__ballot(mine <= (int)blockIdx.x)) - 1);
+    const fp8q_adamw_tensor t = table.t[i];
+    const int64_t base = (int64_t)((int)blockIdx.x - table.first[i]) * kChunk;
+    Factors f = s.f;
+    uint32_t step32 = (uint32_t)s.step;
+    if (s.lr_dev || s.step_dev) {
+        int64_t step = s.step_dev ? *s.step_dev : s.step;
+        step = step < 1 ? 1 : step;
+        step32 = (uint32_t)step;
+        f = factors(s.lr_dev ? (double)*s.lr_dev : s.lr, s.weight_decay, s.beta1, s.beta2, step);
+    }
+    uint32_t key = 0;
+    if constexpr (BITS8) {
+        key = mix(mix(mix(s.seed_lo) + s.seed_hi) + step32);
+        key = mix(mix(key + (uint32_t)(table.place + i)) + (uint32_t)(base >> 32));
+    }
+    if (((table.vec >> i) & 1) && base + kChunk <= t.numel)
+        chunk<P32, G32, BITS8, true>(t, base, s, f, grad_scale, key);
+    else
+        chunk<P32, G32, BITS8, false>(t, base, s, f, grad_scale, key);
+}
+
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+hipError_t launch(const Table& table, const Step& s, const Options& o, int64_t blocks, hipStream_t stream) {
+    const dim3 grid((unsigned)blocks), block(kThreads);
+    const int which = (o.param_f32 ? 4 : 0) + (o.grad_f32 ? 2 : 0) + (o.bits8 ? 1 : 0);
+    switch (which) {
+        case 0: hipLaunchKernelGGL((step_kernel<false, false, false>), grid, block, 0, stream, table, s); break;
+        case 1: hipLaunchKernelGGL((step_kernel<false, false, true>), grid, block, 0, stream, table, s); break;
+        case 2: hipLaunchKernelGGL((step_kernel<false, true, false>), grid, block, 0, stream, table, s); break;
+        case 3: hipLaunchKernelGGL((step_kernel<false, true, true>), grid, block, 0, stream, table, s); break;
+        case 4: hipLaunchKernelGGL((step_kernel<true, false, false>), grid, block, 0, stream, table, s); break;
+        case 5: hipLaunchKernelGGL((step_kernel<true, false, true>), grid, block, 0, stream, table, s); break;
+        case 6: hipLaunchKernelGGL((step_kernel<true, true, false>), grid, block, 0, stream, table, s); break;
+        default: hipLaunchKernelGGL((step_kernel<true, true, true>), grid, block, 0, stream, table, s); break;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_step(int32_t count, const fp8q_adamw_tensor* tensors, const Options& o, hipStream_t stream) {
+    Step s = {};
+    s.lr = o.lr; s.beta1 = o.beta1; s.beta2 = o.beta2; s.weight_decay = o.weight_decay;
+    s.lr_dev = o.lr_dev; s.step_dev = o.step_dev; s.grad_scale = o.grad_scale; s.step = o.step;
+    if (!o.lr_dev && !o.step_dev) s.f = factors(o.lr, o.weight_decay, o.beta1, o.beta2, o.step);
+    s.b1 = (float)o.beta1; s.c1 = (float)(1.0 - o.beta1);
+    s.b2 = (float)o.beta2; s.c2 = (float)(1.0 - o.beta2);
+    s.eps = o.eps;
+    s.seed_lo = (uint32_t)o.seed; s.seed_hi = (uint32_t)(o.seed >> 32);
+    Table table;
+    table.count = 0;
+    table.vec = 0;
+    int64_t blocks = 0;
+    for (int32_t i = 0; i <= count; ++i) {
+        const bool end = i == count;
+        const int64_t need = end || !tensors[i].grad ? 0 : (tensors[i].numel + kChunk - 1) / kChunk;
+        // (a table holds consecutive tensors, so that a place is known from the first one's)
+        if (table.count > 0 &&
+            (end || table.count == kMaxTensors || !launchable({blocks + need, kThreads}))) {
+            for (int j = table.count; j < kMaxTensors; ++j) table.first[j] = 0x7FFFFFFF;
+            if (blocks > 0) {
+                const hipError_t e = launch(table, s, o, blocks, stream);
+                if (e != hipSuccess) return e;
+            }
+            table.count = 0;
+            table.vec = 0;
+            blocks = 0;
+        }
+        if (end) break;
+        const fp8q_adamw_tensor& t = tensors[i];
+        if (!launchable({need, kThreads})) return hipErrorInvalidValue;
+        if (table.count == 0) table.place = i;
+        const int j = table.count++;
+        table.t[j] = t;
+        table.first[j] = (int32_t)blocks;
+        const int states = o.bits8 ? 4 : 16;
+        const bool vec = aligned(t.param, o.param_f32 ? 16 : 8) && aligned(t.grad, o.grad_f32 ? 16 : 8) &&
+                         aligned(t.exp_avg, states) && aligned(t.exp_avg_sq, states) && aligned(t.copy, 8);
+        if (vec) table.vec |= 1ULL << j;
+        blocks += need;
+    }
+    return hipSuccess;
+}
+
+}  // namespace adamw
+}  // namespace fp8q
