@@ -53,6 +53,11 @@ Layouts (row-major, K contiguous for GEMM operands):
   routes: what the scattering quantizers and the grouped GEMMs take.
 * ``moe_balance_loss(logits, ids)`` / ``moe_balance_loss_backward(...)`` -- the
   router's balance loss with per-expert counts, and its gradient.
+* ``fp8_gated_gemm(a, a_scale, b, b_scale)`` / ``fp8_grouped_gated_gemm(...)``
+  -- both projections of a gated feed-forward block, the activation and the
+  product in one kernel, dense or for the experts; bf16, FP32 or E4M3 out.
+* ``fp8_gated_backward(dh, gate_up)`` -- the gradients of gate and up, in E4M3
+  for both products that follow, in one pass.
 * ``adamw_plan(params, exp_avg, exp_avg_sq, ...)`` / ``adamw_step(plan, grads,
   step, lr)`` -- AdamW over many tensors in one call, states in FP32 or in
   E4M3 with a scale for each 128 elements.
@@ -92,6 +97,9 @@ __all__ = [
     "moe_dispatch",
     "moe_balance_loss",
     "moe_balance_loss_backward",
+    "fp8_gated_gemm",
+    "fp8_grouped_gated_gemm",
+    "fp8_gated_backward",
     "adamw_plan",
     "adamw_step",
     "fp8q_status_string",
@@ -797,3 +805,4 @@ from ._mx4 import (  # noqa: E402
     fp4_dequantize_mx, fp4_gemm_mx, fp4_grouped_gemm_mx, fp4_quantize_mx, fp4_quantize_mx_scatter)
 from ._moe import moe_balance_loss, moe_balance_loss_backward, moe_dispatch  # noqa: E402
 from ._adamw import AdamwPlan, adamw_plan, adamw_step  # noqa: E402
+from ._gated import fp8_gated_backward, fp8_gated_gemm, fp8_grouped_gated_gemm  # noqa: E402

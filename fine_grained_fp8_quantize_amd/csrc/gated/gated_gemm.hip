@@ -1,0 +1,196 @@
+// gated_gemm.hip -- the gated feed-forward products for gfx950.
+//
+// H = act(A Wg^T) * (A Wu^T), both products as the block-scaled FP8 GEMM makes
+// them (gemm.hip). Many rows: its 256 x 256 tile whose B rows alternate by 16
+// between gate and up weights of 128 columns (gemm_kernel.h, GATED), so that a
+// lane ends with the two products of the same outputs in its registers and H
+// is all that has to be written. The 128 columns are one 1x128 tile of H, which
+// can be stored as E4M3 without another pass. Few rows: the kernel below.
+#include "gated/gated.h"
+
+#include "gemm_kernel.h"
+
+namespace fp8q {
+namespace gated {
+namespace {
+
+// Few rows of A: the weights are streamed from HBM straight to registers. A
+// workgroup owns 16 MS rows by 8 columns: the 16 rows of its MFMA's B operand
+// are the weights of 8 gate and 8 up columns. Wave w takes the slabs w, w +
+// waves, ..., U of them in flight, and promotes each one's products with its
+// scales; the waves' FP32 partials are added in wave order through LDS, so the
+// result does not depend on timing.
+template <int MS, int U, bool F32>
+__global__ __launch_bounds__(1024) void gated_rows_kernel(Params p) {
+    extern __shared__ v4f partial[];  // [waves][MS][64]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int i = lane & 15, g = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * kRowsColumns;
+    const int slabs = (int)(p.k / kSlab);
+    // rows and columns past the last ones repeat it: loaded, not stored
+    const uint8_t* const wrow = p.b + (i >= 8 ? p.stride_up : 0) + min(n0 + (i & 7), p.n - 1) * p.ldb + 16 * g;
+    // (an MFMA result's four rows are 4 g..4 g + 3: gate for g < 2)
+    const float* const sb = p.b_scale + (g >= 2 ? p.stride_ups : 0) + n0 / 128 * p.ld_bs;
+    const uint8_t* arow[MS];
+    const float* sa[MS];
+    v4f acc[MS];
+#pragma unroll
+    for (int s = 0; s < MS; ++s) {
+        const int64_t row = min((int64_t)(16 * s + i), p.m - 1);
+        arow[s] = p.a + row * p.lda + 16 * g;
+        sa[s] = p.a_scale + row;
+        acc[s] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+    for (int j0 = wave; j0 < slabs; j0 += U * waves) {
+        v4i w[U][2], a[U][MS][2];
+        float f[U][MS];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t j = min(j0 + u * waves, slabs - 1);  // past the last slab: skipped below
+            w[u][0] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(wrow + j * kSlab));
+            w[u][1] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(wrow + j * kSlab + 64));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t j = min(j0 + u * waves, slabs - 1);
+            const float b = sb[j];
+#pragma unroll
+            for (int s = 0; s < MS; ++s) {
+                a[u][s][0] = *reinterpret_cast<const v4i*>(arow[s] + j * kSlab);
+                a[u][s][1] = *reinterpret_cast<const v4i*>(arow[s] + j * kSlab + 64);
+                f[u][s] = sa[s][j * p.ld_as] * b;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (j0 + u * waves < slabs) {
+                const v8i bw = __builtin_shufflevector(w[u][0], w[u][1], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                for (int s = 0; s < MS; ++s) {
+                    const v8i aw = __builtin_shufflevector(a[u][s][0], a[u][s][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                    const v4f zero = {0.f, 0.f, 0.f, 0.f};
+                    const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bw, aw, zero, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[s][r] = __builtin_fmaf(part[r], f[u][s], acc[s][r]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < MS; ++s) partial[(wave * MS + s) * 64 + lane] = acc[s];
+    __syncthreads();
+    for (int x = threadIdx.x; x < MS * 32; x += blockDim.x) {
+        const int l = x & 31, s = x >> 5;
+        const int64_t m = 16 * s + (l & 15), n = n0 + 4 * (l >> 4);
+        if (m >= p.m) continue;
+        v4f gate = partial[s * 64 + l], up = partial[s * 64 + 32 + l];
+        for (int w = 1; w < waves; ++w) {
+            gate += partial[(w * MS + s) * 64 + l];
+            up += partial[(w * MS + s) * 64 + 32 + l];
+        }
+        if (p.gate_up != nullptr) {
+            uint16_t* const dst = p.gate_up + m * p.ldg + n;
+            store4_bf16(dst, gate, n, p.n, p.g_vec);
+            store4_bf16(dst + p.n, up, n, p.n, p.u_vec);
+        }
+        v4f h;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = gate_act(p.act, gate[r]) * up[r];
+        if constexpr (F32)
+            store4_f32(static_cast<float*>(p.c) + m * p.ldc + n, h, n, p.n, p.h_vec);
+        else
+            store4_bf16(static_cast<uint16_t*>(p.c) + m * p.ldc + n, h, n, p.n, p.h_vec);
+    }
+}
+
+// FP32 rows [m][n] to E4M3 codes and scales of 1x128 tiles: 16 lanes per tile.
+__global__ __launch_bounds__(256) void quantize_rows_kernel(const float* __restrict__ x, int64_t m, int64_t n,
+                                                            uint8_t* __restrict__ q, int64_t ld_q,
+                                                            float* __restrict__ scale, int64_t ld_s) {
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x, per = n / 8;
+    if (t >= m * per) return;  // whole tiles of 16 lanes
+    const int64_t row = t / per, c = (t - row * per) * 8;
+    const v4f lo = *reinterpret_cast<const v4f*>(x + row * n + c), hi = *reinterpret_cast<const v4f*>(x + row * n + c + 4);
+    uint32_t top = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        top = umax32(top, umax32(__float_as_uint(lo[r]) & 0x7FFFFFFFu, __float_as_uint(hi[r]) & 0x7FFFFFFFu));
+    const GroupScale gs = group_scale_f32(__uint_as_float(row16_max(top)));
+    *reinterpret_cast<uint2*>(q + row * ld_q + c) = make_uint2(e4m3x4(lo, gs), e4m3x4(hi, gs));
+    if (c % 128 == 0) scale[c / 128 * ld_s + row] = gs.s;
+}
+
+Params gated_params(const GatedArgs& g) {
+    Params p = to_params(g.g);
+    p.stride_up = g.stride_up; p.stride_ups = g.stride_ups;
+    p.act = g.act;
+    p.out_scale = g.out_scale; p.ld_os = g.ld_os;
+    p.gate_up = g.gate_up; p.ldg = g.ldg;
+    auto vec = [](const void* x, int64_t ld, uintptr_t bytes) {
+        return ld % 4 == 0 && reinterpret_cast<uintptr_t>(x) % bytes == 0;
+    };
+    p.h_vec = vec(p.c, p.ldc, g.g.out_f32 ? 16 : 8);
+    p.g_vec = vec(p.gate_up, p.ldg, 8);
+    p.u_vec = p.g_vec && p.n % 4 == 0;
+    return p;
+}
+
+template <int MS, int U>
+void launch_rows(const Params& p, RowsForm f, bool f32, hipStream_t stream) {
+    const LaunchShape s = rows_shape(f, p.n);
+    const dim3 grid((unsigned)s.blocks), block(s.threads);
+    const size_t lds = (size_t)s.threads * MS * sizeof(v4f);
+    if (f32)
+        hipLaunchKernelGGL((gated_rows_kernel<MS, U, true>), grid, block, lds, stream, p);
+    else
+        hipLaunchKernelGGL((gated_rows_kernel<MS, U, false>), grid, block, lds, stream, p);
+}
+
+}  // namespace
+
+hipError_t launch_gated(const GatedArgs& g, float* workspace, hipStream_t stream) {
+    Params p = gated_params(g);
+    const RowsForm f = rows_form(g.g.m, g.g.k);
+    if (f.ms != 0 && (!g.e4m3 || workspace)) {
+        if (g.e4m3) {
+            p.c = workspace;
+            p.ldc = p.n;
+            p.h_vec = true;
+        }
+        const bool f32 = g.e4m3 || g.g.out_f32;
+        if (f.ms == 1) launch_rows<1, 4>(p, f, f32, stream);
+        else if (f.ms == 2) launch_rows<2, 2>(p, f, f32, stream);
+        else launch_rows<4, 2>(p, f, f32, stream);
+        if (g.e4m3) {
+            const int64_t blocks = parts_of(p.m * p.n / 8, 256);
+            hipLaunchKernelGGL(quantize_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, workspace, p.m, p.n,
+                               static_cast<uint8_t*>(g.g.c), g.g.ldc, p.out_scale, p.ld_os);
+        }
+        return hipGetLastError();
+    }
+    const LaunchShape s = tiles_shape(p.m, p.n);
+    const dim3 grid((unsigned)s.blocks), block(s.threads);
+    if (g.e4m3)
+        hipLaunchKernelGGL((gemm_kernel<256, false, false, kDense, false, false, kGatedE4M3>), grid, block, 0, stream, p);
+    else if (g.g.out_f32)
+        hipLaunchKernelGGL((gemm_kernel<256, false, true, kDense, false, false, kGated>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((gemm_kernel<256, false, false, kDense, false, false, kGated>), grid, block, 0, stream, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_grouped_gated(const GatedArgs& g, hipStream_t stream) {
+    const Params p = gated_params(g);
+    const LaunchShape s = grouped_shape(p.m, p.n);
+    const dim3 grid((unsigned)s.blocks), block(s.threads);
+    if (g.e4m3)
+        hipLaunchKernelGGL((gemm_kernel<256, false, false, kGroupedM, false, false, kGatedE4M3>), grid, block, 0, stream, p);
+    else if (g.g.out_f32)
+        hipLaunchKernelGGL((gemm_kernel<256, false, true, kGroupedM, false, false, kGated>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((gemm_kernel<256, false, false, kGroupedM, false, false, kGated>), grid, block, 0, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace gated
+}  // namespace fp8q

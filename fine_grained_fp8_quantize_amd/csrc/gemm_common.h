@@ -70,6 +70,17 @@ struct Params {
     TailRecord* split_records;
     float* split_ws;
     int32_t split_pieces;
+    // gated products: B is the gate's weights, the up ones lie stride_up bytes
+    // (scales: stride_ups floats) behind them, n counts the columns of one of
+    // them; c is H, and with E4M3 output out_scale [n/128][ld_os] its scales
+    int64_t stride_up;
+    int64_t stride_ups;
+    int act;
+    float* out_scale;
+    int64_t ld_os;
+    uint16_t* gate_up;  // bf16 [m][ldg], gate and up side by side; NULL: not kept
+    int64_t ldg;
+    bool h_vec, g_vec, u_vec;  // four adjacent outputs of H, gate, up may be stored together
 };
 
 // Which rows of the output a block tile owns.
@@ -374,6 +385,13 @@ Params to_params(const GemmProblem& g) {
     p.split_records = nullptr;
     p.split_ws = nullptr;
     p.split_pieces = 0;
+    p.stride_up = p.stride_ups = 0;
+    p.act = 0;
+    p.out_scale = nullptr;
+    p.ld_os = 0;
+    p.gate_up = nullptr;
+    p.ldg = 0;
+    p.h_vec = p.g_vec = p.u_vec = false;
     return p;
 }
 
