@@ -58,6 +58,9 @@ Layouts (row-major, K contiguous for GEMM operands):
   product in one kernel, dense or for the experts; bf16, FP32 or E4M3 out.
 * ``fp8_gated_backward(dh, gate_up)`` -- the gradients of gate and up, in E4M3
   for both products that follow, in one pass.
+* ``fp4_gemv_mx(x, w, w_scale)`` / ``fp4_gated_gemv_mx(...)`` -- few bf16 rows
+  times FP4 weights (weight-only), plain or as the first half of a gated block,
+  of one matrix or of the experts that ``ids`` name.
 * ``adamw_plan(params, exp_avg, exp_avg_sq, ...)`` / ``adamw_step(plan, grads,
   step, lr)`` -- AdamW over many tensors in one call, states in FP32 or in
   E4M3 with a scale for each 128 elements.
@@ -100,6 +103,8 @@ __all__ = [
     "fp8_gated_gemm",
     "fp8_grouped_gated_gemm",
     "fp8_gated_backward",
+    "fp4_gemv_mx",
+    "fp4_gated_gemv_mx",
     "adamw_plan",
     "adamw_step",
     "fp8q_status_string",
@@ -806,3 +811,4 @@ from ._mx4 import (  # noqa: E402
 from ._moe import moe_balance_loss, moe_balance_loss_backward, moe_dispatch  # noqa: E402
 from ._adamw import AdamwPlan, adamw_plan, adamw_step  # noqa: E402
 from ._gated import fp8_gated_backward, fp8_gated_gemm, fp8_grouped_gated_gemm  # noqa: E402
+from ._gemv import fp4_gated_gemv_mx, fp4_gemv_mx  # noqa: E402

@@ -549,6 +549,7 @@ int fp8q_last_hip_error(void);
 #include "fp8q_mx4.h" /* FP4 microscaling quantization and products */
 #include "fp8q_moe.h" /* MoE routing: row layout, balance loss */
 #include "fp8q_gated.h" /* gated feed-forward block: products, activation, gradient */
+#include "fp8q_gemv.h" /* few bf16 rows times FP4 weights */
 #include "fp8q_adamw.h" /* AdamW over many tensors, states in 32 or 8 bits */
 
 #endif /* FP8Q_H */
