@@ -48,10 +48,13 @@ int adamw_step(int32_t count, const fp8q_adamw_tensor* tensors, int param_dtype,
     if (!tensors) return FP8Q_ERR_NULL;
     if (!is_aligned(lr_dev, 4) || !is_aligned(step_dev, 8) || !is_aligned(grad_scale, 4)) return FP8Q_ERR_ALIGN;
     const bool param_f32 = param_dtype == FP8Q_ADAMW_F32, grad_f32 = grad_dtype == FP8Q_ADAMW_F32;
+    bool work = false;
     for (int32_t i = 0; i < count; ++i) {
         const int st = check_tensor(tensors[i], param_f32, grad_f32, state_bits == 8);
         if (st != FP8Q_OK) return st;
+        work |= tensors[i].grad && tensors[i].numel > 0;
     }
+    if (!work) return FP8Q_OK;
     Options o = {};
     o.lr = lr; o.beta1 = beta1; o.beta2 = beta2; o.weight_decay = weight_decay;
     o.eps = (float)eps; o.step = step;
