@@ -19,7 +19,7 @@ _lib = None
 
 
 class _Tensor(ctypes.Structure):
-    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+    _fields_ = [("param", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
                 ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
                 ("exp_avg_sq_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("numel", ctypes.c_int64)]
 
@@ -30,7 +30,7 @@ def _library():
     if _lib is None:
         L = _load()
         p, i64, i32, cint, f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_double
-        L.adamw_step.argtypes = [i32, p, cint, cint, cint, f64, f64, f64, f64, f64, i64, p, p, p, ctypes.c_uint64, p]
+        L.adamw_step.argtypes = [i32, p, p, cint, cint, cint, f64, f64, f64, f64, f64, i64, p, p, p, ctypes.c_uint64, p]
         L.adamw_step.restype = cint
         _lib = L
     return _lib
@@ -38,13 +38,15 @@ def _library():
 
 class AdamwPlan:
     """The tensors of an optimizer, checked once by :func:`adamw_plan`. It keeps
-    the tensors alive; their storage must stay where it is."""
+    the tensors alive; their storage must stay where it is. One thread at a time
+    steps a plan."""
 
-    __slots__ = ("device", "shapes", "param_dtype", "state_bits", "_entries", "_tensors")
+    __slots__ = ("device", "shapes", "param_dtype", "state_bits", "_entries", "_tensors", "_grads")
 
     def __init__(self, device, shapes, param_dtype, state_bits, entries, tensors):
         self.device, self.shapes, self.param_dtype, self.state_bits = device, shapes, param_dtype, state_bits
         self._entries, self._tensors = entries, tensors
+        self._grads = (ctypes.c_void_p * len(shapes))()
 
     def __len__(self):
         return len(self.shapes)
@@ -114,11 +116,41 @@ def adamw_plan(params, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale
             if dtype is not torch.float32:
                 raise Fp8qError("copies belong to float32 params")
             _array(copies[i], shape, (torch.bfloat16,), "copies", i)
-        entries[i] = _Tensor(p.data_ptr(), 0, avg[i].data_ptr(), sq[i].data_ptr(), _address(avg_s[i]),
+        entries[i] = _Tensor(p.data_ptr(), avg[i].data_ptr(), sq[i].data_ptr(), _address(avg_s[i]),
                              _address(sq_s[i]), _address(copies[i]), p.numel())
     if _overlaps(every):
         raise Fp8qError("two of the plan's tensors share memory")
     return AdamwPlan(device, [p.shape for p in params], dtype, bits, entries, every)
+
+
+_dtype_of, _shape_of = torch.Tensor.dtype.__get__, torch.Tensor.shape.__get__
+_is_contiguous, _device_of, _address_of = torch.Tensor.is_contiguous, torch.Tensor.get_device, torch.Tensor.data_ptr
+
+
+def _gradients(plan: AdamwPlan, grads):
+    """Checks the gradients, puts their addresses into the plan's array and returns their dtype (None: there is none)."""
+    shapes, there = plan.shapes, grads
+    if type(None) in set(map(type, grads)):
+        there = [g for g in grads if g is not None]
+        shapes = [s for s, g in zip(shapes, grads) if g is not None]
+    if not there:
+        return None
+    dtype, device = there[0].dtype, plan.device
+    if dtype not in _DTYPES:
+        raise Fp8qError("grads must be float32 or bfloat16, got %s" % dtype)
+    # (whole lists at a time: a step of many small tensors takes the GPU less than a look at each of them takes here)
+    if (list(map(_shape_of, there)) != shapes or set(map(_dtype_of, there)) != {dtype}
+            or not all(map(_is_contiguous, there)) or set(map(_device_of, there)) != {device}):
+        for i, g in enumerate(grads):
+            if g is not None:
+                _array(g, plan.shapes[i], (dtype,), "grads", i)
+                if g.get_device() != device:
+                    raise Fp8qError("grads[%d] must live on cuda:%d" % (i, device))
+    if there is grads:
+        plan._grads[:] = list(map(_address_of, grads))
+    else:
+        plan._grads[:] = [None if g is None else g.data_ptr() for g in grads]
+    return dtype
 
 
 def _one(t: torch.Tensor, dtype, name: str) -> int:
@@ -148,22 +180,13 @@ def adamw_step(plan: AdamwPlan, grads, step, lr, beta1: float = 0.9, beta2: floa
     changed behind its back.
     """
     grads = _same_list(grads, len(plan), "grads")
-    entries, dtype, device = plan._entries, None, plan.device
-    for i, g in enumerate(grads):
-        if g is None:
-            entries[i].grad = 0
-            continue
-        if dtype is None:
-            dtype = g.dtype
-            if dtype not in _DTYPES:
-                raise Fp8qError("grads must be float32 or bfloat16, got %s" % dtype)
-        if g.dtype is not dtype or g.shape != plan.shapes[i] or not g.is_contiguous() or g.get_device() != device:
-            _array(g, plan.shapes[i], (dtype,), "grads", i)
-            raise Fp8qError("grads[%d] must live on cuda:%d" % (i, device))
-        entries[i].grad = g.data_ptr()
+    dtype = _gradients(plan, grads)
     if dtype is None:
         return
-    _on_gpu(plan._tensors[0], grad_scale, step if torch.is_tensor(step) else None, lr if torch.is_tensor(lr) else None)
+    device = plan.device
+    on_gpu = [t for t in (grad_scale, step, lr) if torch.is_tensor(t)]
+    if on_gpu and _on_gpu(*on_gpu) != device:
+        raise Fp8qError("step, lr and grad_scale must live on cuda:%d" % device)
     lr_dev = step_dev = 0
     if torch.is_tensor(lr):
         lr, lr_dev = 0.0, _one(lr, torch.float32, "lr")
@@ -174,6 +197,6 @@ def adamw_step(plan: AdamwPlan, grads, step, lr, beta1: float = 0.9, beta2: floa
     if not 0 <= seed < 1 << 64:
         raise Fp8qError("seed must be within 64 bits, got %d" % seed)
     scale = 0 if grad_scale is None else _one(grad_scale, torch.float32, "grad_scale")
-    st = _call(_library().adamw_step, device, stream, len(grads), entries, _DTYPES[plan.param_dtype], _DTYPES[dtype],
+    st = _call(_library().adamw_step, device, stream, len(grads), plan._entries, plan._grads, _DTYPES[plan.param_dtype], _DTYPES[dtype],
                plan.state_bits, lr, beta1, beta2, eps, weight_decay, int(step), lr_dev, step_dev, scale, seed)
     _check(st, "adamw_step")

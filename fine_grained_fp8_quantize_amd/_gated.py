@@ -53,6 +53,9 @@ def _out_code(dtype, allowed) -> int:
     return _OUTS[dtype]
 
 
+_GRADS = (torch.float8_e4m3fn, torch.bfloat16)
+
+
 def _ld(t: torch.Tensor) -> int:
     """Leading dimension of a row-major matrix (a lone row has none)."""
     return t.shape[1] if t.shape[0] <= 1 else t.stride(0)
@@ -74,7 +77,19 @@ def _f32(t: torch.Tensor, shape, what: str) -> None:
 
 
 def _operands(a, a_scale, b, b_scale, lead: int):
-    """Checked A and W of the gated products; m, n, k and the weights' strides."""
+    """Checked A and W of the gated products; m, n, k, the leading dimensions of A and its scales, and the weights'
+    strides."""
+    if a.dim() == 2:
+        m, k = a.shape
+        bs, ss = b.shape, b_scale.shape
+        n = bs[-2] if len(bs) > 2 else -1
+        f32 = torch.float32
+        if (a.dtype in _CODES and b.dtype in _CODES and a_scale.dtype is f32 and b_scale.dtype is f32
+                and bs[lead:] == (2, n, k) and len(bs) == 3 + lead and k % 128 == 0 and a.is_contiguous()
+                and b.is_contiguous() and a_scale.is_contiguous() and b_scale.is_contiguous()
+                and a_scale.shape == (k // 128, m) and ss[lead:] == (2, -(-n // 128), k // 128)
+                and ss[:lead] == bs[:lead]):
+            return m, n, k, k, m, (k, n * k), (k // 128, ss[-2] * ss[-1])  # the usual case, in few steps
     _rowmajor(_codes(a, "a"), "a")
     _codes(b, "b")
     what = "[E][2][n][k]" if lead else "[2][n][k]"
@@ -92,25 +107,43 @@ def _operands(a, a_scale, b, b_scale, lead: int):
     _f32(b_scale, (*b.shape[:-2], -(-n // 128), k // 128), "b_scale")
     ldb = k if n <= 1 else b.stride(-2)
     ld_bs = k // 128 if b_scale.shape[-2] <= 1 else b_scale.stride(-2)
-    return m, n, k, (ldb, b.stride(lead)), (ld_bs, b_scale.stride(lead))
+    return m, n, k, _ld(a), _ld(a_scale), (ldb, b.stride(lead)), (ld_bs, b_scale.stride(lead))
 
 
 def _outputs(m, n, out_dtype, out, scale, gate_up, dev, stream):
-    """H, its scales (E4M3) and gate_up: new when absent (gate_up: not kept), checked otherwise."""
-    code = _out_code(out_dtype, tuple(_OUTS))
+    """H, its scales (E4M3) and gate_up: new when absent (gate_up: not kept), checked otherwise. With the arguments of
+    the C call."""
+    code = _out_code(out_dtype, _OUTS)
+    ld_o = n
     if code == OUT_E4M3:
         if n % 128:
             raise Fp8qError("E4M3 output needs n in whole 1x128 tiles, got %d" % n)
-        out = _matrix_out(out, (m, n), _CODES, dev, stream, "out")
-        scale = _matrix_out(scale, (n // 128, m), (torch.float32,), dev, stream, "scale")
+        if out is None:
+            out = _new((m, n), torch.float8_e4m3fn, dev, stream)
+        else:
+            _check_tensor(out, (m, n), _CODES, "out")
+            ld_o = _ld(out)
+        if scale is None:
+            scale, ld_s = _new((n // 128, m), torch.float32, dev, stream), m
+        else:
+            _f32(scale, (n // 128, m), "scale")
+            ld_s = _ld(scale)
     else:
         if scale is not None:
             raise Fp8qError("scale belongs to E4M3 output")
-        out = _matrix_out(out, (m, n), (out_dtype,), dev, stream, "out")
+        ld_s = 0
+        if out is None:
+            out = _new((m, n), out_dtype, dev, stream)
+        else:
+            _check_tensor(out, (m, n), (out_dtype,), "out")
+            ld_o = _ld(out)
+    ld_g = 0
     if gate_up is not None:
-        _check_tensor(gate_up, (m, 2 * n), (torch.bfloat16,), "gate_up")
-    tail = (out.data_ptr(), _ld(out), code, _address(scale), 0 if scale is None else _ld(scale), _address(gate_up),
-            0 if gate_up is None else _ld(gate_up))
+        ld_g = 2 * n
+        if gate_up.dtype is not torch.bfloat16 or gate_up.shape != (m, ld_g) or not gate_up.is_contiguous():
+            _check_tensor(gate_up, (m, ld_g), (torch.bfloat16,), "gate_up")
+            ld_g = _ld(gate_up)
+    tail = (out.data_ptr(), ld_o, code, _address(scale), ld_s, _address(gate_up), ld_g)
     return out, scale, tail
 
 
@@ -133,7 +166,7 @@ def fp8_gated_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sc
     scratch for E4M3 output of few rows (taken from torch when left out).
     """
     dev = _on_gpu(a, a_scale, b, b_scale, out, scale, gate_up, workspace)
-    m, n, k, (ldb, stride_b), (ld_bs, stride_bs) = _operands(a, a_scale, b, b_scale, 0)
+    m, n, k, lda, ld_as, (ldb, stride_b), (ld_bs, stride_bs) = _operands(a, a_scale, b, b_scale, 0)
     code = _act_code(act)
     out, scale, tail = _outputs(m, n, out_dtype, out, scale, gate_up, dev, stream)
     lib = _library()
@@ -142,7 +175,7 @@ def fp8_gated_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sc
     if workspace is None and scale is not None:
         need = lib.fp8_gated_workspace_bytes(m, n, k)
         workspace = _new(need, torch.uint8, dev, stream) if need else None
-    st = _call(lib.fp8_gated_gemm, dev, stream, m, n, k, a.data_ptr(), _ld(a), a_scale.data_ptr(), _ld(a_scale),
+    st = _call(lib.fp8_gated_gemm, dev, stream, m, n, k, a.data_ptr(), lda, a_scale.data_ptr(), ld_as,
                b.data_ptr(), ldb, stride_b, b_scale.data_ptr(), ld_bs, stride_bs, code, *tail, _address(workspace),
                0 if workspace is None else workspace.numel())
     _check(st, "fp8_gated_gemm")
@@ -162,7 +195,7 @@ def fp8_grouped_gated_gemm(group_offsets: torch.Tensor, group_rows: torch.Tensor
     ``b_scale[E][2][n/128][k/128]``. Padding rows of all outputs are zeros.
     """
     dev = _on_gpu(a, a_scale, b, b_scale, group_offsets, group_rows, out, scale, gate_up)
-    m, n, k, (ldb, stride_b), (ld_bs, stride_bs) = _operands(a, a_scale, b, b_scale, 1)
+    m, n, k, lda, ld_as, (ldb, stride_b), (ld_bs, stride_bs) = _operands(a, a_scale, b, b_scale, 1)
     groups = b.shape[0]
     for t, entries, name in ((group_offsets, groups + 1, "group_offsets"), (group_rows, groups, "group_rows")):
         if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.numel() != entries or not t.is_contiguous()):
@@ -172,7 +205,7 @@ def fp8_grouped_gated_gemm(group_offsets: torch.Tensor, group_rows: torch.Tensor
         raise Fp8qError("%d rows belong to no expert" % m)
     out, scale, tail = _outputs(m, n, out_dtype, out, scale, gate_up, dev, stream)
     st = _call(_library().fp8_grouped_gated_gemm, dev, stream, groups, group_offsets.data_ptr(), _address(group_rows),
-               m, n, k, a.data_ptr(), _ld(a), a_scale.data_ptr(), _ld(a_scale), b.data_ptr(), ldb, stride_b,
+               m, n, k, a.data_ptr(), lda, a_scale.data_ptr(), ld_as, b.data_ptr(), ldb, stride_b,
                b.stride(0), b_scale.data_ptr(), ld_bs, stride_bs, b_scale.stride(0), code, *tail)
     _check(st, "fp8_grouped_gated_gemm")
     return out if scale is None else (out, scale)
@@ -192,32 +225,39 @@ def fp8_gated_backward(dh: torch.Tensor, gate_up: torch.Tensor, act: str = "silu
     ``torch.bfloat16``: returns D in bf16, any n.
     """
     dev = _on_gpu(dh, gate_up, out, scale, out_t, scale_t)
-    _rowmajor(dh, "dh")
-    if dh.dtype != torch.bfloat16:
+    code = _out_code(out_dtype, _GRADS)
+    if dh.dtype is not torch.bfloat16:
         raise Fp8qError("dh must be bfloat16")
+    if dh.dim() != 2:
+        raise Fp8qError("dh must be [m][n]")
     m, n = dh.shape
-    _check_tensor(gate_up, (m, 2 * n), (torch.bfloat16,), "gate_up")
-    code = _out_code(out_dtype, (torch.float8_e4m3fn, torch.bfloat16))
+    if gate_up.dtype is torch.bfloat16 and gate_up.shape == (m, 2 * n) and dh.is_contiguous() and gate_up.is_contiguous():
+        ld_dh, ld_g = n, 2 * n
+    else:
+        _check_tensor(dh, (m, n), (torch.bfloat16,), "dh")
+        _check_tensor(gate_up, (m, 2 * n), (torch.bfloat16,), "gate_up")
+        ld_dh, ld_g = _ld(dh), _ld(gate_up)
+    given = out is not None or scale is not None or out_t is not None or scale_t is not None
     if code == OUT_BF16:
-        if transposed or any(t is not None for t in (scale, out_t, scale_t)):
+        if transposed or scale is not None or out_t is not None or scale_t is not None:
             raise Fp8qError("scales and transposed codes belong to E4M3 output")
         out = _matrix_out(out, (m, 2 * n), (torch.bfloat16,), dev, stream, "out")
     else:
         if n % 128:
             raise Fp8qError("E4M3 output needs n in whole 1x128 tiles, got %d" % n)
+        if transposed and m % 128:
+            raise Fp8qError("transposed codes need m in whole 128x1 tiles, got %d" % m)
+        if not transposed and (out_t is not None or scale_t is not None):
+            raise Fp8qError("out_t and scale_t belong to transposed=True")
         out = _matrix_out(out, (m, 2 * n), _CODES, dev, stream, "out")
         scale = _matrix_out(scale, (n // 64, m), (torch.float32,), dev, stream, "scale")
         if transposed:
-            if m % 128:
-                raise Fp8qError("transposed codes need m in whole 128x1 tiles, got %d" % m)
             out_t = _matrix_out(out_t, (2 * n, m), _CODES, dev, stream, "out_t")
             scale_t = _matrix_out(scale_t, (m // 128, 2 * n), (torch.float32,), dev, stream, "scale_t")
-        elif out_t is not None or scale_t is not None:
-            raise Fp8qError("out_t and scale_t belong to transposed=True")
-    lds = [0 if t is None else _ld(t) for t in (scale, out_t, scale_t)]
-    st = _call(_library().fp8_gated_backward, dev, stream, m, n, dh.data_ptr(), _ld(dh), gate_up.data_ptr(),
-               _ld(gate_up), _act_code(act), code, out.data_ptr(), _ld(out), _address(scale), lds[0], _address(out_t),
-               lds[1], _address(scale_t), lds[2])
+    lds = [0 if t is None else _ld(t) for t in (out, scale, out_t, scale_t)] if given else (2 * n, m, m, 2 * n)
+    st = _call(_library().fp8_gated_backward, dev, stream, m, n, dh.data_ptr(), ld_dh, gate_up.data_ptr(), ld_g,
+               _act_code(act), code, out.data_ptr(), lds[0], _address(scale), lds[1], _address(out_t), lds[2],
+               _address(scale_t), lds[3])
     _check(st, "fp8_gated_backward")
     if code == OUT_BF16:
         return out

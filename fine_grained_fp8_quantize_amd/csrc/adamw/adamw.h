@@ -25,7 +25,8 @@ struct Options {
     bool param_f32, grad_f32, bits8;
 };
 
-hipError_t launch_step(int32_t count, const fp8q_adamw_tensor* tensors, const Options& o, hipStream_t stream);
+hipError_t launch_step(int32_t count, const fp8q_adamw_tensor* tensors, const void* const* grads, const Options& o,
+                       hipStream_t stream);
 
 }  // namespace adamw
 }  // namespace fp8q

@@ -52,8 +52,13 @@ constexpr int kPieces = kChunk / (kThreads * kVec);    // pieces of a workgroup'
 constexpr int kBlock = 128;                            // elements that share a scale
 static_assert(kPieces * kThreads * kVec == kChunk && kBlock == 32 * kVec, "a block is half a wave");
 
+struct Entry {
+    fp8q_adamw_tensor t;
+    const void* grad;
+};
+
 struct Table {
-    fp8q_adamw_tensor t[kMaxTensors];
+    Entry t[kMaxTensors];
     int32_t first[kMaxTensors];   // first workgroup of each tensor
     uint64_t vec;                 // bit i: the arrays of tensor i can be accessed four elements at a time
     int32_t place;                // place of t[0] in the call
@@ -96,28 +101,34 @@ __device__ __forceinline__ float4 decode4(uint32_t codes) {
     return make_float4(lo[0], lo[1], hi[0], hi[1]);
 }
 
+// How a chunk is accessed: four elements at a time where all four exist, with
+// no look at the end in chunks that lie before it; or one at a time, at any
+// address.
+enum class Access { kWhole, kTail, kSingle };
+
 // Four elements of a tensor, from `at` on, of which `left` exist.
 template <class T>
 struct Four {
     T x[4];
 };
-template <class T, bool VEC>
+template <class T, Access A>
 __device__ __forceinline__ Four<T> load4(const T* p, int64_t at, int left) {
-    Four<T> v;
-    if constexpr (VEC) {
+    Four<T> v = {};
+    if (A == Access::kWhole || (A == Access::kTail && left == 4)) {
         typedef T vec_t __attribute__((ext_vector_type(4)));
         const vec_t w = __builtin_nontemporal_load(reinterpret_cast<const vec_t*>(p + at));
 #pragma unroll
         for (int i = 0; i < 4; ++i) v.x[i] = w[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v.x[i] = i < left ? p[at + i] : T(0);
+        for (int i = 0; i < 4; ++i)
+            if (i < left) v.x[i] = p[at + i];
     }
     return v;
 }
-template <class T, bool VEC>
+template <class T, Access A>
 __device__ __forceinline__ void store4(T* p, int64_t at, int left, const Four<T>& v) {
-    if constexpr (VEC) {
+    if (A == Access::kWhole || (A == Access::kTail && left == 4)) {
         typedef T vec_t __attribute__((ext_vector_type(4)));
         vec_t w;
 #pragma unroll
@@ -161,112 +172,110 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], const uint32_t 
     return word;
 }
 
-template <bool P32, bool G32, bool BITS8, bool VEC>
-__device__ __forceinline__ void chunk(const fp8q_adamw_tensor& t, int64_t base, const Step& s, const Factors& f,
+template <bool P32, bool G32, bool BITS8, Access A>
+__device__ __forceinline__ void chunk(const Entry& e, int64_t base, const Step& s, const Factors& f,
                                       float grad_scale, uint32_t key) {
     using P = Elem<P32>;
     using G = Elem<G32>;
+    const fp8q_adamw_tensor& t = e.t;
     P* const param = static_cast<P*>(t.param);
-    const G* const grad = static_cast<const G*>(t.grad);
+    const G* const grad = static_cast<const G*>(e.grad);
     const int tid = threadIdx.x;
-    // One piece at a time where elements are looked at one by one.
-    constexpr int U = VEC ? kPieces : 1;
-    for (int first = 0; first < kPieces; first += U) {
-        Four<P> p[U];
-        Four<G> g[U];
-        Four<float> m32[U], v32[U];
-        uint32_t m8[U], v8[U];
-        float ms[U], vs[U];
-        int64_t at[U];
-        int left[U];
+    constexpr int U = kPieces;
+    Four<P> p[U];
+    Four<G> g[U];
+    Four<float> m32[U], v32[U];
+    uint32_t m8[U], v8[U];
+    float ms[U], vs[U];
+    int64_t at[U];
+    int left[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            at[u] = base + ((first + u) * kThreads + tid) * kVec;
-            const int64_t rest = t.numel - at[u];
-            left[u] = rest < 0 ? 0 : (rest < kVec ? (int)rest : kVec);
-            p[u] = load4<P, VEC>(param, at[u], left[u]);
-            g[u] = load4<G, VEC>(grad, at[u], left[u]);
-            if constexpr (BITS8) {
-                const Four<uint8_t> a = load4<uint8_t, VEC>(static_cast<const uint8_t*>(t.exp_avg), at[u], left[u]);
-                const Four<uint8_t> b = load4<uint8_t, VEC>(static_cast<const uint8_t*>(t.exp_avg_sq), at[u], left[u]);
-                m8[u] = a.x[0] | a.x[1] << 8 | a.x[2] << 16 | (uint32_t)a.x[3] << 24;
-                v8[u] = b.x[0] | b.x[1] << 8 | b.x[2] << 16 | (uint32_t)b.x[3] << 24;
-                ms[u] = left[u] > 0 ? t.exp_avg_scale[at[u] / kBlock] : 0.0f;
-                vs[u] = left[u] > 0 ? t.exp_avg_sq_scale[at[u] / kBlock] : 0.0f;
-            } else {
-                m32[u] = load4<float, VEC>(static_cast<const float*>(t.exp_avg), at[u], left[u]);
-                v32[u] = load4<float, VEC>(static_cast<const float*>(t.exp_avg_sq), at[u], left[u]);
-            }
+    for (int u = 0; u < U; ++u) {
+        at[u] = base + (u * kThreads + tid) * kVec;
+        const int64_t rest = t.numel - at[u];
+        left[u] = rest < 0 ? 0 : (rest < kVec ? (int)rest : kVec);
+        p[u] = load4<P, A>(param, at[u], left[u]);
+        g[u] = load4<G, A>(grad, at[u], left[u]);
+        if constexpr (BITS8) {
+            const Four<uint8_t> a = load4<uint8_t, A>(static_cast<const uint8_t*>(t.exp_avg), at[u], left[u]);
+            const Four<uint8_t> b = load4<uint8_t, A>(static_cast<const uint8_t*>(t.exp_avg_sq), at[u], left[u]);
+            m8[u] = a.x[0] | a.x[1] << 8 | a.x[2] << 16 | (uint32_t)a.x[3] << 24;
+            v8[u] = b.x[0] | b.x[1] << 8 | b.x[2] << 16 | (uint32_t)b.x[3] << 24;
+            ms[u] = left[u] > 0 ? t.exp_avg_scale[at[u] / kBlock] : 0.0f;
+            vs[u] = left[u] > 0 ? t.exp_avg_sq_scale[at[u] / kBlock] : 0.0f;
+        } else {
+            m32[u] = load4<float, A>(static_cast<const float*>(t.exp_avg), at[u], left[u]);
+            v32[u] = load4<float, A>(static_cast<const float*>(t.exp_avg_sq), at[u], left[u]);
         }
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if constexpr (BITS8) {
-                const float4 a = decode4(m8[u]), b = decode4(v8[u]);
-                const float am[4] = {a.x, a.y, a.z, a.w}, bm[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    m32[u].x[i] = am[i] * ms[u];
-                    const float r = bm[i] * vs[u];
-                    v32[u].x[i] = r * r;
-                }
-            }
-            float np[4], root[4];
+    for (int u = 0; u < U; ++u) {
+        if constexpr (BITS8) {
+            const float4 a = decode4(m8[u]), b = decode4(v8[u]);
+            const float am[4] = {a.x, a.y, a.z, a.w}, bm[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float gi = as_float(g[u].x[i]) * grad_scale;
-                const float m = m32[u].x[i] * s.b1 + gi * s.c1;
-                const float v = v32[u].x[i] * s.b2 + (gi * gi) * s.c2;
-                root[i] = sqrtf(v);
-                np[i] = as_float(p[u].x[i]) * f.decay - (m / (root[i] * f.root + s.eps)) * f.step_size;
-                m32[u].x[i] = m;
-                v32[u].x[i] = v;
+                m32[u].x[i] = am[i] * ms[u];
+                const float r = bm[i] * vs[u];
+                v32[u].x[i] = r * r;
             }
-            if constexpr (P32) {
-                Four<float> w;
+        }
+        float np[4], root[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w.x[i] = np[i];
-                store4<float, VEC>(param, at[u], left[u], w);
-                if (t.copy) store4<uint16_t, VEC>(t.copy, at[u], left[u], to_bf16(np));
-            } else {
-                store4<uint16_t, VEC>(param, at[u], left[u], to_bf16(np));
-            }
-            if constexpr (BITS8) {
-                uint32_t lo[4], hi[4];
+        for (int i = 0; i < 4; ++i) {
+            const float gi = as_float(g[u].x[i]) * grad_scale;
+            const float m = m32[u].x[i] * s.b1 + gi * s.c1;
+            const float v = v32[u].x[i] * s.b2 + (gi * gi) * s.c2;
+            root[i] = sqrtf(v);
+            np[i] = as_float(p[u].x[i]) * f.decay - (m / (root[i] * f.root + s.eps)) * f.step_size;
+            m32[u].x[i] = m;
+            v32[u].x[i] = v;
+        }
+        if constexpr (P32) {
+            Four<float> w;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t bits = mix((uint32_t)(at[u] + i) ^ key);
-                    lo[i] = bits & 0xFFFFu;
-                    hi[i] = bits >> 16;
-                    // elements past the tensor must not count in its last block
-                    if (!VEC && i >= left[u]) m32[u].x[i] = root[i] = 0.0f;
-                }
-                float sm, sv;
-                const uint32_t cm = encode4<false>(m32[u].x, lo, sm), cv = encode4<true>(root, hi, sv);
-                auto bytes = [](uint32_t w) {
-                    return Four<uint8_t>{{(uint8_t)w, (uint8_t)(w >> 8), (uint8_t)(w >> 16), (uint8_t)(w >> 24)}};
-                };
-                store4<uint8_t, VEC>(static_cast<uint8_t*>(t.exp_avg), at[u], left[u], bytes(cm));
-                store4<uint8_t, VEC>(static_cast<uint8_t*>(t.exp_avg_sq), at[u], left[u], bytes(cv));
-                if (left[u] > 0 && at[u] % kBlock == 0) {
-                    t.exp_avg_scale[at[u] / kBlock] = sm;
-                    t.exp_avg_sq_scale[at[u] / kBlock] = sv;
-                }
-            } else {
-                store4<float, VEC>(static_cast<float*>(t.exp_avg), at[u], left[u], m32[u]);
-                store4<float, VEC>(static_cast<float*>(t.exp_avg_sq), at[u], left[u], v32[u]);
+            for (int i = 0; i < 4; ++i) w.x[i] = np[i];
+            store4<float, A>(param, at[u], left[u], w);
+            if (t.copy) store4<uint16_t, A>(t.copy, at[u], left[u], to_bf16(np));
+        } else {
+            store4<uint16_t, A>(param, at[u], left[u], to_bf16(np));
+        }
+        if constexpr (BITS8) {
+            uint32_t lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t bits = mix((uint32_t)(at[u] + i) ^ key);
+                lo[i] = bits & 0xFFFFu;
+                hi[i] = bits >> 16;
+                // elements past the tensor must not count in its last block
+                if (A != Access::kWhole && i >= left[u]) m32[u].x[i] = root[i] = 0.0f;
             }
+            float sm, sv;
+            const uint32_t cm = encode4<false>(m32[u].x, lo, sm), cv = encode4<true>(root, hi, sv);
+            auto bytes = [](uint32_t w) {
+                return Four<uint8_t>{{(uint8_t)w, (uint8_t)(w >> 8), (uint8_t)(w >> 16), (uint8_t)(w >> 24)}};
+            };
+            store4<uint8_t, A>(static_cast<uint8_t*>(t.exp_avg), at[u], left[u], bytes(cm));
+            store4<uint8_t, A>(static_cast<uint8_t*>(t.exp_avg_sq), at[u], left[u], bytes(cv));
+            if (left[u] > 0 && at[u] % kBlock == 0) {
+                t.exp_avg_scale[at[u] / kBlock] = sm;
+                t.exp_avg_sq_scale[at[u] / kBlock] = sv;
+            }
+        } else {
+            store4<float, A>(static_cast<float*>(t.exp_avg), at[u], left[u], m32[u]);
+            store4<float, A>(static_cast<float*>(t.exp_avg_sq), at[u], left[u], v32[u]);
         }
     }
 }
 
 template <bool P32, bool G32, bool BITS8>
-__global__ __launch_bounds__(kThreads) void step_kernel(Table table, Step s) {
+__global__ __launch_bounds__(kThreads, 4) void step_kernel(Table table, Step s) {
     const float grad_scale = s.grad_scale ? *s.grad_scale : 1.0f;
     if (!(__builtin_fabsf(grad_scale) < __builtin_inff())) return;
     const int lane = threadIdx.x & 63;
     const int mine = lane < table.count ? table.first[lane] : 0x7FFFFFFF;
     const int i = __builtin_amdgcn_readfirstlane(__popcll(__ballot(mine <= (int)blockIdx.x)) - 1);
-    const fp8q_adamw_tensor t = table.t[i];
+    const Entry t = table.t[i];
     const int64_t base = (int64_t)((int)blockIdx.x - table.first[i]) * kChunk;
     Factors f = s.f;
     uint32_t step32 = (uint32_t)s.step;
@@ -281,10 +290,12 @@ __global__ __launch_bounds__(kThreads) void step_kernel(Table table, Step s) {
         key = mix(mix(mix(s.seed_lo) + s.seed_hi) + step32);
         key = mix(mix(key + (uint32_t)(table.place + i)) + (uint32_t)(base >> 32));
     }
-    if (((table.vec >> i) & 1) && base + kChunk <= t.numel)
-        chunk<P32, G32, BITS8, true>(t, base, s, f, grad_scale, key);
+    if (((table.vec >> i) & 1) && base + kChunk <= t.t.numel)
+        chunk<P32, G32, BITS8, Access::kWhole>(t, base, s, f, grad_scale, key);
+    else if ((table.vec >> i) & 1)
+        chunk<P32, G32, BITS8, Access::kTail>(t, base, s, f, grad_scale, key);
     else
-        chunk<P32, G32, BITS8, false>(t, base, s, f, grad_scale, key);
+        chunk<P32, G32, BITS8, Access::kSingle>(t, base, s, f, grad_scale, key);
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -307,7 +318,8 @@ hipError_t launch(const Table& table, const Step& s, const Options& o, int64_t b
 
 }  // namespace
 
-hipError_t launch_step(int32_t count, const fp8q_adamw_tensor* tensors, const Options& o, hipStream_t stream) {
+hipError_t launch_step(int32_t count, const fp8q_adamw_tensor* tensors, const void* const* grads, const Options& o,
+                       hipStream_t stream) {
     Step s = {};
     s.lr = o.lr; s.beta1 = o.beta1; s.beta2 = o.beta2; s.weight_decay = o.weight_decay;
     s.lr_dev = o.lr_dev; s.step_dev = o.step_dev; s.grad_scale = o.grad_scale; s.step = o.step;
@@ -322,7 +334,7 @@ hipError_t launch_step(int32_t count, const fp8q_adamw_tensor* tensors, const Op
     int64_t blocks = 0;
     for (int32_t i = 0; i <= count; ++i) {
         const bool end = i == count;
-        const int64_t need = end || !tensors[i].grad ? 0 : (tensors[i].numel + kChunk - 1) / kChunk;
+        const int64_t need = end || !grads[i] ? 0 : (tensors[i].numel + kChunk - 1) / kChunk;
         // (a table holds consecutive tensors, so that a place is known from the first one's)
         if (table.count > 0 &&
             (end || table.count == kMaxTensors || !launchable({blocks + need, kThreads}))) {
@@ -340,10 +352,10 @@ hipError_t launch_step(int32_t count, const fp8q_adamw_tensor* tensors, const Op
         if (!launchable({need, kThreads})) return hipErrorInvalidValue;
         if (table.count == 0) table.place = i;
         const int j = table.count++;
-        table.t[j] = t;
+        table.t[j] = Entry{t, grads[i]};
         table.first[j] = (int32_t)blocks;
         const int states = o.bits8 ? 4 : 16;
-        const bool vec = aligned(t.param, o.param_f32 ? 16 : 8) && aligned(t.grad, o.grad_f32 ? 16 : 8) &&
+        const bool vec = aligned(t.param, o.param_f32 ? 16 : 8) && aligned(grads[i], o.grad_f32 ? 16 : 8) &&
                          aligned(t.exp_avg, states) && aligned(t.exp_avg_sq, states) && aligned(t.copy, 8);
         if (vec) table.vec |= 1ULL << j;
         blocks += need;

@@ -15,13 +15,13 @@ using namespace fp8q::adamw;
 
 constexpr int64_t kMaxNumel = 1LL << 40;
 
-int check_tensor(const fp8q_adamw_tensor& t, bool param_f32, bool grad_f32, bool bits8) {
+int check_tensor(const fp8q_adamw_tensor& t, const void* grad, bool param_f32, bool grad_f32, bool bits8) {
     if (t.numel < 0 || t.numel > kMaxNumel) return FP8Q_ERR_SHAPE;
-    if (t.numel == 0 || !t.grad) return FP8Q_OK;
+    if (t.numel == 0 || !grad) return FP8Q_OK;
     if (!t.param || !t.exp_avg || !t.exp_avg_sq) return FP8Q_ERR_NULL;
     if (bits8 != (t.exp_avg_scale != nullptr) || bits8 != (t.exp_avg_sq_scale != nullptr)) return FP8Q_ERR_NULL;
     if (t.copy && !param_f32) return FP8Q_ERR_ENUM;
-    if (!is_aligned(t.param, param_f32 ? 4 : 2) || !is_aligned(t.grad, grad_f32 ? 4 : 2) || !is_aligned(t.copy, 2) ||
+    if (!is_aligned(t.param, param_f32 ? 4 : 2) || !is_aligned(grad, grad_f32 ? 4 : 2) || !is_aligned(t.copy, 2) ||
         (!bits8 && (!is_aligned(t.exp_avg, 4) || !is_aligned(t.exp_avg_sq, 4))) ||
         !is_aligned(t.exp_avg_scale, 4) || !is_aligned(t.exp_avg_sq_scale, 4))
         return FP8Q_ERR_ALIGN;
@@ -32,9 +32,9 @@ int check_tensor(const fp8q_adamw_tensor& t, bool param_f32, bool grad_f32, bool
 
 extern "C" {
 
-int adamw_step(int32_t count, const fp8q_adamw_tensor* tensors, int param_dtype, int grad_dtype, int state_bits,
-               double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
-               const float* lr_dev, const int64_t* step_dev, const float* grad_scale, uint64_t seed,
+int adamw_step(int32_t count, const fp8q_adamw_tensor* tensors, const void* const* grads, int param_dtype,
+               int grad_dtype, int state_bits, double lr, double beta1, double beta2, double eps, double weight_decay,
+               int64_t step, const float* lr_dev, const int64_t* step_dev, const float* grad_scale, uint64_t seed,
                hipStream_t stream) {
     if ((param_dtype != FP8Q_ADAMW_BF16 && param_dtype != FP8Q_ADAMW_F32) ||
         (grad_dtype != FP8Q_ADAMW_BF16 && grad_dtype != FP8Q_ADAMW_F32) || (state_bits != 32 && state_bits != 8))
@@ -45,14 +45,14 @@ int adamw_step(int32_t count, const fp8q_adamw_tensor* tensors, int param_dtype,
         !std::isfinite(eps) || !std::isfinite(lr) || !std::isfinite(weight_decay))
         return FP8Q_ERR_SHAPE;
     if (count == 0) return FP8Q_OK;
-    if (!tensors) return FP8Q_ERR_NULL;
+    if (!tensors || !grads) return FP8Q_ERR_NULL;
     if (!is_aligned(lr_dev, 4) || !is_aligned(step_dev, 8) || !is_aligned(grad_scale, 4)) return FP8Q_ERR_ALIGN;
     const bool param_f32 = param_dtype == FP8Q_ADAMW_F32, grad_f32 = grad_dtype == FP8Q_ADAMW_F32;
     bool work = false;
     for (int32_t i = 0; i < count; ++i) {
-        const int st = check_tensor(tensors[i], param_f32, grad_f32, state_bits == 8);
+        const int st = check_tensor(tensors[i], grads[i], param_f32, grad_f32, state_bits == 8);
         if (st != FP8Q_OK) return st;
-        work |= tensors[i].grad && tensors[i].numel > 0;
+        work |= grads[i] && tensors[i].numel > 0;
     }
     if (!work) return FP8Q_OK;
     Options o = {};
@@ -60,7 +60,7 @@ int adamw_step(int32_t count, const fp8q_adamw_tensor* tensors, int param_dtype,
     o.eps = (float)eps; o.step = step;
     o.lr_dev = lr_dev; o.step_dev = step_dev; o.grad_scale = grad_scale; o.seed = seed;
     o.param_f32 = param_f32; o.grad_f32 = grad_f32; o.bits8 = state_bits == 8;
-    return hip_status(launch_step(count, tensors, o, stream));
+    return hip_status(launch_step(count, tensors, grads, o, stream));
 }
 
 }  // extern "C"

@@ -19,7 +19,7 @@ struct Args {
     int32_t kt;          // K tiles
     const uint16_t* x;
     int64_t ld_x, ld_xj;
-    bool x_vec;          // rows of x start on 16-byte boundaries
+    bool x_vec;          // rows of x are whole pieces of 16 bytes on 16-byte boundaries
     const uint8_t* w;
     int64_t ld_w, stride_up, stride_w;
     const uint32_t* s;

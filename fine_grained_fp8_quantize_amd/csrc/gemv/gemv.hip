@@ -27,7 +27,7 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kTilesInFlight = 4;
+constexpr int kInFlight = 4;  // tiles of weights that a wave loads at once
 
 // 2^(byte - 127) as a float (2^-127 is subnormal; 255 is the infinity that
 // makes the block's values NaN).
@@ -44,15 +44,21 @@ __device__ __forceinline__ bf16x8 dequant8(uint32_t codes, float scale) {
     return __builtin_bit_cast(bf16x8, w);
 }
 
-// Elements k..k + 7 of a row of x, zeros from `end` on.
+// Elements k..k + 7 of a row of x, zeros from `end` on. VEC: rows start on
+// 16-byte boundaries and `end` is a multiple of 8.
 template <bool VEC>
 __device__ __forceinline__ bf16x8 load_x(const uint16_t* row, int64_t k, int64_t end) {
-    if (VEC && k + 8 <= end) return *reinterpret_cast<const bf16x8*>(row + k);
-    uint32_t w[4] = {0, 0, 0, 0};
+    uint4 w = {};
+    if constexpr (VEC) {
+        if (k < end) w = *reinterpret_cast<const uint4*>(row + k);
+    } else {
+        uint32_t h[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (k + i < end) w[i >> 1] |= (uint32_t)row[k + i] << (16 * (i & 1));
-    return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+        for (int i = 0; i < 8; ++i)
+            if (k + i < end) h[i >> 1] |= (uint32_t)row[k + i] << (16 * (i & 1));
+        w = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    return __builtin_bit_cast(bf16x8, w);
 }
 
 template <bool F32>
@@ -127,18 +133,24 @@ __device__ __forceinline__ int find_routes(const Args& p, Routes& r, int slot, b
     return none ? p.experts : want;
 }
 
-// A workgroup owns 16 MS rows by 16 columns (GATED: 8 gate and 8 up columns):
-// wave w takes `tiles` K tiles from w * tiles on, four of them in flight; the
-// waves' partials are added in wave order through LDS, so the result does not
-// depend on timing.
-template <int MS, bool GATED, bool F32, bool VEC>
-__global__ __launch_bounds__(64 * kMaxWaves) void gemv_kernel(Args p, int tiles) {
-    extern __shared__ v4f partial[];  // [waves][MS][64]
+// A workgroup owns 16 MS rows by NT groups of 16 columns (GATED: of 8 gate and 8
+// up columns): wave w takes `tiles` K tiles from w * tiles on, with its loads of
+// x serving all NT groups; the waves' partials are added in wave order through
+// LDS, so the result does not depend on timing.
+template <int MS, int NT, bool GATED, bool F32, bool VEC>
+__global__ __launch_bounds__(64 * max_waves(MS)) void gemv_kernel(Args p, int tiles) {
+    extern __shared__ v4f partial[];  // [waves][NT][MS][64]
     __shared__ Routes found;
     constexpr int COLS = GATED ? 8 : 16;
+    constexpr int TI = kInFlight / NT;
+    // x of a step: one row tile and up to two K tiles at once, so that all loads of the step are in flight together;
+    // one K tile at a time with four of them, one piece of 8 k at a time with more row tiles: more registers would be
+    // spilled (1 x 1024 x 512, four K tiles at once: 4.3 instead of 3.1 us).
+    constexpr int Q = MS == 1 ? 4 : 1;
+    constexpr bool AHEAD = MS == 1 && TI < 4;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int i = lane & 15, b = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * COLS;
+    const int64_t g0 = (int64_t)blockIdx.x * NT, groups = (p.n + COLS - 1) / COLS;
     const bool routed = p.ids != nullptr;
     int expert = 0, rows = 0, row0 = 0;
     if (routed) {
@@ -147,101 +159,152 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_kernel(Args p, int tiles)
         if (expert < 0) return;
         rows = found.count;
         if (none) {
-            for (int x = threadIdx.x; x < rows * (COLS / 4); x += blockDim.x)
-                store4<F32>(p, found.list[x / (COLS / 4)], n0 + x % (COLS / 4) * 4, v4f{0.f, 0.f, 0.f, 0.f});
+            constexpr int QUADS = NT * COLS / 4;
+            for (int x = threadIdx.x; x < rows * QUADS; x += blockDim.x)
+                store4<F32>(p, found.list[x / QUADS], g0 * COLS + x % QUADS * 4, v4f{0.f, 0.f, 0.f, 0.f});
             return;
         }
     } else {
         row0 = (int)blockIdx.y * 16 * MS;
         rows = (int)min(p.tokens - row0, (int64_t)16 * MS);
     }
-    // GATED: rows 0..7 of the MFMA's operand are gate columns n0.., 8..15 up ones
-    const int r = GATED ? (int)(n0 & 15) + (i & 7) : i;
+    // GATED: rows 0..7 of the MFMA's operand are gate columns, 8..15 up ones
     const bool up = GATED && i >= 8;
-    const uint8_t* const w = p.w + expert * p.stride_w + (up ? p.stride_up : 0) + n0 / 16 * mx4::kTileBytes + r * 64 +
-                             ((b ^ (r >> 2)) & 3) * 16;
-    const uint32_t* const sw = p.s + expert * p.stride_s + (up ? p.stride_ups : 0) + n0 / 16 * mx4::kScaleWords + 4 * r + b;
+    const uint8_t* w[NT];
+    const uint32_t* sw[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int64_t n0 = min(g0 + j, groups - 1) * COLS;  // groups past the last repeat it: not stored
+        const int r = GATED ? (int)(n0 & 15) + (i & 7) : i;
+        w[j] = p.w + expert * p.stride_w + (up ? p.stride_up : 0) + n0 / 16 * mx4::kTileBytes + r * 64 +
+               ((b ^ (r >> 2)) & 3) * 16;
+        sw[j] = p.s + expert * p.stride_s + (up ? p.stride_ups : 0) + n0 / 16 * mx4::kScaleWords + 4 * r + b;
+    }
     const int first = wave * tiles, last = min(first + tiles, p.kt);
     for (int done = 0; done < rows; done += 16 * MS) {
         const int left = rows - done;  // rows of this pass, and behind it
         const uint16_t* xr[MS];
-        v4f acc[MS];
+        v4f acc[NT][MS];
 #pragma unroll
         for (int s = 0; s < MS; ++s) {
-            const int at = done + min(16 * s + i, left - 1);  // rows past the last repeat it: not stored
+            const int at = done + min(16 * s + i, left - 1);
             const int route = routed ? found.list[at] : row0 + at;
             const int t = route / p.topk;
             xr[s] = p.x + t * p.ld_x + (route - t * p.topk) * p.ld_xj;
-            acc[s] = v4f{0.f, 0.f, 0.f, 0.f};
-        }
-        for (int kt = first; kt < last; kt += kTilesInFlight) {
-            v4i codes[kTilesInFlight];
-            uint32_t words[kTilesInFlight];
 #pragma unroll
-            for (int u = 0; u < kTilesInFlight; ++u) {
-                const int64_t t = min(kt + u, last - 1);  // past the wave's last tile: skipped below
-                codes[u] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(w + t * p.ld_w * mx4::kTileBytes));
-                words[u] = sw[t / mx4::kGroupTiles * p.ld_s * mx4::kScaleWords];
+            for (int j = 0; j < NT; ++j) acc[j][s] = v4f{0.f, 0.f, 0.f, 0.f};
+        }
+        // (lanes of rows past the last load nothing: zeros)
+        int64_t end[MS];
+#pragma unroll
+        for (int s = 0; s < MS; ++s) end[s] = 16 * s + i < left ? p.k : 0;
+        for (int kt = first; kt < last; kt += TI) {
+            // Past the wave's last tile that one is loaded again, and counts as zeros (x) times codes of scale 1
+            // (finite).
+            v4i codes[TI][NT];
+            uint32_t words[TI][NT];
+            bf16x8 xv[TI][MS][Q];
+#pragma unroll
+            for (int u = 0; u < TI; ++u) {
+                const int64_t t = min(kt + u, last - 1);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    codes[u][j] =
+                        __builtin_nontemporal_load(reinterpret_cast<const v4i*>(w[j] + t * p.ld_w * mx4::kTileBytes));
+                    words[u][j] = sw[j][t / mx4::kGroupTiles * p.ld_s * mx4::kScaleWords];
+                }
+            }
+            auto load_row = [&](int u, int s, int q) {
+                const int64_t k0 = (int64_t)(kt + u) * mx4::kTileK + 32 * b + 8 * q;
+                return load_x<VEC>(xr[s], k0, kt + u < last ? end[s] : 0);
+            };
+            auto load_tile = [&](int u) {
+#pragma unroll
+                for (int s = 0; s < MS; ++s)
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) xv[u][s][q] = load_row(u, s, q);
+            };
+            if constexpr (AHEAD) {
+#pragma unroll
+                for (int u = 0; u < TI; ++u) load_tile(u);
             }
 #pragma unroll
-            for (int u = 0; u < kTilesInFlight; ++u) {
-                if (kt + u >= last) break;
-                const float scale = block_scale((words[u] >> (8 * ((kt + u) % mx4::kGroupTiles))) & 255u);
-                const int64_t k0 = (int64_t)(kt + u) * mx4::kTileK + 32 * b;
+            for (int u = 0; u < TI; ++u) {
+                if constexpr (!AHEAD) {
+                    if (kt + u >= last) break;
+                    if constexpr (Q == 4) load_tile(u);
+                }
+                float scale[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const uint32_t word = kt + u < last ? words[u][j] >> (8 * ((kt + u) % mx4::kGroupTiles)) : 127u;
+                    scale[j] = block_scale(word & 255u);
+                }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const bf16x8 wv = dequant8((uint32_t)codes[u][q], scale);
+                    if constexpr (Q == 1) {
 #pragma unroll
-                    for (int s = 0; s < MS; ++s) {
-                        const bf16x8 xv = load_x<VEC>(xr[s], k0 + 8 * q, p.k);
-                        acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xv, acc[s], 0, 0, 0);
+                        for (int s = 0; s < MS; ++s) xv[u][s][0] = load_row(u, s, q);
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const bf16x8 wv = dequant8((uint32_t)codes[u][j][q], scale[j]);
+#pragma unroll
+                        for (int s = 0; s < MS; ++s)
+                            acc[j][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xv[u][s][q % Q], acc[j][s], 0, 0, 0);
                     }
                 }
             }
         }
         if (done > 0) __syncthreads();  // the partials of the rows before have been read
 #pragma unroll
-        for (int s = 0; s < MS; ++s) partial[(wave * MS + s) * 64 + lane] = acc[s];
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int s = 0; s < MS; ++s) partial[((wave * NT + j) * MS + s) * 64 + lane] = acc[j][s];
         __syncthreads();
         // a lane's result: row l % 16 of x, columns 4 (l / 16)..; GATED: gate for l < 32, up for the same columns
         // 32 lanes on
-        constexpr int LANES = GATED ? 32 : 64;
-        for (int x = threadIdx.x; x < MS * LANES; x += blockDim.x) {
-            const int l = x % LANES, s = x / LANES, row = 16 * s + (l & 15);
+        constexpr int LANES = GATED ? 32 : 64, PART = NT * MS * 64;
+        for (int x = threadIdx.x; x < NT * MS * LANES; x += blockDim.x) {
+            const int l = x % LANES, s = x / LANES % MS, j = x / LANES / MS, row = 16 * s + (l & 15);
             if (row >= left) continue;
-            v4f v = partial[s * 64 + l];
-            for (int k = 1; k < waves; ++k) v += partial[(k * MS + s) * 64 + l];
+            const v4f* const from = partial + (j * MS + s) * 64 + l;
+            v4f v = from[0];
+            for (int k = 1; k < waves; ++k) v += from[k * PART];
             if constexpr (GATED) {
-                v4f u = partial[s * 64 + 32 + l];
-                for (int k = 1; k < waves; ++k) u += partial[(k * MS + s) * 64 + 32 + l];
+                v4f u = from[32];
+                for (int k = 1; k < waves; ++k) u += from[k * PART + 32];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = gate_act(p.act, v[j]) * u[j];
+                for (int c = 0; c < 4; ++c) v[c] = gate_act(p.act, v[c]) * u[c];
             }
             const int64_t route = routed ? found.list[done + row] : row0 + done + row;
-            store4<F32>(p, route, n0 + 4 * (l >> 4), v);
+            const int64_t n = (g0 + j) * COLS + 4 * (l >> 4);
+            if (n < p.n) store4<F32>(p, route, n, v);
         }
     }
 }
 
+template <int MS, int NT, bool GATED, bool F32>
+void launch_nt(const Args& p, const Form& f, dim3 grid, hipStream_t stream) {
+    const dim3 block(64 * f.waves);
+    const size_t lds = (size_t)f.waves * NT * MS * 64 * sizeof(v4f);
+    if (p.x_vec)
+        hipLaunchKernelGGL((gemv_kernel<MS, NT, GATED, F32, true>), grid, block, lds, stream, p, f.tiles);
+    else
+        hipLaunchKernelGGL((gemv_kernel<MS, NT, GATED, F32, false>), grid, block, lds, stream, p, f.tiles);
+}
+
 template <int MS, bool GATED, bool F32>
 void launch_ms(const Args& p, const Form& f, dim3 grid, hipStream_t stream) {
-    const dim3 block(64 * f.waves);
-    const size_t lds = (size_t)f.waves * MS * 64 * sizeof(v4f);
-    if (p.x_vec)
-        hipLaunchKernelGGL((gemv_kernel<MS, GATED, F32, true>), grid, block, lds, stream, p, f.tiles);
-    else
-        hipLaunchKernelGGL((gemv_kernel<MS, GATED, F32, false>), grid, block, lds, stream, p, f.tiles);
+    if (f.nt == 1) launch_nt<MS, 1, GATED, F32>(p, f, grid, stream);
+    else if (f.nt == 2) launch_nt<MS, 2, GATED, F32>(p, f, grid, stream);
+    else launch_nt<MS, 4, GATED, F32>(p, f, grid, stream);
 }
 
 template <bool GATED, bool F32>
 void launch_form(const Args& p, hipStream_t stream) {
-    // with ids, no expert gets more than the tokens' routes, and mostly one of each token at the most
-    const Form f = form(p.tokens, p.k);
-    const unsigned columns = (unsigned)column_groups(p.n, GATED);
-    const int64_t routes = p.tokens * p.topk;
-    const unsigned rows = p.ids ? (unsigned)(routes < p.experts ? routes : p.experts) + 1
-                                : (unsigned)ceil_div(p.tokens, 16 * f.ms);
-    const dim3 grid(columns, rows);
+    const Form f = form(p.tokens, p.ids ? p.topk : 0, p.experts, p.n, p.k, GATED);
+    const dim3 grid((unsigned)ceil_div(column_groups(p.n, GATED), f.nt), (unsigned)f.rows);
     if (f.ms == 1) launch_ms<1, GATED, F32>(p, f, grid, stream);
     else if (f.ms == 2) launch_ms<2, GATED, F32>(p, f, grid, stream);
     else launch_ms<4, GATED, F32>(p, f, grid, stream);

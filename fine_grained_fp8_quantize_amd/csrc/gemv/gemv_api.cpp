@@ -57,10 +57,10 @@ int run(const Args& p, int out_dtype, hipStream_t stream) {
             p.stride_up % 16 != 0)
             return FP8Q_ERR_ALIGN;
     }
-    if (!launchable({gemv::column_groups(p.n, p.gated), 64 * gemv::kMaxWaves})) return FP8Q_ERR_SHAPE;
+    if (!launchable({gemv::column_groups(p.n, p.gated), 64 * gemv::max_waves(1)})) return FP8Q_ERR_SHAPE;
     Args a = p;
     a.kt = (int32_t)ceil_div(p.k, mx4::kTileK);
-    a.x_vec = is_aligned(p.x, 16) && p.ld_x % 8 == 0 && p.ld_xj % 8 == 0;
+    a.x_vec = is_aligned(p.x, 16) && p.ld_x % 8 == 0 && p.ld_xj % 8 == 0 && p.k % 8 == 0;
     a.y_vec = is_aligned(p.y, p.f32 ? 16 : 8) && p.ld_y % 4 == 0;
     return hip_status(gemv::launch(a, stream));
 }

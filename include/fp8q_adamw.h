@@ -20,7 +20,6 @@ extern "C" {
 /*
  * One tensor of a step: device arrays of `numel` elements, contiguous.
  *   param      updated in place.
- *   grad       read; NULL: the tensor takes no part in this step.
  *   exp_avg, exp_avg_sq  the two moments, updated in place. 32-bit states: FP32.
  *              8-bit states: E4M3 codes, with FP32 scales [ceil(numel / 128)],
  *              one for each 128 consecutive elements; exp_avg_sq then holds the
@@ -33,7 +32,6 @@ extern "C" {
  */
 typedef struct fp8q_adamw_tensor {
     void *param;
-    const void *grad;
     void *exp_avg;
     void *exp_avg_sq;
     float *exp_avg_scale;
@@ -65,6 +63,9 @@ typedef struct fp8q_adamw_tensor {
  * or a NaN reads back as NaN.
  *
  * tensors     HOST array of `count` entries, read during the call.
+ * grads       HOST array of `count` device addresses, read during the call: the
+ *             gradient of each tensor, contiguous; NULL: the tensor takes no
+ *             part in this step.
  * param_dtype, grad_dtype  FP8Q_ADAMW_*, the same for all tensors of a call.
  * state_bits  32 or 8.
  * lr, step    used where lr_dev, step_dev are NULL; else DEVICE arrays of one
@@ -79,9 +80,9 @@ typedef struct fp8q_adamw_tensor {
  *         FP8Q_ERR_ALIGN, FP8Q_ERR_ENUM, FP8Q_ERR_HIP. Everything is checked
  *         before the first launch.
  */
-int adamw_step(int32_t count, const fp8q_adamw_tensor *tensors, int param_dtype, int grad_dtype, int state_bits,
-               double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
-               const float *lr_dev, const int64_t *step_dev, const float *grad_scale, uint64_t seed,
+int adamw_step(int32_t count, const fp8q_adamw_tensor *tensors, const void *const *grads, int param_dtype,
+               int grad_dtype, int state_bits, double lr, double beta1, double beta2, double eps, double weight_decay,
+               int64_t step, const float *lr_dev, const int64_t *step_dev, const float *grad_scale, uint64_t seed,
                hipStream_t stream);
 
 #ifdef __cplusplus

@@ -15,6 +15,8 @@ namespace gemv {
 hipError_t launch(const Args&, hipStream_t) { return hipErrorNoDevice; }
 }  // namespace gemv
 namespace adamw {
-hipError_t launch_step(int32_t, const fp8q_adamw_tensor*, const Options&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_step(int32_t, const fp8q_adamw_tensor*, const void* const*, const Options&, hipStream_t) {
+    return hipErrorNoDevice;
+}
 }  // namespace adamw
 }  // namespace fp8q

@@ -37,15 +37,18 @@ def test_header_is_exported_and_bound():
 
 
 def _step(count=1, tensors=None, pd=1, gd=0, bits=32, lr=1e-3, b1=0.9, b2=0.99, eps=1e-8, wd=0.1, step=1, lr_dev=0,
-          step_dev=0, scale=0, null=False, **entry):
+          step_dev=0, scale=0, null=False,
+          no_grads=False, **entry):
     """A call whose one tensor is empty, unless `entry` gives it elements: nothing is ever launched."""
     e = (_adamw._Tensor * 1)()
-    fields = dict(param=0x1000, grad=0x2000, exp_avg=0x3000, exp_avg_sq=0x4000, copy=0x5000, numel=0)
+    grad = entry.pop("grad", 0x2000)
+    fields = dict(param=0x1000, exp_avg=0x3000, exp_avg_sq=0x4000, copy=0x5000, numel=0)
     if bits == 8:
         fields.update(exp_avg_scale=0x6000, exp_avg_sq_scale=0x7000)
     for k, v in {**fields, **entry}.items():
         setattr(e[0], k, v)
-    return _lib().adamw_step(count, None if null else e, pd, gd, bits, lr, b1, b2, eps, wd, step, lr_dev, step_dev, scale, 0,
+    g = (ctypes.c_void_p * 1)(grad)
+    return _lib().adamw_step(count, None if null else e, None if no_grads else g, pd, gd, bits, lr, b1, b2, eps, wd, step, lr_dev, step_dev, scale, 0,
                              None)
 
 
@@ -54,6 +57,7 @@ NAN, INF = float("nan"), float("inf")
 
 @pytest.mark.parametrize("kw,want", [
     (dict(), OK), (dict(count=0, null=True), OK), (dict(numel=5, grad=0), OK), (dict(null=True), ERR_NULL),
+    (dict(no_grads=True), ERR_NULL),
     (dict(pd=2), ERR_ENUM), (dict(gd=-1), ERR_ENUM), (dict(bits=16), ERR_ENUM), (dict(count=-1), ERR_SHAPE),
     (dict(step=0), ERR_SHAPE), (dict(step=0, step_dev=0x100), OK), (dict(step_dev=0x104), ERR_ALIGN),
     (dict(lr_dev=0x102), ERR_ALIGN), (dict(scale=0x101), ERR_ALIGN), (dict(b1=1.0), ERR_SHAPE),
