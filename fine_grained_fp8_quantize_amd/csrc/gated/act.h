@@ -32,15 +32,6 @@ __device__ __forceinline__ float gate_share(int act, float g) {
 }
 __device__ __forceinline__ float gate_act(int act, float g) { return g * gate_share(act, g); }
 
-// act(g) and its slope s + g s (1 - s) w', with s the logistic function of w.
-__device__ __forceinline__ float gate_act_slope(int act, float g, float& slope) {
-    const float s = gate_share(act, g);
-    float by = g * (1.0f - s);
-    if (act != FP8Q_ACT_SILU) by *= kGeluScale * __builtin_fmaf(3.0f * kGeluCube * g, g, 1.0f);
-    slope = __builtin_fmaf(s, by, s);
-    return g * s;
-}
-
 // Four floats to columns n..n+3 of a row of `cols`, together where they all
 // exist and the address allows it (vec): as they are, or as bf16.
 template <class V4>

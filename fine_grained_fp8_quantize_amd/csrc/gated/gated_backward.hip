@@ -35,11 +35,61 @@ __device__ __forceinline__ Eight load8(const uint16_t* p, int64_t left) {
     }
 }
 
+// e^-w is taken as 2^(-w log2 e) with one rounded product: |w| 2^-24 of it,
+// where the bf16 of the gate is |w| 2^-9. An infinite power gives a share of 0.
 __device__ __forceinline__ void gradients(int act, float dh, float g, float u, float& dg, float& du) {
-    float slope;
-    du = dh * gate_act_slope(act, g, slope);
-    dg = dh * u * slope;
+    constexpr float kLog2e = 1.44269504088896340736f;
+    float w = g, by = 1.0f;
+    if (act != FP8Q_ACT_SILU) {
+        w = kGeluScale * __builtin_fmaf(kGeluCube * g * g, g, g);
+        by = kGeluScale * __builtin_fmaf(3.0f * kGeluCube * g, g, 1.0f);
+    }
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-w * kLog2e));
+    const float r = g * (1.0f - s);
+    const float ds = dh * s;
+    du = ds * g;
+    dg = (ds * u) * (act != FP8Q_ACT_SILU ? __builtin_fmaf(r, by, 1.0f) : 1.0f + r);
 }
+
+// The scale of a tile, fl(amax / 448) (one correction of the product with the
+// rounded reciprocal), and what its elements are multiplied with: 1 / s, a hair
+// less, so that the largest stays within 448. A quotient in place of the product
+// would take as many operations again as everything else here, and would differ
+// where it lies within 2^-21 of the border of two codes. Tiny scales, whose
+// reciprocals are not finite, take the quotient.
+struct TileScale {
+    float s, y;
+    bool slow;
+};
+__device__ __forceinline__ TileScale tile_scale(float amax) {
+    constexpr float kBy = 1.0f / kE4M3Max;
+    TileScale t;
+    const float q = amax * kBy;
+    t.s = __builtin_fmaf(__builtin_fmaf(-q, kE4M3Max, amax), kBy, q);
+    t.slow = !(t.s >= kSmallScale);
+    t.y = __builtin_amdgcn_rcpf(t.s) * (1.0f - 0x1p-22f);
+    return t;
+}
+__device__ __forceinline__ float tiny_quotient(float x, float s) {
+    return s == 0.0f ? __builtin_copysignf(0.0f, x) : __builtin_fminf(__builtin_fmaxf(x / s, -kE4M3Max), kE4M3Max);
+}
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, const TileScale& t) {
+    float q[4] = {a * t.y, b * t.y, c * t.y, d * t.y};
+    if (t.slow) {
+        q[0] = tiny_quotient(a, t.s);
+        q[1] = tiny_quotient(b, t.s);
+        q[2] = tiny_quotient(c, t.s);
+        q[3] = tiny_quotient(d, t.s);
+    }
+    uint32_t w = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], (int)w, true);
+}
+// (a NaN does not count here: it has a code of its own)
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+    return __builtin_fmaxf(__builtin_fmaxf(m, __builtin_fabsf(a)), __builtin_fabsf(b));
+}
+// The largest of 16 lanes' values >= 0, whose bits are ordered as they are.
+__device__ __forceinline__ float row_max(float m) { return __uint_as_float(row16_max(__float_as_uint(m))); }
 
 // Eight columns of a row per thread; 16 lanes hold a 1x128 tile.
 template <bool E4M3, bool VEC>
@@ -56,20 +106,20 @@ __global__ __launch_bounds__(kBackwardThreads) void backward_rows_kernel(Backwar
     for (int i = 0; i < 8; ++i) gradients(p.act, dh.at(i), g.at(i), u.at(i), d[0][i], d[1][i]);
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
+        const float(&v)[8] = d[o];
         if constexpr (E4M3) {
-            uint32_t top = 0;
+            float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = umax32(top, __float_as_uint(d[o][i]) & 0x7FFFFFFFu);
-            const GroupScale gs = group_scale_f32(__uint_as_float(row16_max(top)));
-            const v4f lo = {d[o][0], d[o][1], d[o][2], d[o][3]}, hi = {d[o][4], d[o][5], d[o][6], d[o][7]};
+            for (int i = 0; i < 8; i += 2) top = max_abs(top, v[i], v[i + 1]);
+            const TileScale ts = tile_scale(row_max(top));
             *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * p.ldo + o * p.n + c) =
-                make_uint2(e4m3x4(lo, gs), e4m3x4(hi, gs));
-            if (c % 128 == 0) p.out_scale[(o * p.n + c) / 128 * p.ld_os + row] = gs.s;
+                make_uint2(codes4(v[0], v[1], v[2], v[3], ts), codes4(v[4], v[5], v[6], v[7], ts));
+            if (c % 128 == 0) p.out_scale[(o * p.n + c) / 128 * p.ld_os + row] = ts.s;
         } else {
             uint16_t* const dst = static_cast<uint16_t*>(p.out) + row * p.ldo + o * p.n + c;
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(d[o][2 * i], d[o][2 * i + 1]);
+            for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
             if constexpr (VEC) {
                 *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
             } else {
@@ -81,21 +131,38 @@ __global__ __launch_bounds__(kBackwardThreads) void backward_rows_kernel(Backwar
     }
 }
 
+// max(a, b) of two values per lane, one of them kept by each half (HALF: 32
+// lanes) or each odd and even row of 16 lanes: the lower lanes get a's maximum
+// with their partner's a, the upper ones b's with theirs.
+template <int HALF>
+__device__ __forceinline__ float fold(float a, float b) {
+    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    if constexpr (HALF == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+        return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    } else {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+        return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+}
+
 // Both tilings: a workgroup takes the panel of 128 tokens by 128 columns of
 // dG and of dU. Thread (r = t / 16, g = t % 16) has tokens 4 r..4 r + 3 and
 // columns 8 g..8 g + 7: a token's 1x128 tile is one row of 16 lanes, a column's
-// 128x1 tile the threads of one g, joined over the wave by shuffles and over
-// the waves through LDS. Codes along the columns pass through LDS, so that both
-// sides write whole 128-byte lines. The 16-byte chunks of a transposed row are
-// placed by an XOR with the column's group, so that the 16 groups' writes of
-// one row index spread over the banks.
+// 128x1 tile the threads of one g, joined over a wave's four rows of lanes by
+// folding (16 columns' maxima, 8 of each output, end as four in each lane) and
+// over the waves through LDS. Codes along the columns pass through LDS, so that
+// both sides write whole 128-byte lines. The 16-byte chunks of a transposed row
+// are placed by an XOR with the column's group, so that the 16 groups' writes
+// of one row index spread over the banks.
 constexpr int kWaves = kPanelThreads / 64;
 __device__ __forceinline__ int panel_chunk(int chunk, int col) { return chunk ^ ((col >> 3) & 7); }
 
-__global__ __launch_bounds__(kPanelThreads) void backward_panel_kernel(BackwardArgs p) {
+__global__ __launch_bounds__(kPanelThreads, 4) void backward_panel_kernel(BackwardArgs p) {
     __shared__ __attribute__((aligned(16))) uint8_t codes[2][128 * 128];
-    __shared__ uint32_t red[kWaves][2][128];
-    __shared__ float row_s[2][128], col_s[2][128], col_y[2][128];
+    __shared__ float red[kWaves][2][128];
+    __shared__ float row_s[2][128];
+    __shared__ float col_top[2][128];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, g = t & 15, r = t >> 4;
     const int64_t panels = p.n / 128, tb = blockIdx.x / panels, cb = blockIdx.x - tb * panels;
     const int64_t t0 = tb * 128, c0 = cb * 128;
@@ -110,47 +177,48 @@ __global__ __launch_bounds__(kPanelThreads) void backward_panel_kernel(BackwardA
         up[i] = load8<true>(gate + p.n, 8);
     }
     float d[2][4][8];
+    float col[2][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             gradients(p.act, dh[i].at(k), gt[i].at(k), up[i].at(k), d[0][i][k], d[1][i][k]);
-#pragma unroll
-    for (int o = 0; o < 2; ++o) {
         // along the rows
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t top = 0;
+        for (int o = 0; o < 2; ++o) {
+            const float(&v)[8] = d[o][i];
+            float top = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) top = umax32(top, __float_as_uint(d[o][i][k]) & 0x7FFFFFFFu);
-            const GroupScale gs = group_scale_f32(__uint_as_float(row16_max(top)));
-            const v4f lo = {d[o][i][0], d[o][i][1], d[o][i][2], d[o][i][3]};
-            const v4f hi = {d[o][i][4], d[o][i][5], d[o][i][6], d[o][i][7]};
+            for (int k = 0; k < 8; k += 2) top = max_abs(top, v[k], v[k + 1]);
+            const TileScale ts = tile_scale(row_max(top));
             *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + (t0 + 4 * r + i) * p.ldo + o * p.n + c0 + 8 * g) =
-                make_uint2(e4m3x4(lo, gs), e4m3x4(hi, gs));
-            if (g == 0) row_s[o][4 * r + i] = gs.s;
-        }
-        // the largest of the wave's 16 tokens in each column
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = umax32(top, __float_as_uint(d[o][i][k]) & 0x7FFFFFFFu);
-            top = umax32(top, (uint32_t)__shfl_xor((int)top, 16));
-            top = umax32(top, (uint32_t)__shfl_xor((int)top, 32));
-            if (lane < 16) red[wave][o][8 * g + k] = top;
+                make_uint2(codes4(v[0], v[1], v[2], v[3], ts), codes4(v[4], v[5], v[6], v[7], ts));
+            if (g == 0) row_s[o][4 * r + i] = ts.s;
         }
     }
+    // the largest of the wave's 16 tokens in each column: lanes 0..31 keep dG's, 32..63 dU's, of those even rows of
+    // lanes the columns 8 g..8 g + 3, odd ones the next four
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            col[o][k] = max_abs(max_abs(0.0f, d[o][0][k], d[o][1][k]), d[o][2][k], d[o][3][k]);
+    float half[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) half[k] = fold<32>(col[0][k], col[1][k]);
+    v4f mine;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mine[k] = fold<16>(half[k], half[k + 4]);
+    *reinterpret_cast<v4f*>(&red[wave][lane >> 5][8 * g + 4 * ((lane >> 4) & 1)]) = mine;
     __syncthreads();
     if (t < 256) {
         const int o = t >> 7, c = t & 127;
-        uint32_t top = 0;
+        float top = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = umax32(top, red[w][o][c]);
-        const GroupScale gs = group_scale_f32(__uint_as_float(top));
-        col_s[o][c] = gs.s;
-        col_y[o][c] = gs.y;
-        p.out_t_scale[tb * p.ld_ts + o * p.n + c0 + c] = gs.s;
+        for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, red[w][o][c]);
+        const TileScale ts = tile_scale(top);
+        col_top[o][c] = top;
+        p.out_t_scale[tb * p.ld_ts + o * p.n + c0 + c] = ts.s;
         p.out_scale[(o * p.n + c0) / 128 * p.ld_os + t0 + c] = row_s[o][c];
     }
     __syncthreads();
@@ -159,12 +227,9 @@ __global__ __launch_bounds__(kPanelThreads) void backward_panel_kernel(BackwardA
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int c = 8 * g + k;
-            GroupScale gs;
-            gs.s = col_s[o][c];
-            gs.y = col_y[o][c];
-            gs.slow = !(gs.s >= kSmallScale);
-            const v4f v = {d[o][0][k], d[o][1][k], d[o][2][k], d[o][3][k]};
-            *reinterpret_cast<uint32_t*>(&codes[o][c * 128 + panel_chunk(r >> 2, c) * 16 + (r & 3) * 4]) = e4m3x4(v, gs);
+            const TileScale ts = tile_scale(col_top[o][c]);
+            *reinterpret_cast<uint32_t*>(&codes[o][c * 128 + panel_chunk(r >> 2, c) * 16 + (r & 3) * 4]) =
+                codes4(d[o][0][k], d[o][1][k], d[o][2][k], d[o][3][k], ts);
         }
     __syncthreads();
 #pragma unroll
