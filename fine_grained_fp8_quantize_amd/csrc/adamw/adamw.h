@@ -10,7 +10,6 @@
 namespace fp8q {
 namespace adamw {
 
-constexpr int kChunk = 4096;    // elements per workgroup
 constexpr int kThreads = 256;
 constexpr int kMaxTensors = 56;  // per launch: the table travels as a kernel argument of at most 4 KB
 

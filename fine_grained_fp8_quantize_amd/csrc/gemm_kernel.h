@@ -125,7 +125,9 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_kernel(Params p) {
         const int lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave >> 1, wn = wave & 1;
-        const int slabs = tr.slabs;
+        // (gated: a tile of padding only has nothing to multiply; rows that a program sets aside for the experts can be
+        // many of them)
+        const int slabs = GATED && tr.real_end <= tr.m0 ? 0 : tr.slabs;
         const int64_t m_last = p.m - 1;
         const int64_t n_last = p.n - 1;
 
