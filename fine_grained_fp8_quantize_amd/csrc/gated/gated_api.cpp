@@ -78,7 +78,7 @@ GatedArgs gated_args(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t 
 extern "C" {
 
 int64_t fp8_gated_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    if (!size_ok(m) || !size_ok(n) || !size_ok(k)) return 0;
+    if (!size_ok(m) || !size_ok(n) || !size_ok(k) || mul_limit(m, n, kMaxSize) < 0) return 0;
     return workspace_bytes(m, n, k);
 }
 
@@ -94,7 +94,7 @@ int fp8_gated_gemm(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t ld
                                out_dtype, out_scale, ld_os, gate_up, ldg);
     if (st != FP8Q_OK) return st;
     if (!is_aligned(workspace, 16)) return FP8Q_ERR_ALIGN;
-    if (mul_limit(parts_of(m, 256), parts_of(n, 128), kMaxSize) < 0 || !launchable(tiles_shape(m, n)) ||
+    if (mul_limit(m, n, kMaxBytes) < 0 || !launchable(tiles_shape(m, n)) ||
         !launchable({parts_of(n, kRowsColumns), 1024}))
         return FP8Q_ERR_SHAPE;
     const GatedArgs p = gated_args(m, n, k, a, lda, a_scale, ld_as, b, ldb, stride_b, b_scale, ld_bs, stride_bs, act,

@@ -15,78 +15,96 @@ namespace gated {
 namespace {
 
 // Few rows of A: the weights are streamed from HBM straight to registers. A
-// workgroup owns 16 MS rows by 8 columns: the 16 rows of its MFMA's B operand
+// workgroup owns 16 MS rows by 8 NT columns: the 16 rows of an MFMA's B operand
 // are the weights of 8 gate and 8 up columns. Wave w takes the slabs w, w +
 // waves, ..., U of them in flight, and promotes each one's products with its
 // scales; the waves' FP32 partials are added in wave order through LDS, so the
 // result does not depend on timing.
-template <int MS, int U, bool F32>
-__global__ __launch_bounds__(1024) void gated_rows_kernel(Params p) {
-    extern __shared__ v4f partial[];  // [waves][MS][64]
+template <int MS, int NT, int U, bool F32>
+__global__ __launch_bounds__(64 * rows_waves(MS * NT)) void gated_rows_kernel(Params p) {
+    extern __shared__ v4f partial[];  // [waves][NT][MS][64]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int i = lane & 15, g = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * kRowsColumns;
+    const int64_t n0 = (int64_t)blockIdx.x * kRowsColumns * NT, m0 = (int64_t)blockIdx.y * 16 * MS;
     const int slabs = (int)(p.k / kSlab);
     // rows and columns past the last ones repeat it: loaded, not stored
-    const uint8_t* const wrow = p.b + (i >= 8 ? p.stride_up : 0) + min(n0 + (i & 7), p.n - 1) * p.ldb + 16 * g;
-    // (an MFMA result's four rows are 4 g..4 g + 3: gate for g < 2)
-    const float* const sb = p.b_scale + (g >= 2 ? p.stride_ups : 0) + n0 / 128 * p.ld_bs;
+    const uint8_t* wrow[NT];
+    const float* sb[NT];
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+        const int64_t first = n0 + kRowsColumns * c;
+        wrow[c] = p.b + (i >= 8 ? p.stride_up : 0) + min(first + (i & 7), p.n - 1) * p.ldb + 16 * g;
+        // (an MFMA result's four rows are 4 g..4 g + 3: gate for g < 2)
+        sb[c] = p.b_scale + (g >= 2 ? p.stride_ups : 0) + min(first, p.n - 1) / 128 * p.ld_bs;
+    }
     const uint8_t* arow[MS];
     const float* sa[MS];
-    v4f acc[MS];
+    v4f acc[NT][MS];
 #pragma unroll
     for (int s = 0; s < MS; ++s) {
-        const int64_t row = min((int64_t)(16 * s + i), p.m - 1);
+        const int64_t row = min(m0 + 16 * s + i, p.m - 1);
         arow[s] = p.a + row * p.lda + 16 * g;
         sa[s] = p.a_scale + row;
-        acc[s] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < NT; ++c) acc[c][s] = v4f{0.f, 0.f, 0.f, 0.f};
     }
     for (int j0 = wave; j0 < slabs; j0 += U * waves) {
-        v4i w[U][2], a[U][MS][2];
-        float f[U][MS];
+        v4i w[U][NT][2], a[U][MS][2];
+        float fb[U][NT], fa[U][MS];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t j = min(j0 + u * waves, slabs - 1);  // past the last slab: skipped below
-            w[u][0] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(wrow + j * kSlab));
-            w[u][1] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(wrow + j * kSlab + 64));
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                w[u][c][0] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(wrow[c] + j * kSlab));
+                w[u][c][1] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(wrow[c] + j * kSlab + 64));
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t j = min(j0 + u * waves, slabs - 1);
-            const float b = sb[j];
+#pragma unroll
+            for (int c = 0; c < NT; ++c) fb[u][c] = sb[c][j];
 #pragma unroll
             for (int s = 0; s < MS; ++s) {
                 a[u][s][0] = *reinterpret_cast<const v4i*>(arow[s] + j * kSlab);
                 a[u][s][1] = *reinterpret_cast<const v4i*>(arow[s] + j * kSlab + 64);
-                f[u][s] = sa[s][j * p.ld_as] * b;
+                fa[u][s] = sa[s][j * p.ld_as];
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (j0 + u * waves < slabs) {
-                const v8i bw = __builtin_shufflevector(w[u][0], w[u][1], 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-                for (int s = 0; s < MS; ++s) {
-                    const v8i aw = __builtin_shufflevector(a[u][s][0], a[u][s][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                    const v4f zero = {0.f, 0.f, 0.f, 0.f};
-                    const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bw, aw, zero, 0, 0, 0, 0, 0, 0);
+                for (int c = 0; c < NT; ++c) {
+                    const v8i bw = __builtin_shufflevector(w[u][c][0], w[u][c][1], 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[s][r] = __builtin_fmaf(part[r], f[u][s], acc[s][r]);
+                    for (int s = 0; s < MS; ++s) {
+                        const v8i aw = __builtin_shufflevector(a[u][s][0], a[u][s][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                        const v4f zero = {0.f, 0.f, 0.f, 0.f};
+                        const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bw, aw, zero, 0, 0, 0, 0, 0, 0);
+                        const float f = fa[u][s] * fb[u][c];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[c][s][r] = __builtin_fmaf(part[r], f, acc[c][s][r]);
+                    }
                 }
             }
         }
     }
 #pragma unroll
-    for (int s = 0; s < MS; ++s) partial[(wave * MS + s) * 64 + lane] = acc[s];
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int s = 0; s < MS; ++s) partial[((wave * NT + c) * MS + s) * 64 + lane] = acc[c][s];
     __syncthreads();
-    for (int x = threadIdx.x; x < MS * 32; x += blockDim.x) {
-        const int l = x & 31, s = x >> 5;
-        const int64_t m = 16 * s + (l & 15), n = n0 + 4 * (l >> 4);
-        if (m >= p.m) continue;
-        v4f gate = partial[s * 64 + l], up = partial[s * 64 + 32 + l];
+    for (int x = threadIdx.x; x < NT * MS * 32; x += blockDim.x) {
+        const int l = x & 31, s = (x >> 5) % MS, c = (x >> 5) / MS;
+        const int64_t m = m0 + 16 * s + (l & 15), n = n0 + kRowsColumns * c + 4 * (l >> 4);
+        if (m >= p.m || n >= p.n) continue;
+        const v4f* const from = partial + (c * MS + s) * 64 + l;
+        v4f gate = from[0], up = from[32];
         for (int w = 1; w < waves; ++w) {
-            gate += partial[(w * MS + s) * 64 + l];
-            up += partial[(w * MS + s) * 64 + 32 + l];
+            gate += from[w * NT * MS * 64];
+            up += from[w * NT * MS * 64 + 32];
         }
         if (p.gate_up != nullptr) {
             uint16_t* const dst = p.gate_up + m * p.ldg + n;
@@ -135,22 +153,21 @@ Params gated_params(const GatedArgs& g) {
     return p;
 }
 
-template <int MS, int U>
+template <int MS, int NT, int U>
 void launch_rows(const Params& p, RowsForm f, bool f32, hipStream_t stream) {
-    const LaunchShape s = rows_shape(f, p.n);
-    const dim3 grid((unsigned)s.blocks), block(s.threads);
-    const size_t lds = (size_t)s.threads * MS * sizeof(v4f);
+    const dim3 grid((unsigned)parts_of(p.n, kRowsColumns * NT), (unsigned)parts_of(p.m, 16 * MS)), block(64 * f.waves);
+    const size_t lds = (size_t)f.waves * 64 * NT * MS * sizeof(v4f);
     if (f32)
-        hipLaunchKernelGGL((gated_rows_kernel<MS, U, true>), grid, block, lds, stream, p);
+        hipLaunchKernelGGL((gated_rows_kernel<MS, NT, U, true>), grid, block, lds, stream, p);
     else
-        hipLaunchKernelGGL((gated_rows_kernel<MS, U, false>), grid, block, lds, stream, p);
+        hipLaunchKernelGGL((gated_rows_kernel<MS, NT, U, false>), grid, block, lds, stream, p);
 }
 
 }  // namespace
 
 hipError_t launch_gated(const GatedArgs& g, float* workspace, hipStream_t stream) {
     Params p = gated_params(g);
-    const RowsForm f = rows_form(g.g.m, g.g.k);
+    const RowsForm f = rows_form(g.g.m, g.g.n, g.g.k);
     if (f.ms != 0 && (!g.e4m3 || workspace)) {
         if (g.e4m3) {
             p.c = workspace;
@@ -158,9 +175,10 @@ hipError_t launch_gated(const GatedArgs& g, float* workspace, hipStream_t stream
             p.h_vec = true;
         }
         const bool f32 = g.e4m3 || g.g.out_f32;
-        if (f.ms == 1) launch_rows<1, 4>(p, f, f32, stream);
-        else if (f.ms == 2) launch_rows<2, 2>(p, f, f32, stream);
-        else launch_rows<4, 2>(p, f, f32, stream);
+        if (f.ms == 1) launch_rows<1, 1, 4>(p, f, f32, stream);
+        else if (f.ms == 2) launch_rows<2, 1, 2>(p, f, f32, stream);
+        else if (f.nt == 1) launch_rows<4, 1, 2>(p, f, f32, stream);
+        else launch_rows<4, 2, 2>(p, f, f32, stream);
         if (g.e4m3) {
             const int64_t blocks = parts_of(p.m * p.n / 8, 256);
             hipLaunchKernelGGL(quantize_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, workspace, p.m, p.n,

@@ -10,28 +10,37 @@ namespace gated {
 
 inline int64_t parts_of(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Few rows: 16 ms rows by 8 columns (8 gate and 8 up weight rows) per
-// workgroup, K split over its waves, `unroll` slabs of a wave in flight.
+// Few rows: 16 ms rows by 8 nt columns (nt times 8 gate and 8 up weight rows)
+// per workgroup, K split over its waves, four slabs of a wave in flight with
+// one row tile and two with more.
 struct RowsForm {
     int ms;  // 0: the tile kernel
-    int unroll;
+    int nt;
     int waves;
 };
 constexpr int kRowsColumns = 8;
-constexpr int kRowsMost = 64;
-
-inline RowsForm rows_form(int64_t m, int64_t k) {
-    if (m > kRowsMost) return {0, 0, 0};
-    const int ms = m <= 16 ? 1 : (m <= 32 ? 2 : 4), unroll = ms == 1 ? 4 : 2;
-    const int64_t slabs = k / 128, steps = parts_of(slabs > 0 ? slabs : 1, 16 * unroll);
-    return {ms, unroll, (int)parts_of(slabs > 0 ? slabs : 1, steps * unroll)};
-}
-inline LaunchShape rows_shape(RowsForm f, int64_t n) { return {parts_of(n, kRowsColumns), 64 * f.waves}; }
+// (eight accumulators and more take more than 128 registers)
+constexpr int rows_waves(int accumulators) { return accumulators >= 8 ? 8 : 16; }
 
 // Tiles of 256 rows by 128 columns.
-inline LaunchShape tiles_shape(int64_t m, int64_t n) {
-    return {parts_of(parts_of(m, 256) * parts_of(n, 128), 8) * 8, 512};
+inline int64_t tiles_of(int64_t m, int64_t n) { return parts_of(m, 256) * parts_of(n, 128); }
+
+inline RowsForm rows_form(int64_t m, int64_t n, int64_t k) {
+    const int ms = m <= 16 ? 1 : (m <= 32 ? 2 : 4);
+    const int64_t wgs = parts_of(m, 16 * ms) * parts_of(n, kRowsColumns);
+    // Against the tile kernel, which takes as long for one row of tiles as for 256 of them (us, rows kernel and tiles:
+    // 2048 columns, K = 7168, 64 rows: 22 / 73; 256: 50 / 97; 512, 2048 pieces of 64 x 8: 94 / 95; 1024: 205 / 94;
+    // 1000 columns, K = 1024, 1024 rows, 2000 pieces: 18.4 / 19.4).
+    if (wgs > 2048 * parts_of(tiles_of(m, n), 256)) return {0, 0, 0};
+    // Twice the columns, so that A is read half as often, once one column group each makes more than one round of the
+    // CUs (64 rows x 2048: 21.8 us with one, 30.1 with two; 128: 40.5 / 29.8; 256: 77 / 50).
+    const int nt = ms == 4 && wgs > 256 ? 2 : 1;
+    const int64_t slabs = k >= 128 ? k / 128 : 1, at_once = (int64_t)rows_waves(ms * nt) * (ms == 1 ? 4 : 2);
+    const int64_t steps = parts_of(slabs, at_once);
+    return {ms, nt, (int)parts_of(slabs, steps * (ms == 1 ? 4 : 2))};
 }
+
+inline LaunchShape tiles_shape(int64_t m, int64_t n) { return {parts_of(tiles_of(m, n), 8) * 8, 512}; }
 // (every 256-row tile of an expert holds at least 128 of its rows)
 inline LaunchShape grouped_shape(int64_t m_total, int64_t n) {
     return {parts_of(m_total / 128 * parts_of(n, 128), 256) * 256, 512};
@@ -39,7 +48,7 @@ inline LaunchShape grouped_shape(int64_t m_total, int64_t n) {
 
 // Bytes of FP32 scratch that E4M3 output goes through: the 128 columns of a
 // scale belong to 16 workgroups of the rows kernel.
-inline int64_t workspace_bytes(int64_t m, int64_t n, int64_t k) { return rows_form(m, k).ms ? m * n * 4 : 0; }
+inline int64_t workspace_bytes(int64_t m, int64_t n, int64_t k) { return rows_form(m, n, k).ms ? m * n * 4 : 0; }
 
 // Gradient: 8 columns of a row per thread, or panels of 128 x 128.
 constexpr int kBackwardThreads = 256;

@@ -58,7 +58,7 @@ def _close(got, ref, what):
 
 
 SHAPES = [(1, 128, 128), (1, 2048, 1024), (3, 8, 256), (16, 130, 384), (17, 129, 128), (33, 250, 640), (64, 100, 2048),
-          (65, 128, 256), (130, 300, 384), (256, 128, 512), (300, 131, 128), (513, 384, 1152), (1, 1, 128), (2, 7, 7168)]
+          (65, 128, 256), (130, 300, 384), (256, 128, 512), (300, 131, 128), (513, 384, 1152), (1, 1, 128), (2, 7, 7168), (90, 2100, 384), (2100, 521, 256), (4097, 260, 128)]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
@@ -77,7 +77,8 @@ def test_products(m, n, k, act):
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
-@pytest.mark.parametrize("m,n,k", [(1, 128, 256), (5, 256, 1024), (40, 384, 512), (70, 128, 384), (300, 256, 1280)])
+@pytest.mark.parametrize("m,n,k", [(1, 128, 256), (5, 256, 1024), (40, 384, 512), (70, 128, 384), (300, 256, 1280),
+                                   (2300, 640, 256)])
 def test_codes_are_those_of_the_fp32_result(m, n, k, act):
     d = _dev(*_problem(m + n, m, n, k))
     h = fq.fp8_gated_gemm(*d, act, torch.float32).cpu().numpy()
@@ -98,7 +99,7 @@ def test_codes_are_those_of_the_fp32_result(m, n, k, act):
         assert np.all(np.abs(v - v2) <= step) and np.mean(np.abs(v - v2) > 1e-3 * step) < 0.01
 
 
-@pytest.mark.parametrize("m,n,k", [(300, 256, 1280), (96, 384, 384)])
+@pytest.mark.parametrize("m,n,k", [(2300, 640, 256), (4099, 384, 1152)])
 def test_products_are_those_of_the_plain_gemm(m, n, k):
     """The same instructions in the same order: gate and up bit for bit, and H from them with the activation's few
     roundings (the logistic's power, its correction, sum and reciprocal, and two products: 8 last places)."""
