@@ -25,12 +25,14 @@ def mix(x: np.ndarray) -> np.ndarray:
     return x ^ (x >> np.uint64(16))
 
 
-def random_bits(numel: int, place: int, step: int, seed: int) -> np.ndarray:
-    """The 32 random bits of each element of the tensor at `place` of a call."""
+def random_bits(numel: int, place: int, step: int, seed: int, first: int = 0) -> np.ndarray:
+    """The 32 random bits of `numel` elements, from number `first` on, of the tensor at `place` of a call. (They lie in
+    one range of 2^32 element numbers.)"""
     key = np.uint64(seed & 0xFFFFFFFF)
-    for v in (seed >> 32, step & 0xFFFFFFFF, place, 0):
+    for v in (seed >> 32, step & 0xFFFFFFFF, place, first >> 32):
         key = (mix(key) + np.uint64(v)) & _M32
-    return mix(np.arange(numel, dtype=np.uint64) ^ mix(key))
+    at = (np.arange(numel, dtype=np.uint64) + np.uint64(first)) & _M32
+    return mix(at ^ mix(key))
 
 
 def stochastic_e4m3(y: np.ndarray, bits16: np.ndarray) -> np.ndarray:
