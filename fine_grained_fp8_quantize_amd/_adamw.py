@@ -165,7 +165,7 @@ def adamw_step(plan: AdamwPlan, grads, step, lr, beta1: float = 0.9, beta2: floa
     """One AdamW step of a plan's tensors, in place:
     ``m = beta1 m + (1 - beta1) g``, ``v = beta2 v + (1 - beta2) g^2``,
     ``p = p (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)``,
-    one launch for each 56 tensors.
+    one launch for each 64 tensors (56 with 8-bit states).
 
     ``grads``: bf16 or FP32 tensors (all of one dtype), contiguous, of the
     params' shapes; None leaves a tensor as it is. ``step``: 1 in the first

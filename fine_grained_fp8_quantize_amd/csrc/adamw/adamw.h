@@ -11,7 +11,6 @@ namespace fp8q {
 namespace adamw {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTensors = 56;  // per launch: the table travels as a kernel argument of at most 4 KB
 
 struct Options {
     double lr, beta1, beta2, weight_decay;

@@ -2,13 +2,15 @@
 //
 // The step is a stream: with FP32 parameters, bf16 gradients and a bf16 copy
 // it reads and writes 28 bytes an element with 32-bit states, 16.1 with 8-bit
-// ones, and HBM bounds it. A launch takes up to 56 tensors, whose table is a
-// kernel argument (it is captured with the launch, and nothing has to be copied
-// to the device first); a workgroup takes 1024 elements of one of them, a thread
-// four consecutive ones, so that every load and store of a wave is contiguous.
-// (Four times the elements per thread were no faster where there are many,
-// 64M: 311 and 306 us, and their code takes longer to fetch and run where there
-// are few, 56 tensors of 20011: 10.7 and 7.9 us, with 8-bit states 13.7 and 7.5.)
+// ones, and HBM bounds it: 64M elements 305 us, 5.9 TB/s, and 128M in 8 bits 383
+// us, 5.4 TB/s (a copy of 1 GiB: 5.1). A launch takes up to 64 tensors (56 with
+// 8-bit states), whose table is a kernel argument: it is captured with the
+// launch, and nothing has to be copied to the device first. A workgroup takes
+// 1024 elements of one of them, a thread four consecutive ones, so that every
+// load and store of a wave is contiguous. (Four times the elements per thread
+// were no faster where there are many, 64M: 311 and 306 us, and their code takes
+// longer to fetch and run where there are few, 56 tensors of 20011: 10.7 and 7.9
+// us, with 8-bit states 13.7 and 7.5.)
 #include "adamw/adamw.h"
 
 #include <hip/hip_runtime.h>
@@ -57,15 +59,28 @@ constexpr int kBlock = 128;                            // elements that share a 
 static_assert(kBlock == 32 * kVec, "a block is half a wave");
 
 struct Entry {
-    fp8q_adamw_tensor t;
+    void* param;
     const void* grad;
+    void* exp_avg;
+    void* exp_avg_sq;
+    uint16_t* copy;
+    int64_t numel;
+};
+struct Scales {
+    float* exp_avg;
+    float* exp_avg_sq;
 };
 
+// Tensors of a launch: as many as fit 4 KB of kernel arguments, and one lane
+// each for the search of a workgroup's.
+template <bool BITS8>
 struct Table {
-    Entry t[kMaxTensors];
-    int32_t first[kMaxTensors];   // first workgroup of each tensor
-    uint64_t vec;                 // bit i: the arrays of tensor i can be accessed four elements at a time
-    int32_t place;                // place of t[0] in the call
+    static constexpr int kMost = BITS8 ? 56 : 64;
+    Entry t[kMost];
+    Scales s[BITS8 ? kMost : 1];
+    int32_t first[kMost];  // first workgroup of each tensor
+    uint64_t vec;          // bit i: the arrays of tensor i can be accessed four elements at a time
+    int32_t place;         // place of t[0] in the call
     int32_t count;
 };
 
@@ -79,7 +94,8 @@ struct Step {
     float b1, c1, b2, c2, eps;    // beta1, 1 - beta1, beta2, 1 - beta2
     uint32_t seed_lo, seed_hi;
 };
-static_assert(sizeof(Table) + sizeof(Step) <= 4096, "kernel arguments");
+static_assert(sizeof(Table<true>) + sizeof(Step) <= 4096 && sizeof(Table<false>) + sizeof(Step) <= 4096,
+              "kernel arguments");
 
 // A 32-bit mixing step (odd multipliers: the golden ratio and the root of two).
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
@@ -196,13 +212,12 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], const uint32_t 
 }
 
 template <bool P32, bool G32, bool BITS8, Access A>
-__device__ __forceinline__ void chunk(const Entry& e, int64_t base, const Step& s, const Factors& f,
-                                      float grad_scale, uint32_t key) {
+__device__ __forceinline__ void chunk(const Entry& t, const Scales& scales, int64_t base, const Step& s,
+                                      const Factors& f, float grad_scale, uint32_t key) {
     using P = Elem<P32>;
     using G = Elem<G32>;
-    const fp8q_adamw_tensor& t = e.t;
     P* const param = static_cast<P*>(t.param);
-    const G* const grad = static_cast<const G*>(e.grad);
+    const G* const grad = static_cast<const G*>(t.grad);
     const int64_t at = base + threadIdx.x * kVec, rest = t.numel - at;
     const int left = rest < 0 ? 0 : (rest < kVec ? (int)rest : kVec);
     const Four<P> p = load4<P, A>(param, at, left);
@@ -214,8 +229,8 @@ __device__ __forceinline__ void chunk(const Entry& e, int64_t base, const Step& 
         mc = load4<uint8_t, A>(static_cast<const uint8_t*>(t.exp_avg), at, left);
         vc = load4<uint8_t, A>(static_cast<const uint8_t*>(t.exp_avg_sq), at, left);
         if (left > 0) {
-            ms = t.exp_avg_scale[at / kBlock];
-            vs = t.exp_avg_sq_scale[at / kBlock];
+            ms = scales.exp_avg[at / kBlock];
+            vs = scales.exp_avg_sq[at / kBlock];
         }
     } else {
         m = load4<float, A>(static_cast<const float*>(t.exp_avg), at, left);
@@ -264,8 +279,8 @@ __device__ __forceinline__ void chunk(const Entry& e, int64_t base, const Step& 
         store4<uint8_t, A>(static_cast<uint8_t*>(t.exp_avg), at, left, bytes_of(cm));
         store4<uint8_t, A>(static_cast<uint8_t*>(t.exp_avg_sq), at, left, bytes_of(cv));
         if (left > 0 && at % kBlock == 0) {
-            t.exp_avg_scale[at / kBlock] = sm;
-            t.exp_avg_sq_scale[at / kBlock] = sv;
+            scales.exp_avg[at / kBlock] = sm;
+            scales.exp_avg_sq[at / kBlock] = sv;
         }
     } else {
         store4<float, A>(static_cast<float*>(t.exp_avg), at, left, m);
@@ -274,13 +289,14 @@ __device__ __forceinline__ void chunk(const Entry& e, int64_t base, const Step& 
 }
 
 template <bool P32, bool G32, bool BITS8>
-__global__ __launch_bounds__(kThreads) void step_kernel(Table table, Step s) {
+__global__ __launch_bounds__(kThreads) void step_kernel(Table<BITS8> table, Step s) {
     const float grad_scale = s.grad_scale ? *s.grad_scale : 1.0f;
     if (!(__builtin_fabsf(grad_scale) < __builtin_inff())) return;
     const int lane = threadIdx.x & 63;
     const int mine = lane < table.count ? table.first[lane] : 0x7FFFFFFF;
     const int i = __builtin_amdgcn_readfirstlane(__popcll(__ballot(mine <= (int)blockIdx.x)) - 1);
     const Entry t = table.t[i];
+    const Scales scales = table.s[BITS8 ? i : 0];
     const int64_t base = (int64_t)((int)blockIdx.x - table.first[i]) * kChunk;
     Factors f = s.f;
     uint32_t step32 = (uint32_t)s.step;
@@ -295,29 +311,67 @@ __global__ __launch_bounds__(kThreads) void step_kernel(Table table, Step s) {
         key = mix(mix(mix(s.seed_lo) + s.seed_hi) + step32);
         key = mix(mix(key + (uint32_t)(table.place + i)) + (uint32_t)(base >> 32));
     }
-    if (((table.vec >> i) & 1) && base + kChunk <= t.t.numel)
-        chunk<P32, G32, BITS8, Access::kWhole>(t, base, s, f, grad_scale, key);
+    if (((table.vec >> i) & 1) && base + kChunk <= t.numel)
+        chunk<P32, G32, BITS8, Access::kWhole>(t, scales, base, s, f, grad_scale, key);
     else if ((table.vec >> i) & 1)
-        chunk<P32, G32, BITS8, Access::kTail>(t, base, s, f, grad_scale, key);
+        chunk<P32, G32, BITS8, Access::kTail>(t, scales, base, s, f, grad_scale, key);
     else
-        chunk<P32, G32, BITS8, Access::kSingle>(t, base, s, f, grad_scale, key);
+        chunk<P32, G32, BITS8, Access::kSingle>(t, scales, base, s, f, grad_scale, key);
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-void launch(const Table& table, const Step& s, const Options& o, int64_t blocks, hipStream_t stream) {
+template <bool BITS8>
+void launch(const Table<BITS8>& table, const Step& s, const Options& o, int64_t blocks, hipStream_t stream) {
     const dim3 grid((unsigned)blocks), block(kThreads);
-    const int which = (o.param_f32 ? 4 : 0) + (o.grad_f32 ? 2 : 0) + (o.bits8 ? 1 : 0);
-    switch (which) {
-        case 0: hipLaunchKernelGGL((step_kernel<false, false, false>), grid, block, 0, stream, table, s); break;
-        case 1: hipLaunchKernelGGL((step_kernel<false, false, true>), grid, block, 0, stream, table, s); break;
-        case 2: hipLaunchKernelGGL((step_kernel<false, true, false>), grid, block, 0, stream, table, s); break;
-        case 3: hipLaunchKernelGGL((step_kernel<false, true, true>), grid, block, 0, stream, table, s); break;
-        case 4: hipLaunchKernelGGL((step_kernel<true, false, false>), grid, block, 0, stream, table, s); break;
-        case 5: hipLaunchKernelGGL((step_kernel<true, false, true>), grid, block, 0, stream, table, s); break;
-        case 6: hipLaunchKernelGGL((step_kernel<true, true, false>), grid, block, 0, stream, table, s); break;
-        default: hipLaunchKernelGGL((step_kernel<true, true, true>), grid, block, 0, stream, table, s); break;
+    if (o.param_f32) {
+        if (o.grad_f32)
+            hipLaunchKernelGGL((step_kernel<true, true, BITS8>), grid, block, 0, stream, table, s);
+        else
+            hipLaunchKernelGGL((step_kernel<true, false, BITS8>), grid, block, 0, stream, table, s);
+    } else {
+        if (o.grad_f32)
+            hipLaunchKernelGGL((step_kernel<false, true, BITS8>), grid, block, 0, stream, table, s);
+        else
+            hipLaunchKernelGGL((step_kernel<false, false, BITS8>), grid, block, 0, stream, table, s);
     }
+}
+
+template <bool BITS8>
+hipError_t launch_tables(int32_t count, const fp8q_adamw_tensor* tensors, const void* const* grads, const Step& s,
+                         const Options& o, hipStream_t stream) {
+    Table<BITS8> table;
+    for (int32_t at = 0; at < count;) {
+        // consecutive tensors, so that a place is known from the first one's
+        table.place = at;
+        table.count = 0;
+        table.vec = 0;
+        int64_t blocks = 0;
+        while (table.count < Table<BITS8>::kMost && at < count) {
+            const fp8q_adamw_tensor& t = tensors[at];
+            const void* const grad = grads[at];
+            const int64_t need = grad ? (t.numel + kChunk - 1) / kChunk : 0;
+            if (!launchable({blocks + need, kThreads})) {
+                if (table.count == 0) return hipErrorInvalidValue;
+                break;
+            }
+            const int j = table.count++;
+            ++at;
+            table.t[j] = Entry{t.param, grad, t.exp_avg, t.exp_avg_sq, t.copy, t.numel};
+            if (BITS8) table.s[j] = Scales{t.exp_avg_scale, t.exp_avg_sq_scale};
+            table.first[j] = (int32_t)blocks;
+            const int states = BITS8 ? 4 : 16;
+            const bool vec = aligned(t.param, o.param_f32 ? 16 : 8) && aligned(grad, o.grad_f32 ? 16 : 8) &&
+                             aligned(t.exp_avg, states) && aligned(t.exp_avg_sq, states) && aligned(t.copy, 8);
+            if (vec) table.vec |= 1ULL << j;
+            blocks += need;
+        }
+        if (blocks == 0) continue;
+        launch<BITS8>(table, s, o, blocks, stream);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
@@ -332,38 +386,8 @@ hipError_t launch_step(int32_t count, const fp8q_adamw_tensor* tensors, const vo
     s.b2 = (float)o.beta2; s.c2 = (float)(1.0 - o.beta2);
     s.eps = o.eps;
     s.seed_lo = (uint32_t)o.seed; s.seed_hi = (uint32_t)(o.seed >> 32);
-    Table table;
-    for (int32_t at = 0; at < count;) {
-        // consecutive tensors, so that a place is known from the first one's
-        const int32_t n = std::min(count - at, kMaxTensors);
-        table.place = at;
-        table.count = 0;
-        table.vec = 0;
-        int64_t blocks = 0;
-        while (table.count < n) {
-            const fp8q_adamw_tensor& t = tensors[at];
-            const void* const grad = grads[at];
-            const int64_t need = grad ? (t.numel + kChunk - 1) / kChunk : 0;
-            if (!launchable({blocks + need, kThreads})) {
-                if (table.count == 0) return hipErrorInvalidValue;
-                break;
-            }
-            const int j = table.count++;
-            ++at;
-            table.t[j] = Entry{t, grad};
-            table.first[j] = (int32_t)blocks;
-            const int states = o.bits8 ? 4 : 16;
-            const bool vec = aligned(t.param, o.param_f32 ? 16 : 8) && aligned(grad, o.grad_f32 ? 16 : 8) &&
-                             aligned(t.exp_avg, states) && aligned(t.exp_avg_sq, states) && aligned(t.copy, 8);
-            if (vec) table.vec |= 1ULL << j;
-            blocks += need;
-        }
-        if (blocks == 0) continue;
-        launch(table, s, o, blocks, stream);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    return o.bits8 ? launch_tables<true>(count, tensors, grads, s, o, stream)
+                   : launch_tables<false>(count, tensors, grads, s, o, stream);
 }
 
 }  // namespace adamw

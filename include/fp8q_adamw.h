@@ -75,7 +75,7 @@ typedef struct fp8q_adamw_tensor {
  *             the step leave every array as it was.
  * Shapes: count >= 0, numel >= 0, step >= 1 (a device step below 1 acts as 1),
  *         0 <= beta1, beta2 < 1, eps >= 0.
- * One launch for each 56 tensors. count == 0, or no elements: FP8Q_OK.
+ * One launch for each 64 tensors (56 with 8-bit states). count == 0, or no elements: FP8Q_OK.
  * Errors: FP8Q_ERR_NULL, FP8Q_ERR_SHAPE (also for the options' ranges),
  *         FP8Q_ERR_ALIGN, FP8Q_ERR_ENUM, FP8Q_ERR_HIP. Everything is checked
  *         before the first launch.
