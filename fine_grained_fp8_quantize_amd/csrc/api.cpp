@@ -85,6 +85,13 @@ bool scale_span_ok(int64_t rows, int64_t ld) { return rows <= 0 || ld < FP8Q_MAX
 
 }  // namespace
 
+namespace fp8q {
+int debug_segments(int32_t groups, const int32_t* group_offsets, const int32_t* group_rows, int64_t total,
+                   hipStream_t stream) {
+    return debug_checks() ? check_segments_on_host(groups, group_offsets, group_rows, total, stream) : FP8Q_OK;
+}
+}  // namespace fp8q
+
 extern "C" {
 
 const char* fp8q_status_string(int status) {

@@ -94,8 +94,9 @@ int fp8_gated_gemm(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t ld
                                out_dtype, out_scale, ld_os, gate_up, ldg);
     if (st != FP8Q_OK) return st;
     if (!is_aligned(workspace, 16)) return FP8Q_ERR_ALIGN;
+    const RowsForm f = mul_limit(m, n, kMaxBytes) < 0 ? RowsForm{} : rows_form(m, n, k);
     if (mul_limit(m, n, kMaxBytes) < 0 || !launchable(tiles_shape(m, n)) ||
-        !launchable({parts_of(n, kRowsColumns), 1024}))
+        (f.ms != 0 && !launchable({parts_of(n, kRowsColumns * f.nt), 64 * f.waves})))
         return FP8Q_ERR_SHAPE;
     const GatedArgs p = gated_args(m, n, k, a, lda, a_scale, ld_as, b, ldb, stride_b, b_scale, ld_bs, stride_bs, act,
                                    out, ldo, out_dtype, out_scale, ld_os, gate_up, ldg);
@@ -123,6 +124,8 @@ int fp8_grouped_gated_gemm(int32_t groups, const int32_t* group_offsets, const i
     if ((k > 0 && stride_e % 16 != 0) || !is_aligned(group_offsets, 4) || !is_aligned(group_rows, 4))
         return FP8Q_ERR_ALIGN;
     if (!launchable(grouped_shape(m_total, n))) return FP8Q_ERR_SHAPE;
+    const int seg = debug_segments(groups, group_offsets, group_rows, m_total, stream);
+    if (seg != FP8Q_OK) return seg;
     GatedArgs p = gated_args(m_total, n, k, a, lda, a_scale, ld_as, b, ldb, stride_b, b_scale, ld_bs, stride_bs, act,
                              out, ldo, out_dtype, out_scale, ld_os, gate_up, ldg);
     p.g.groups = groups; p.g.group_offsets = group_offsets; p.g.group_rows = group_rows;

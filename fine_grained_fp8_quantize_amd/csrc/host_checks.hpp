@@ -11,6 +11,11 @@ namespace fp8q {
 // (defined in api.cpp, which owns the thread's last error).
 int hip_status(hipError_t e);
 
+// With FP8Q_DEBUG=1: checks the segment arrays of a grouped call on the host (a
+// synchronizing copy); otherwise FP8Q_OK (defined in api.cpp).
+int debug_segments(int32_t groups, const int32_t* group_offsets, const int32_t* group_rows, int64_t total,
+                   hipStream_t stream);
+
 inline bool is_aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // A grid of more than 2^31 - 1 blocks is not launchable.

@@ -74,7 +74,8 @@ typedef struct fp8q_adamw_tensor {
  * grad_scale  DEVICE FP32 [1] or NULL for 1. A scale that is not finite makes
  *             the step leave every array as it was.
  * Shapes: count >= 0, numel >= 0, step >= 1 (a device step below 1 acts as 1),
- *         0 <= beta1, beta2 < 1, eps >= 0.
+ *         0 <= beta1, beta2 < 1, eps >= 0 (with 0, elements whose moments are
+ *         all zero become NaN: 0 / 0).
  * One launch for each 64 tensors (56 with 8-bit states). count == 0, or no elements: FP8Q_OK.
  * Errors: FP8Q_ERR_NULL, FP8Q_ERR_SHAPE (also for the options' ranges),
  *         FP8Q_ERR_ALIGN, FP8Q_ERR_ENUM, FP8Q_ERR_HIP. Everything is checked

@@ -48,11 +48,12 @@ def test_gated_forms(rules):
     import test_gpu_gated as gpu
     want = {(1, 1), (2, 1), (4, 1), (4, 2), (0, 0)}
     assert {tuple(rules("rows_form", *s, size=3)[:2]) for s in gpu.SHAPES} == want
-    for m in (1, 16, 17, 32, 33, 64, 65, 256, 1000, 5000, 1 << 20):
+    for m in (1, 16, 17, 32, 33, 64, 65, 256, 1000, 5000, 1 << 20, 1 << 23, 1 << 30):
         for n in (1, 8, 128, 1000, 2048, 1 << 20):
             for k in (0, 128, 1024, 7168, 1 << 20):
                 ms, nt, waves = rules("rows_form", m, n, k, size=3)
                 assert (ms, nt) in want
+                assert ms == 0 or m <= 16 * ms * 65535
                 if ms:
                     assert 1 <= waves <= (8 if ms * nt >= 8 else 16) and waves * nt * ms <= 64  # KB of LDS
 

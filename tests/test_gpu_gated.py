@@ -397,3 +397,17 @@ def test_refusals():
         fq.fp8_gated_backward(x[:, :100], gu[:, :200].contiguous())
     with pytest.raises(E, match="dh must be bfloat16"):
         fq.fp8_gated_backward(x.float(), gu)
+
+
+def test_debug_checks_of_the_segments(monkeypatch):
+    """FP8Q_DEBUG=1: segment arrays that break the contract are refused before the launch."""
+    m, n, k = 256, 128, 128
+    a, a_s, b, b_s = _problem(1, m, n, k, (2,))
+    d = _dev(a, a_s, b, b_s)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    monkeypatch.setenv("FP8Q_DEBUG", "1")
+    fq.fp8_grouped_gated_gemm(i32(0, 128, 256), i32(5, 128), *d)
+    for off, rows in (((0, 64, 256), (5, 5)), ((0, 256, 128), (5, 5)), ((0, 128, 128), (5, 0)), ((128, 128, 256), (0, 5)),
+                      ((0, 128, 256), (129, 5)), ((0, 128, 256), (-1, 5))):
+        with pytest.raises(fq.Fp8qError, match="status 2"):
+            fq.fp8_grouped_gated_gemm(i32(*off), i32(*rows), *d)
