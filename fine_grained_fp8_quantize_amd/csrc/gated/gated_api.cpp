@@ -94,10 +94,8 @@ int fp8_gated_gemm(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t ld
                                out_dtype, out_scale, ld_os, gate_up, ldg);
     if (st != FP8Q_OK) return st;
     if (!is_aligned(workspace, 16)) return FP8Q_ERR_ALIGN;
-    const RowsForm f = mul_limit(m, n, kMaxBytes) < 0 ? RowsForm{} : rows_form(m, n, k);
-    if (mul_limit(m, n, kMaxBytes) < 0 || !launchable(tiles_shape(m, n)) ||
-        (f.ms != 0 && !launchable({parts_of(n, kRowsColumns * f.nt), 64 * f.waves})))
-        return FP8Q_ERR_SHAPE;
+    // (the rows kernel is chosen for a few thousand workgroups at the most)
+    if (mul_limit(m, n, kMaxBytes) < 0 || !launchable(tiles_shape(m, n))) return FP8Q_ERR_SHAPE;
     const GatedArgs p = gated_args(m, n, k, a, lda, a_scale, ld_as, b, ldb, stride_b, b_scale, ld_bs, stride_bs, act,
                                    out, ldo, out_dtype, out_scale, ld_os, gate_up, ldg);
     const bool enough = workspace && workspace_bytes >= fp8q::gated::workspace_bytes(m, n, k);

@@ -30,9 +30,10 @@ inline RowsForm rows_form(int64_t m, int64_t n, int64_t k) {
     const int64_t wgs = parts_of(m, 16 * ms) * parts_of(n, kRowsColumns);
     // Against the tile kernel, which takes as long for one row of tiles as for 256 of them (us, rows kernel and tiles:
     // 2048 columns, K = 7168, 64 rows: 22 / 73; 256: 50 / 97; 512, 2048 pieces of 64 x 8: 94 / 95; 1024: 205 / 94;
-    // 1000 columns, K = 1024, 1024 rows, 2000 pieces: 18.4 / 19.4).
+    // 1000 columns, K = 1024, 1024 rows, 2000 pieces: 18.4 / 19.4; K = 7168, 16384 columns, 2048 pieces, 1 row: 56 / 81,
+    // 16: 75 / 81, 32: 102 / 83; 24576 columns, 1 row: 82 / 86, 16: 111 / 87).
     // (A launch has fewer than 2^16 workgroups along the rows.)
-    if (wgs > 2048 * parts_of(tiles_of(m, n), 256) || m > 1 << 20) return {0, 0, 0};
+    if (wgs > (ms == 2 ? 1536 : 2048) * parts_of(tiles_of(m, n), 256) || m > 1 << 20) return {0, 0, 0};
     // Twice the columns, so that A is read half as often, once one column group each makes more than one round of the
     // CUs (64 rows x 2048: 21.8 us with one, 30.1 with two; 128: 40.5 / 29.8; 256: 77 / 50).
     const int nt = ms == 4 && wgs > 256 ? 2 : 1;
