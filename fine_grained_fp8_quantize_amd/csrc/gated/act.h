@@ -9,16 +9,17 @@ namespace fp8q {
 namespace {
 
 // 1 / (1 + e^-w). e^-w = 2^t (1 + d ln 2) with t the rounded and d the rest of
-// -w log2(e): without d the result would lose |w| places in the last bit. The
-// exponent stays below 126, where the result is 0 for every purpose: an
-// infinite power would make the correction a NaN.
+// -w log2(e): without d the result would lose |w| places in the last bit. Past
+// +-256 the result is 0 or 1 in any case, and d would be the difference of two
+// infinities. (An infinite power gives exactly 0, whatever w's factor is.)
 __device__ __forceinline__ float logistic(float w) {
     constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
     constexpr float kLog2eRest = 1.92596299112661746887e-8f;  // log2(e) - kLog2e
+    w = __builtin_amdgcn_fmed3f(w, -256.0f, 256.0f);
     const float t = -w * kLog2e;
     const float d = __builtin_fmaf(-w, kLog2eRest, __builtin_fmaf(-w, kLog2e, -t));
-    const float e = __builtin_amdgcn_exp2f(__builtin_fminf(t, 126.0f));
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, d * kLn2, e));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_amdgcn_rcpf(1.0f + e * __builtin_fmaf(d, kLn2, 1.0f));
 }
 
 // Both activations are g times a logistic function: sigmoid(g), or, as (1 +

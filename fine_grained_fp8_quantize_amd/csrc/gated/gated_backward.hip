@@ -37,15 +37,18 @@ __device__ __forceinline__ Eight load8(const uint16_t* p, int64_t left) {
 
 // e^-w is taken as 2^(-w log2 e) with one rounded product: |w| 2^-24 of it,
 // where the bf16 of the gate is |w| 2^-9. An infinite power gives a share of 0.
+// From +-16 on gelu's share is 0 or 1 exactly: the powers of g that would
+// overflow are taken of that (w keeps a NaN, and the infinities).
 __device__ __forceinline__ void gradients(int act, float dh, float g, float u, float& dg, float& du) {
     constexpr float kLog2e = 1.44269504088896340736f;
-    float w = g, by = 1.0f;
+    float w = g, by = 1.0f, c = g;
     if (act != FP8Q_ACT_SILU) {
-        w = kGeluScale * __builtin_fmaf(kGeluCube * g * g, g, g);
-        by = kGeluScale * __builtin_fmaf(3.0f * kGeluCube * g, g, 1.0f);
+        c = __builtin_amdgcn_fmed3f(g, -16.0f, 16.0f);
+        w = kGeluScale * __builtin_fmaf(kGeluCube * c * c, c, g);
+        by = kGeluScale * __builtin_fmaf(3.0f * kGeluCube * c, c, 1.0f);
     }
     const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-w * kLog2e));
-    const float r = g * (1.0f - s);
+    const float r = c * (1.0f - s);
     const float ds = dh * s;
     du = ds * g;
     dg = (ds * u) * (act != FP8Q_ACT_SILU ? __builtin_fmaf(r, by, 1.0f) : 1.0f + r);

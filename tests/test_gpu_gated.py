@@ -130,6 +130,42 @@ def test_extremes_of_the_activation():
         assert np.all(np.abs(h - want) <= (16 + 4 * (act == "gelu") * np.minimum(w, 88)) * U * np.abs(want) + 1e-30), act
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gates_of_any_size(act):
+    """Gates whose powers pass FP32: the activation is g or 0 there, its slope 1 or 0."""
+    k, n = 128, 128
+    big = np.array([17.0, 90.0, 300.0, 5e12, 1e13, 3e19, 1e25, 1e38], np.float32)
+    gates = np.concatenate([big, -big])
+    a = np.full((16, k), 0x38, np.uint8)          # 1.0
+    b = np.zeros((2, n, k), np.uint8)
+    b[0, :, 0], b[1, :, 0] = 0x38, 0x38
+    b_s = np.array([1.0, 2e-38], np.float32).reshape(2, 1, 1)
+    d = _dev(np.repeat(a, 5, 0), np.tile(gates, 5).reshape(1, 80), b, b_s)
+    x = gates.astype(np.float64)
+    with np.errstate(over="ignore"):
+        want = model.act(act, x) * x * float(b_s[1, 0, 0])
+    # (act(-17) is the smallest that is not 0 for both: 7e-7 of it; gelu's argument as in the test above)
+    room = (16 + 4 * 88) * U * np.abs(want) + 1e-38
+    for m in (16, 80):
+        h = _finite(fq.fp8_gated_gemm(d[0][:m], d[1][:, :m], *d[2:], act, torch.float32))
+        assert np.all(np.abs(h - np.tile(want, m // 16)[:, None]) <= np.tile(room, m // 16)[:, None]), m
+    for m, cols in ((16, 128), (128, 128)):
+        g = torch.from_numpy(gates).to(torch.bfloat16).cuda().repeat(m // 16)[:, None].expand(m, cols)
+        one = torch.full((m, cols), 0.5, dtype=torch.bfloat16, device="cuda")
+        got = _finite(fq.fp8_gated_backward(one, torch.cat((g, one), 1), act, torch.bfloat16))
+        y = _finite(g)[:16, :1]
+        with np.errstate(over="ignore"):
+            dg, du = model.gradients(act, np.full_like(y, 0.5), y, np.full_like(y, 0.5))
+        want2 = np.tile(np.concatenate((np.repeat(dg, cols, 1), np.repeat(du, cols, 1)), 1), (m // 16, 1))
+        # bf16's rounding, and the slope's terms past -17 of either sign: 17 * 4e-8 and less
+        assert np.all(np.abs(got - want2) <= 2.0 ** -8 * 1.001 * np.abs(want2) + 16 * U * 17), m
+        outs = fq.fp8_gated_backward(one, torch.cat((g, one), 1), act, transposed=m == 128)
+        for t in outs[1::2]:
+            assert torch.isfinite(t).all()
+        for t in outs[0::2]:
+            assert ((t.view(torch.uint8) & 127) != 127).all()
+
+
 def test_strides_and_padded_operands():
     m, n, k = 100, 200, 256
     a, a_s, b, b_s = _problem(9, m, n, k)
