@@ -130,7 +130,7 @@ def fp4_gemv_mx(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, n: int 
     ``[tokens][topk][k]`` where every route has a row of its own, and a stack of
     the experts' matrices ``w[E][..]``; route ``(t, j)`` goes through expert
     ``ids[t][j] - first``. Returns ``[tokens][topk][n]``, zeros for ids outside
-    ``[first, first + E)``. Up to 4096 routes, topk up to 32.
+    ``[first, first + E)`` (all of them on a rank with E = 0). Up to 4096 routes, topk up to 32.
     """
     return _gemv(x, w, w_scale, n, ids, first, False, None, out_dtype, out, stream, "fp4_gemv_mx")
 

@@ -31,7 +31,7 @@ int run(const Args& p, int out_dtype, hipStream_t stream) {
     if (p.tokens == 0 || p.topk == 0 || p.n == 0) return FP8Q_OK;
     if (p.tokens > kMaxRows) return FP8Q_ERR_SHAPE;
     if (p.ids) {
-        if (p.topk > gemv::kMaxTopk || p.tokens * p.topk > gemv::kMaxRoutes || p.experts < 1 ||
+        if (p.topk > gemv::kMaxTopk || p.tokens * p.topk > gemv::kMaxRoutes || p.experts < 0 ||
             p.experts > gemv::kMaxExperts || p.first < 0 || (int64_t)p.first + p.experts > 0x7FFFFFFFLL)
             return FP8Q_ERR_SHAPE;
         if (!is_aligned(p.ids, 4)) return FP8Q_ERR_ALIGN;
@@ -42,7 +42,7 @@ int run(const Args& p, int out_dtype, hipStream_t stream) {
     const int64_t routes = p.tokens * p.topk;
     if (p.ld_y < p.n || mul_limit(routes, p.ld_y, kMaxBytes / 4) < 0) return FP8Q_ERR_SHAPE;
     if (!is_aligned(p.y, p.f32 ? 4 : 2)) return FP8Q_ERR_ALIGN;
-    if (p.k > 0) {
+    if (p.k > 0 && p.experts > 0) {
         if (!p.x || !p.w || !p.s) return FP8Q_ERR_NULL;
         const int64_t kt = ceil_div(p.k, mx4::kTileK), rt = ceil_div(p.n, mx4::kTileRows);
         if (!tiles_ok(kt, p.ld_w, rt, mx4::kTileBytes) ||
@@ -60,6 +60,7 @@ int run(const Args& p, int out_dtype, hipStream_t stream) {
     if (!launchable({gemv::column_groups(p.n, p.gated), 64 * gemv::max_waves(1)})) return FP8Q_ERR_SHAPE;
     Args a = p;
     a.kt = (int32_t)ceil_div(p.k, mx4::kTileK);
+    if (a.experts == 0) a.k = a.kt = 0;  // zeros: nothing is read but the ids
     a.x_vec = is_aligned(p.x, 16) && p.ld_x % 8 == 0 && p.ld_xj % 8 == 0 && p.k % 8 == 0;
     a.y_vec = is_aligned(p.y, p.f32 ? 16 : 8) && p.ld_y % 4 == 0;
     return hip_status(gemv::launch(a, stream));

@@ -40,8 +40,9 @@ extern "C" {
  * (64 with more than 32 rows, 32 with more than 16); products of many rows
  * belong to fp4_gemm_mx and fp4_grouped_gemm_mx. The sums are taken in a fixed
  * order; a row's result does not depend on the other rows.
- * k == 0 writes zeros (x and weights may be NULL). tokens, topk or n == 0:
- * returns FP8Q_OK without launching.
+ * k == 0, and with ids experts == 0 (a rank without any), write zeros (x and
+ * weights may be NULL). tokens, topk or n == 0: returns FP8Q_OK without
+ * launching.
  * Limits: n <= FP4Q_MAX_GEMM_ROWS, k <= FP4Q_MAX_GEMM_K, 64 * 65535 rows;
  *         with ids FP4Q_GEMV_MAX_EXPERTS experts, _MAX_ROUTES routes, _MAX_TOPK.
  * Errors: FP8Q_ERR_NULL, FP8Q_ERR_SHAPE, FP8Q_ERR_ALIGN (w not 16-byte, w_scale

@@ -52,7 +52,7 @@ R = dict(ids=I, topk=3, experts=4)
     (dict(topk=2), ERR_SHAPE), (dict(experts=2), ERR_SHAPE), (dict(tokens=64 * 65535 + 1), ERR_SHAPE),
     (dict(n=1 << 31, ld_y=1 << 31), ERR_SHAPE), (dict(k=1 << 38), ERR_SHAPE), (dict(ld_y=1 << 61), ERR_SHAPE),
     (dict(ld_x=1 << 61), ERR_SHAPE), (dict(ld_w=1 << 41), ERR_SHAPE), (dict(R, ids=I + 2), ERR_ALIGN),
-    (dict(R, topk=33), ERR_SHAPE), (dict(R, tokens=2000), ERR_SHAPE), (dict(R, experts=0), ERR_SHAPE),
+    (dict(R, topk=33), ERR_SHAPE), (dict(R, tokens=2000), ERR_SHAPE), (dict(R, experts=-1), ERR_SHAPE), (dict(R, experts=0, y=0), ERR_NULL),
     (dict(R, experts=1025), ERR_SHAPE), (dict(R, first=-1), ERR_SHAPE), (dict(R, first=0x7FFFFFFE), ERR_SHAPE),
     (dict(R, tokens=0), OK), (dict(R, sw=1 << 60), ERR_SHAPE)])
 def test_refusals(kw, want):

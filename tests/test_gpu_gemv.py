@@ -117,6 +117,19 @@ def test_experts(tokens, topk, experts, own_rows):
     assert torch.equal(fq.fp4_gated_gemv_mx(x, q, s, n, "silu", d, first), got.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("n", [16, 40, 2050])
+def test_a_rank_without_experts(n):
+    kt, rt = 2, -(-n // 16)
+    x = torch.full((5, 256), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ids = torch.arange(15, dtype=torch.int32, device="cuda").reshape(5, 3) - 2
+    for lead, f in (((0,), fq.fp4_gemv_mx), ((0, 2), fq.fp4_gated_gemv_mx)):
+        q = torch.zeros((*lead, kt, rt, 1024), dtype=torch.uint8, device="cuda")
+        s = torch.zeros((*lead, 1, rt, 64), dtype=torch.int32, device="cuda")
+        out = torch.full((5, 3, n + 4), float("nan"), device="cuda")
+        f(x, q, s, n, ids=ids, first=4, out_dtype=torch.float32, out=out[..., :n])
+        assert (out[..., :n] == 0).all() and torch.isnan(out[..., n:]).all()
+
+
 def test_special_values_stay_in_their_row_and_column():
     rng = np.random.default_rng(4)
     m, n, k = 5, 40, 300
