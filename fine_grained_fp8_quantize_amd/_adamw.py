@@ -38,8 +38,8 @@ def _library():
 
 class AdamwPlan:
     """The tensors of an optimizer, checked once by :func:`adamw_plan`. It keeps
-    the tensors alive; their storage must stay where it is. One thread at a time
-    steps a plan."""
+    their storage alive and steps what is there: after a tensor has been given
+    other storage, make a new plan. One thread at a time steps a plan."""
 
     __slots__ = ("device", "shapes", "param_dtype", "state_bits", "_entries", "_tensors", "_grads")
 
@@ -120,7 +120,8 @@ def adamw_plan(params, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale
                              _address(sq_s[i]), _address(copies[i]), p.numel())
     if _overlaps(every):
         raise Fp8qError("two of the plan's tensors share memory")
-    return AdamwPlan(device, [p.shape for p in params], dtype, bits, entries, every)
+    # (views of their own: a parameter that is given other storage leaves this one to the plan)
+    return AdamwPlan(device, [p.shape for p in params], dtype, bits, entries, [t.detach() for t in every])
 
 
 _dtype_of, _shape_of = torch.Tensor.dtype.__get__, torch.Tensor.shape.__get__

@@ -267,6 +267,20 @@ def test_streams_and_odd_calls():
     fq.adamw_step(empty, [], 1, 1e-3)
 
 
+def test_a_plan_keeps_its_storage():
+    """A parameter that is given other storage: the plan's step changes what it was made for, which it keeps alive."""
+    t = Tensors([4096, 100])
+    plan = fq.adamw_plan(t.tp, t.tm, t.tv, copies=t.tc)
+    before = [p.clone() for p in t.tp]
+    old = t.tp[0].detach()
+    t.tp[0].data = before[0].clone()
+    assert t.tp[0].data_ptr() != old.data_ptr()
+    del t.tm, t.tv
+    fq.adamw_step(plan, t.tg, 1, **HYPER)
+    assert torch.equal(t.tp[0], before[0]) and not torch.equal(old, before[0])
+    assert torch.equal(t.tc[0], old.to(torch.bfloat16))
+
+
 def test_refusals():
     f = lambda n, dt=torch.float32: torch.zeros(n, dtype=dt, device="cuda")  # noqa: E731
     E = fq.Fp8qError
