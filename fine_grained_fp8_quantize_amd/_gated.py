@@ -65,7 +65,10 @@ def _matrix_out(t, shape, dtypes, dev, stream, what: str) -> torch.Tensor:
     """An output matrix: new when absent, checked otherwise."""
     if t is None:
         return _new(shape, dtypes[0], dev, stream)
-    _check_tensor(t, shape, dtypes, what)
+    if dtypes[0] is torch.float32:
+        _f32(t, shape, what)
+    else:
+        _check_tensor(t, shape, dtypes, what)
     return t
 
 
