@@ -195,7 +195,11 @@ __device__ __forceinline__ int wave_inclusive_sum(int v) {
 
 // Tile `slot` of the grouped order (see above), or false past the last tile.
 // Every lane of the wave must take part.
-template <int BN>
+// EVEN (the gated products): an expert's 64-row quarters are dealt out evenly
+// to its m-tiles, as many of them, unless the last is of padding only: no tile
+// is full where the one beside it is nearly empty (32 experts, 2 x 2048 x 7168,
+// us: 384 rows each 440 -> 387, 8192 rows at random 389 -> 368 and 327 -> 322).
+template <int BN, bool EVEN = false>
 __device__ __forceinline__ bool grouped_slot(const Params& p, int slot, TileRows& t) {
     const int tiles_n = (int)((p.n + BN - 1) / BN);
     for (int base = 0; base < p.groups; base += 64) {
@@ -212,12 +216,20 @@ __device__ __forceinline__ bool grouped_slot(const Params& p, int slot, TileRows
             const int k = x.tiles;
             const int tn = slot / k, mt = slot % k;
             const int end = x.beg + max(p.group_offsets[e + 1] - x.beg, 0);
-            t.m0 = x.beg + (int64_t)mt * kBM;
-            // offsets that break the contract must not move stores outside C
-            if (t.m0 < 0 || t.m0 >= p.m) return false;
-            t.row_hi = min(min((int64_t)end, t.m0 + kBM), p.m);
             const int seg = end - x.beg;
             const int real = p.group_rows ? min(max(p.group_rows[e], 0), seg) : seg;
+            t.m0 = x.beg + (int64_t)mt * kBM;
+            int rows = kBM;
+            if constexpr (EVEN) {
+                if (real > (k - 1) * kBM) {
+                    const int quarters = (seg + 63) / 64, first = mt * quarters / k;
+                    t.m0 = x.beg + (int64_t)first * 64;
+                    rows = ((mt + 1) * quarters / k - first) * 64;
+                }
+            }
+            // offsets that break the contract must not move stores outside C
+            if (t.m0 < 0 || t.m0 >= p.m) return false;
+            t.row_hi = min(min((int64_t)end, t.m0 + rows), p.m);
             t.real_end = x.beg + (int64_t)real;
             t.n0 = (int64_t)tn * BN;
             t.b = p.b + e * p.stride_b;
@@ -273,7 +285,7 @@ __device__ __forceinline__ TailSplit tail_split(const Params& p) {
 // evenly over the XCDs and panel reuse stays inside one L2. The grid is a
 // multiple of 256 blocks, so this is a bijection onto its slots (the pieces
 // of a split last round fill at most the 256 slots of that round).
-template <int BN>
+template <int BN, bool EVEN = false>
 __device__ __forceinline__ bool grouped_tile(const Params& p, TileRows& t) {
     const int q = (int)(blockIdx.x >> 3);
     const int slot = ((q >> 5) << 8) + ((int)(blockIdx.x & 7) << 5) + (q & 31);
@@ -283,7 +295,7 @@ __device__ __forceinline__ bool grouped_tile(const Params& p, TileRows& t) {
             const int u = slot - ts.first;
             if (u >= ts.tiles * ts.split) return false;
             const int r = u % ts.tiles, i = u / ts.tiles;
-            if (!grouped_slot<BN>(p, ts.first + r, t)) return false;
+            if (!grouped_slot<BN, EVEN>(p, ts.first + r, t)) return false;
             const int slabs = t.slabs;
             t.slab0 = i * slabs / ts.split;
             t.slabs = (i + 1) * slabs / ts.split - t.slab0;
@@ -292,7 +304,7 @@ __device__ __forceinline__ bool grouped_tile(const Params& p, TileRows& t) {
             return true;
         }
     }
-    return grouped_slot<BN>(p, slot, t);
+    return grouped_slot<BN, EVEN>(p, slot, t);
 }
 
 // Grouped-over-K tiles (MoE Wgrad): expert e contracts over its token segment

@@ -104,7 +104,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_kernel(Params p) {
 
     TileRows tr;
     if constexpr (MODE == kGroupedM) {
-        if (!grouped_tile<TN>(p, tr)) return;
+        if (!grouped_tile<TN, GATED != kNotGated>(p, tr)) return;
     } else if constexpr (MODE == kGroupedK) {
         if (!grouped_k_tile<BN>(p, tr)) return;
     } else {

@@ -208,7 +208,8 @@ def test_empty_sizes():
             assert (q.view(torch.uint8) & 127 == 0).all() and (s == 0).all()
 
 
-EXPERTS = [([130, 0, 1, 128], 0), ([256, 300, 64, 5, 0, 0], 128), ([0, 0], 256), ([700], 0), ([1] * 70, 0)]
+EXPERTS = [([130, 0, 1, 128], 0), ([256, 300, 64, 5, 0, 0], 128), ([0, 0], 256), ([700], 0), ([1] * 70, 0), ([385, 520, 1000, 257], 0),
+           ([300, 641, 300], 384)]
 
 
 @pytest.mark.parametrize("rows,more", EXPERTS)
