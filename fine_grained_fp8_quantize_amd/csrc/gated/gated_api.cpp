@@ -115,7 +115,7 @@ int fp8_grouped_gated_gemm(int32_t groups, const int32_t* group_offsets, const i
     const int st = check_gated(m_total, n, k, a, lda, a_scale, ld_as, b, ldb, stride_b, b_scale, ld_bs, stride_bs, out,
                                ldo, out_dtype, out_scale, ld_os, gate_up, ldg);
     if (st != FP8Q_OK) return st;
-    if (m_total % 128 != 0 || n % 128 != 0 || m_total > 0x7FFFFFFFLL) return FP8Q_ERR_SHAPE;
+    if (m_total % 128 != 0 || m_total > 0x7FFFFFFFLL) return FP8Q_ERR_SHAPE;
     if (k > 0 && (stride_e < 0 || stride_es < 0 || mul_limit(groups, stride_e, kMaxBytes) < 0 ||
                   mul_limit(groups, stride_es, kMaxBytes / 4) < 0))
         return FP8Q_ERR_SHAPE;

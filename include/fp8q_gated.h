@@ -73,8 +73,8 @@ int fp8_gated_gemm(int64_t m, int64_t n, int64_t k, const uint8_t *a, int64_t ld
  * (offsets in whole 128 rows, group_offsets[groups] == m_total). Rows of a
  * segment past its group_rows[e] are padding: their rows of out (codes and
  * scales too) and of gate_up are written as zeros, whatever A holds there.
- * n % 128 == 0. Everything else as fp8_gated_gemm with m = m_total. FP8Q_DEBUG
- * applies as in fp8_grouped_gemm.
+ * Everything else as fp8_gated_gemm with m = m_total. FP8Q_DEBUG applies as in
+ * fp8_grouped_gemm.
  */
 int fp8_grouped_gated_gemm(int32_t groups, const int32_t *group_offsets, const int32_t *group_rows, int64_t m_total,
                            int64_t n, int64_t k, const uint8_t *a, int64_t lda, const float *a_scale, int64_t ld_as,
