@@ -42,7 +42,7 @@ def _room(x, v, out):
 
 SHAPES = [(1, 16, 32), (1, 2048, 512), (1, 130, 7168), (2, 7, 100), (5, 300, 129), (16, 64, 2048), (17, 50, 640),
           (33, 33, 1000), (64, 16, 256), (65, 40, 130), (200, 24, 384), (3, 1, 1), (4, 20, 8),
-          (2, 5000, 200), (9, 9000, 640), (20, 5000, 264), (25, 8300, 512), (50, 4500, 392), (60, 8200, 640), (40, 9000, 1100)]
+          (2, 5000, 200), (9, 9000, 640), (20, 5000, 264), (25, 8300, 512), (50, 4500, 392), (60, 8200, 640), (40, 9000, 1100), (48, 8300, 2000)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
