@@ -4,6 +4,10 @@
 // in bf16, 2 in E4M3 along the rows and 2 more along the columns. HBM bounds
 // it. Both E4M3 tilings are made in one pass over the inputs: apart they would
 // be a pass that writes bf16 and two that read it, 22 bytes instead of 10.
+// 8192 x 2048: 36.3 us with both tilings, 4.6 TB/s (16384 x 2048: 63, 5.3), 26.0
+// along the rows alone, 5.2 TB/s; 203 x 512: 3.5 us, the launch. A CU holds two
+// panels, so that 8192 x 2048 is two rounds whose loads, arithmetic and stores
+// overlap little.
 #include "gated/gated.h"
 
 #include <hip/hip_runtime.h>

@@ -5,8 +5,13 @@
 // turned into bf16 with their scales (v_cvt_scalef32_pk_bf16_fp4: exact, a code
 // has two significant bits) and multiplied by v_mfma_f32_16x16x32_bf16, whose
 // other operand holds up to 16 rows of x: the products are exact, the sums
-// FP32. HBM bounds it, so that 16 rows cost what one does until the reads of x
-// through the L2 (2 bytes an element beside 17/32 of the weights) come near.
+// FP32. HBM bounds large weights (1 x 16384 x 7168, 62 MB: 14.4 us, 4.3 TB/s; 16
+// tokens through 28 of 32 experts' 2 x 2048 x 7168, 437 MB: 79 us, 5.5 TB/s),
+// launch, one wait for the loads and the join small ones (1 x 7168 x 2048, 7.8
+// MB: 5.2 us; 5 x 2 x 2050 x 7136: 10.7), and the reads of x through the L2 many
+// rows (2 bytes an element beside 17/32 of the weights: 2 x 2048 x 7168 with 1
+// row 8.1 us, 16: 13.2, 32: 23, 64: 39). All of a wave's x in registers before
+// the first product was no faster (5.2 and 10.7 us), and spilled with one group.
 //
 // In a tile's register a lane has one block of 32 k of one row: it goes through
 // the MFMA in four steps of 8 k per lane group. The order of k inside an MFMA
