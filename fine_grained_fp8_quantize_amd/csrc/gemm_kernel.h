@@ -12,6 +12,8 @@
 // else keeps the default policy. Paired on one MI355X, NT weights took the
 // MoE grouped GEMM from 372 to 359 us; NT on the B operand of dense GEMMs,
 // which is re-read from L2 by the tiles of a band, made Dgrad 14% slower.
+// Experts' gated products, NT and default: one tile an expert 187 and 198 us,
+// 256 rows each 244 and 261, 8192 rows at random 322 and 315, 368 and 365.
 constexpr int kPolicyDefault = 0;
 constexpr int kPolicyNonTemporal = 2;
 
