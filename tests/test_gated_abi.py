@@ -78,7 +78,7 @@ def _gg(groups=3, off=D, rows=D + 64, m=384, n=256, k=512, a=A, lda=512, a_s=AS,
 
 @pytest.mark.parametrize("kw,want", [
     (dict(groups=0), OK), (dict(m=0), OK), (dict(n=0), OK), (dict(groups=-1), ERR_SHAPE), (dict(off=0), ERR_NULL),
-    (dict(m=300), ERR_SHAPE), (dict(n=200), ERR_SHAPE), (dict(se=-16), ERR_SHAPE), (dict(ses=-1), ERR_SHAPE),
+    (dict(m=300), ERR_SHAPE), (dict(n=200, dt=2, os_=CS, ld_os=384), ERR_SHAPE), (dict(se=-16), ERR_SHAPE), (dict(ses=-1), ERR_SHAPE),
     (dict(se=24), ERR_ALIGN), (dict(off=D + 2), ERR_ALIGN), (dict(rows=D + 1), ERR_ALIGN), (dict(act=-1), ERR_ENUM),
     (dict(dt=9), ERR_ENUM), (dict(a=0), ERR_NULL), (dict(dt=2), ERR_NULL), (dict(ldo=248), ERR_SHAPE),
     (dict(m=1 << 31, ld_as=1 << 26), ERR_SHAPE)])
