@@ -32,7 +32,9 @@ def _library():
         L.fp8_gated_gemm.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, i64, p, i64, i64, cint, p, i64, cint, p,
                                      i64, p, i64, p, i64, p]
         L.fp8_grouped_gated_gemm.argtypes = [i32, p, p, i64, i64, i64, p, i64, p, i64, p, i64, i64, i64, p, i64, i64,
-                                             i64, cint, p, i64, cint, p, i64, p, i64, p]
+                                             i64, cint, p, i64, cint, p, i64, p, i64, p, i64, p]
+        L.fp8_grouped_gated_workspace_bytes.argtypes = [i64, i64]
+        L.fp8_grouped_gated_workspace_bytes.restype = i64
         L.fp8_gated_backward.argtypes = [i64, i64, p, i64, p, i64, cint, cint, p, i64, p, i64, p, i64, p, i64, p]
         for name in ("fp8_gated_gemm", "fp8_grouped_gated_gemm", "fp8_gated_backward"):
             getattr(L, name).restype = cint
@@ -150,6 +152,15 @@ def _outputs(m, n, out_dtype, out, scale, gate_up, dev, stream):
     return out, scale, tail
 
 
+def _scratch(workspace, need: int, dev, stream):
+    """A workspace: new when absent (None if none is needed), checked otherwise."""
+    if workspace is None:
+        return _new(need, torch.uint8, dev, stream) if need else None
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise Fp8qError("workspace must be a contiguous uint8 tensor")
+    return workspace
+
+
 def fp8_gated_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, act: str = "silu",
                    out_dtype=torch.bfloat16, out: torch.Tensor | None = None, scale: torch.Tensor | None = None,
                    gate_up: torch.Tensor | None = None, stream=None, workspace: torch.Tensor | None = None):
@@ -173,11 +184,8 @@ def fp8_gated_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sc
     code = _act_code(act)
     out, scale, tail = _outputs(m, n, out_dtype, out, scale, gate_up, dev, stream)
     lib = _library()
-    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
-        raise Fp8qError("workspace must be a contiguous uint8 tensor")
-    if workspace is None and scale is not None:
-        need = lib.fp8_gated_workspace_bytes(m, n, k)
-        workspace = _new(need, torch.uint8, dev, stream) if need else None
+    if workspace is not None or scale is not None:
+        workspace = _scratch(workspace, lib.fp8_gated_workspace_bytes(m, n, k), dev, stream)
     st = _call(lib.fp8_gated_gemm, dev, stream, m, n, k, a.data_ptr(), lda, a_scale.data_ptr(), ld_as,
                b.data_ptr(), ldb, stride_b, b_scale.data_ptr(), ld_bs, stride_bs, code, *tail, _address(workspace),
                0 if workspace is None else workspace.numel())
@@ -188,7 +196,8 @@ def fp8_gated_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sc
 def fp8_grouped_gated_gemm(group_offsets: torch.Tensor, group_rows: torch.Tensor | None, a: torch.Tensor,
                            a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, act: str = "silu",
                            out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
-                           scale: torch.Tensor | None = None, gate_up: torch.Tensor | None = None, stream=None):
+                           scale: torch.Tensor | None = None, gate_up: torch.Tensor | None = None, stream=None,
+                           workspace: torch.Tensor | None = None):
     """:func:`fp8_gated_gemm` for the experts of an expert-sorted row layout
     (:func:`moe_dispatch` with ``align=128``): rows ``[off[e], off[e+1])`` of ``a``
     with ``b[e]``, of which the first ``group_rows[e]`` are real (None: all).
@@ -197,7 +206,7 @@ def fp8_grouped_gated_gemm(group_offsets: torch.Tensor, group_rows: torch.Tensor
     ``m_total``, the rows of ``a``; ``b[E][2][n][k]`` with
     ``b_scale[E][2][ceil(n/128)][k/128]``. Padding rows of all outputs are zeros.
     """
-    dev = _on_gpu(a, a_scale, b, b_scale, group_offsets, group_rows, out, scale, gate_up)
+    dev = _on_gpu(a, a_scale, b, b_scale, group_offsets, group_rows, out, scale, gate_up, workspace)
     m, n, k, lda, ld_as, (ldb, stride_b), (ld_bs, stride_bs) = _operands(a, a_scale, b, b_scale, 1)
     groups = b.shape[0]
     for t, entries, name in ((group_offsets, groups + 1, "group_offsets"), (group_rows, groups, "group_rows")):
@@ -207,9 +216,13 @@ def fp8_grouped_gated_gemm(group_offsets: torch.Tensor, group_rows: torch.Tensor
     if groups == 0 and m > 0:
         raise Fp8qError("%d rows belong to no expert" % m)
     out, scale, tail = _outputs(m, n, out_dtype, out, scale, gate_up, dev, stream)
-    st = _call(_library().fp8_grouped_gated_gemm, dev, stream, groups, group_offsets.data_ptr(), _address(group_rows),
+    lib = _library()
+    if workspace is not None or scale is not None:
+        workspace = _scratch(workspace, lib.fp8_grouped_gated_workspace_bytes(m, n), dev, stream)
+    st = _call(lib.fp8_grouped_gated_gemm, dev, stream, groups, group_offsets.data_ptr(), _address(group_rows),
                m, n, k, a.data_ptr(), lda, a_scale.data_ptr(), ld_as, b.data_ptr(), ldb, stride_b,
-               b.stride(0), b_scale.data_ptr(), ld_bs, stride_bs, b_scale.stride(0), code, *tail)
+               b.stride(0), b_scale.data_ptr(), ld_bs, stride_bs, b_scale.stride(0), code, *tail, _address(workspace),
+               0 if workspace is None else workspace.numel())
     _check(st, "fp8_grouped_gated_gemm")
     return out if scale is None else (out, scale)
 

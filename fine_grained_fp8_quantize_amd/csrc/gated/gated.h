@@ -45,7 +45,7 @@ struct BackwardArgs {
 // workspace: FP32 [m][n] where E4M3 output of few rows needs it (see
 // gated_launch.hpp), else unused.
 hipError_t launch_gated(const GatedArgs& p, float* workspace, hipStream_t stream);
-hipError_t launch_grouped_gated(const GatedArgs& p, hipStream_t stream);
+hipError_t launch_grouped_gated(const GatedArgs& p, float* workspace, hipStream_t stream);
 hipError_t launch_backward(const BackwardArgs& p, hipStream_t stream);
 
 }  // namespace gated

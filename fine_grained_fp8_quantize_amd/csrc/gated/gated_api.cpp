@@ -82,6 +82,11 @@ int64_t fp8_gated_workspace_bytes(int64_t m, int64_t n, int64_t k) {
     return workspace_bytes(m, n, k);
 }
 
+int64_t fp8_grouped_gated_workspace_bytes(int64_t m_total, int64_t n) {
+    if (!size_ok(m_total) || !size_ok(n) || mul_limit(m_total, n, kMaxSize) < 0) return 0;
+    return grouped_workspace_bytes(m_total, n);
+}
+
 int fp8_gated_gemm(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t lda, const float* a_scale,
                    int64_t ld_as, const uint8_t* b, int64_t ldb, int64_t stride_b, const float* b_scale,
                    int64_t ld_bs, int64_t stride_bs, int act, void* out, int64_t ldo, int out_dtype,
@@ -107,9 +112,9 @@ int fp8_grouped_gated_gemm(int32_t groups, const int32_t* group_offsets, const i
                            const uint8_t* b, int64_t ldb, int64_t stride_b, int64_t stride_e, const float* b_scale,
                            int64_t ld_bs, int64_t stride_bs, int64_t stride_es, int act, void* out, int64_t ldo,
                            int out_dtype, float* out_scale, int64_t ld_os, uint16_t* gate_up, int64_t ldg,
-                           hipStream_t stream) {
+                           void* workspace, int64_t workspace_bytes, hipStream_t stream) {
     if (!act_ok(act) || !out_ok(out_dtype)) return FP8Q_ERR_ENUM;
-    if (groups < 0 || !size_ok(m_total) || !size_ok(n) || !size_ok(k)) return FP8Q_ERR_SHAPE;
+    if (groups < 0 || workspace_bytes < 0 || !size_ok(m_total) || !size_ok(n) || !size_ok(k)) return FP8Q_ERR_SHAPE;
     if (groups == 0 || m_total == 0 || n == 0) return FP8Q_OK;
     if (!group_offsets) return FP8Q_ERR_NULL;
     const int st = check_gated(m_total, n, k, a, lda, a_scale, ld_as, b, ldb, stride_b, b_scale, ld_bs, stride_bs, out,
@@ -119,7 +124,8 @@ int fp8_grouped_gated_gemm(int32_t groups, const int32_t* group_offsets, const i
     if (k > 0 && (stride_e < 0 || stride_es < 0 || mul_limit(groups, stride_e, kMaxBytes) < 0 ||
                   mul_limit(groups, stride_es, kMaxBytes / 4) < 0))
         return FP8Q_ERR_SHAPE;
-    if ((k > 0 && stride_e % 16 != 0) || !is_aligned(group_offsets, 4) || !is_aligned(group_rows, 4))
+    if ((k > 0 && stride_e % 16 != 0) || !is_aligned(group_offsets, 4) || !is_aligned(group_rows, 4) ||
+        !is_aligned(workspace, 16))
         return FP8Q_ERR_ALIGN;
     if (!launchable(grouped_shape(m_total, n))) return FP8Q_ERR_SHAPE;
     const int seg = debug_segments(groups, group_offsets, group_rows, m_total, stream);
@@ -128,7 +134,8 @@ int fp8_grouped_gated_gemm(int32_t groups, const int32_t* group_offsets, const i
                              out, ldo, out_dtype, out_scale, ld_os, gate_up, ldg);
     p.g.groups = groups; p.g.group_offsets = group_offsets; p.g.group_rows = group_rows;
     p.g.stride_b = stride_e; p.g.stride_bs = stride_es;
-    return hip_status(launch_grouped_gated(p, stream));
+    const bool enough = workspace && workspace_bytes >= grouped_workspace_bytes(m_total, n);
+    return hip_status(launch_grouped_gated(p, enough ? static_cast<float*>(workspace) : nullptr, stream));
 }
 
 int fp8_gated_backward(int64_t m, int64_t n, const uint16_t* dh, int64_t ld_dh, const uint16_t* gate_up, int64_t ldg,

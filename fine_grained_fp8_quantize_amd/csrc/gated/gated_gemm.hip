@@ -32,12 +32,19 @@ namespace {
 // (four slabs, all that a wave has) and join are 2.7 us of it (one row, K = 128),
 // and the bytes come at 5 TB/s on top (K = 1024: 4.1 us, 2048: 5.1). 16 rows: 12
 // us, 64: 22, A being read through the L2 by every workgroup.
+struct RowsPiece {
+    const uint8_t* b;      // the gate's weights and scales
+    const float* b_scale;
+    int64_t m0, n0;
+    int64_t real_end;      // rows in [real_end, row_hi) are padding: stored as 0
+    int64_t row_hi;
+};
+
 template <int MS, int NT, int U, bool F32>
-__global__ __launch_bounds__(64 * rows_waves(MS * NT)) void gated_rows_kernel(Params p) {
-    extern __shared__ v4f partial[];  // [waves][NT][MS][64]
+__device__ __forceinline__ void gated_rows(const Params& p, const RowsPiece& t, v4f* partial /* [waves][NT][MS][64] */) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int i = lane & 15, g = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * kRowsColumns * NT, m0 = (int64_t)blockIdx.y * 16 * MS;
+    const int64_t n0 = t.n0, m0 = t.m0;
     const int slabs = (int)(p.k / kSlab);
     // rows and columns past the last ones repeat it: loaded, not stored
     const uint8_t* wrow[NT];
@@ -45,16 +52,16 @@ __global__ __launch_bounds__(64 * rows_waves(MS * NT)) void gated_rows_kernel(Pa
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         const int64_t first = n0 + kRowsColumns * c;
-        wrow[c] = p.b + (i >= 8 ? p.stride_up : 0) + min(first + (i & 7), p.n - 1) * p.ldb + 16 * g;
+        wrow[c] = t.b + (i >= 8 ? p.stride_up : 0) + min(first + (i & 7), p.n - 1) * p.ldb + 16 * g;
         // (an MFMA result's four rows are 4 g..4 g + 3: gate for g < 2)
-        sb[c] = p.b_scale + (g >= 2 ? p.stride_ups : 0) + min(first, p.n - 1) / 128 * p.ld_bs;
+        sb[c] = t.b_scale + (g >= 2 ? p.stride_ups : 0) + min(first, p.n - 1) / 128 * p.ld_bs;
     }
     const uint8_t* arow[MS];
     const float* sa[MS];
     v4f acc[NT][MS];
 #pragma unroll
     for (int s = 0; s < MS; ++s) {
-        const int64_t row = min(m0 + 16 * s + i, p.m - 1);
+        const int64_t row = min(m0 + 16 * s + i, t.real_end - 1);
         arow[s] = p.a + row * p.lda + 16 * g;
         sa[s] = p.a_scale + row;
 #pragma unroll
@@ -111,13 +118,14 @@ __global__ __launch_bounds__(64 * rows_waves(MS * NT)) void gated_rows_kernel(Pa
     for (int x = threadIdx.x; x < NT * MS * 32; x += blockDim.x) {
         const int l = x & 31, s = (x >> 5) % MS, c = (x >> 5) / MS;
         const int64_t m = m0 + 16 * s + (l & 15), n = n0 + kRowsColumns * c + 4 * (l >> 4);
-        if (m >= p.m || n >= p.n) continue;
+        if (m >= t.row_hi || n >= p.n) continue;
         const v4f* const from = partial + (c * MS + s) * 64 + l;
         v4f gate = from[0], up = from[32];
         for (int w = 1; w < waves; ++w) {
             gate += from[w * NT * MS * 64];
             up += from[w * NT * MS * 64 + 32];
         }
+        if (m >= t.real_end) gate = up = v4f{0.f, 0.f, 0.f, 0.f};
         if (p.gate_up != nullptr) {
             uint16_t* const dst = p.gate_up + m * p.ldg + n;
             store4_bf16(dst, gate, n, p.n, p.g_vec);
@@ -130,6 +138,72 @@ __global__ __launch_bounds__(64 * rows_waves(MS * NT)) void gated_rows_kernel(Pa
             store4_f32(static_cast<float*>(p.c) + m * p.ldc + n, h, n, p.n, p.h_vec);
         else
             store4_bf16(static_cast<uint16_t*>(p.c) + m * p.ldc + n, h, n, p.n, p.h_vec);
+    }
+}
+
+template <int MS, int NT, int U, bool F32>
+__global__ __launch_bounds__(64 * rows_waves(MS * NT)) void gated_rows_kernel(Params p) {
+    extern __shared__ v4f partial[];
+    const RowsPiece t = {p.b, p.b_scale, (int64_t)blockIdx.y * 16 * MS, (int64_t)blockIdx.x * kRowsColumns * NT, p.m, p.m};
+    gated_rows<MS, NT, U, F32>(p, t, partial);
+}
+
+// The experts' form: a workgroup has the 64-row quarter blockIdx.y of the
+// layout, whose segments are whole 128 rows, and takes as many 16-row tiles of
+// it as hold real rows. A quarter of padding only is written as zeros. (Twice
+// the columns for full quarters, as above, is slower here, where the LDS of
+// every workgroup has to have room for it: 4 experts of 128 rows, 2 x 512 x
+// 7168: 51 us for 40.)
+template <bool F32>
+__global__ __launch_bounds__(64 * rows_waves(4)) void grouped_rows_kernel(Params p) {
+    extern __shared__ v4f partial[];
+    RowsPiece t;
+    t.m0 = (int64_t)blockIdx.y * 64;
+    t.n0 = (int64_t)blockIdx.x * kRowsColumns;
+    // the expert: as many as there are segments that end at or before the quarter (every wave counts for itself)
+    int e = 0;
+    for (int base = 0; base < p.groups; base += 64) {
+        const int l = base + (int)(threadIdx.x & 63);
+        e += __popcll(__ballot(l < p.groups && p.group_offsets[min(l, p.groups - 1) + 1] <= t.m0));
+    }
+    e = __builtin_amdgcn_readfirstlane(e);
+    if (e >= p.groups) return;
+    const int64_t beg = p.group_offsets[e], end = p.group_offsets[e + 1], seg = max(end - beg, (int64_t)0);
+    const int64_t real = p.group_rows ? min(max((int64_t)p.group_rows[e], (int64_t)0), seg) : seg;
+    t.b = p.b + e * p.stride_b;
+    t.b_scale = p.b_scale + e * p.stride_bs;
+    t.row_hi = min(t.m0 + 64, min(end, p.m));
+    t.real_end = min(beg + real, t.row_hi);
+    const int64_t left = t.real_end - t.m0;
+    int done = 0;  // rows
+    if (left > 32) {
+        gated_rows<4, 1, 2, F32>(p, t, partial);
+        return;
+    }
+    if (left > 16) {
+        gated_rows<2, 1, 2, F32>(p, t, partial);
+        done = 32;
+    } else if (left > 0) {
+        // (every wave its share of a short K: 4 experts of 16 rows, 2 x 512 x 2048, 12.0 -> 8.3 us)
+        if (p.k <= 2 * kSlab * (int64_t)(blockDim.x >> 6))
+            gated_rows<1, 1, 2, F32>(p, t, partial);
+        else
+            gated_rows<1, 1, 4, F32>(p, t, partial);
+        done = 16;
+    }
+    for (int x = threadIdx.x; x < 64 * 2; x += blockDim.x) {
+        const int64_t m = t.m0 + (x >> 1), n = t.n0 + 4 * (x & 1);
+        if ((x >> 1) < done || m >= t.row_hi || n >= p.n) continue;
+        const v4f zero = {0.f, 0.f, 0.f, 0.f};
+        if (p.gate_up != nullptr) {
+            uint16_t* const dst = p.gate_up + m * p.ldg + n;
+            store4_bf16(dst, zero, n, p.n, p.g_vec);
+            store4_bf16(dst + p.n, zero, n, p.n, p.u_vec);
+        }
+        if constexpr (F32)
+            store4_f32(static_cast<float*>(p.c) + m * p.ldc + n, zero, n, p.n, p.h_vec);
+        else
+            store4_bf16(static_cast<uint16_t*>(p.c) + m * p.ldc + n, zero, n, p.n, p.h_vec);
     }
 }
 
@@ -165,6 +239,19 @@ Params gated_params(const GatedArgs& g) {
     return p;
 }
 
+// E4M3 output of the rows kernels: FP32 rows in the workspace, and their codes
+// from there.
+void to_workspace(Params& p, float* workspace) {
+    p.c = workspace;
+    p.ldc = p.n;
+    p.h_vec = true;
+}
+void launch_quantize(const GatedArgs& g, const float* workspace, hipStream_t stream) {
+    const int64_t blocks = parts_of(g.g.m * g.g.n / 8, 256);
+    hipLaunchKernelGGL(quantize_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, workspace, g.g.m, g.g.n,
+                       static_cast<uint8_t*>(g.g.c), g.g.ldc, g.out_scale, g.ld_os);
+}
+
 template <int MS, int NT, int U>
 void launch_rows(const Params& p, RowsForm f, bool f32, hipStream_t stream) {
     const dim3 grid((unsigned)parts_of(p.n, kRowsColumns * NT), (unsigned)parts_of(p.m, 16 * MS)), block(64 * f.waves);
@@ -181,21 +268,13 @@ hipError_t launch_gated(const GatedArgs& g, float* workspace, hipStream_t stream
     Params p = gated_params(g);
     const RowsForm f = rows_form(g.g.m, g.g.n, g.g.k);
     if (f.ms != 0 && (!g.e4m3 || workspace)) {
-        if (g.e4m3) {
-            p.c = workspace;
-            p.ldc = p.n;
-            p.h_vec = true;
-        }
+        if (g.e4m3) to_workspace(p, workspace);
         const bool f32 = g.e4m3 || g.g.out_f32;
         if (f.ms == 1) launch_rows<1, 1, 4>(p, f, f32, stream);
         else if (f.ms == 2) launch_rows<2, 1, 2>(p, f, f32, stream);
         else if (f.nt == 1) launch_rows<4, 1, 2>(p, f, f32, stream);
         else launch_rows<4, 2, 2>(p, f, f32, stream);
-        if (g.e4m3) {
-            const int64_t blocks = parts_of(p.m * p.n / 8, 256);
-            hipLaunchKernelGGL(quantize_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, workspace, p.m, p.n,
-                               static_cast<uint8_t*>(g.g.c), g.g.ldc, p.out_scale, p.ld_os);
-        }
+        if (g.e4m3) launch_quantize(g, workspace, stream);
         return hipGetLastError();
     }
     const LaunchShape s = tiles_shape(p.m, p.n);
@@ -209,8 +288,20 @@ hipError_t launch_gated(const GatedArgs& g, float* workspace, hipStream_t stream
     return hipGetLastError();
 }
 
-hipError_t launch_grouped_gated(const GatedArgs& g, hipStream_t stream) {
-    const Params p = gated_params(g);
+hipError_t launch_grouped_gated(const GatedArgs& g, float* workspace, hipStream_t stream) {
+    Params p = gated_params(g);
+    if (grouped_rows(p.m, p.n) && (!g.e4m3 || workspace)) {
+        if (g.e4m3) to_workspace(p, workspace);
+        const int waves = grouped_rows_waves(p.k);
+        const dim3 grid((unsigned)parts_of(p.n, kRowsColumns), (unsigned)(p.m / 64)), block(64 * waves);
+        const size_t lds = (size_t)waves * 64 * 4 * sizeof(v4f);
+        if (g.e4m3 || g.g.out_f32)
+            hipLaunchKernelGGL((grouped_rows_kernel<true>), grid, block, lds, stream, p);
+        else
+            hipLaunchKernelGGL((grouped_rows_kernel<false>), grid, block, lds, stream, p);
+        if (g.e4m3) launch_quantize(g, workspace, stream);
+        return hipGetLastError();
+    }
     const LaunchShape s = grouped_shape(p.m, p.n);
     const dim3 grid((unsigned)s.blocks), block(s.threads);
     if (g.e4m3)

@@ -43,6 +43,23 @@ inline RowsForm rows_form(int64_t m, int64_t n, int64_t k) {
 }
 
 inline LaunchShape tiles_shape(int64_t m, int64_t n) { return {parts_of(tiles_of(m, n), 8) * 8, 512}; }
+// Experts with few columns or few rows set aside: quarters of 64 rows by 8
+// columns, by the same rule. How many of the rows are real only the GPU knows:
+// segments of 128 rows with 2 / 16 / 32 / 64 / 128 real ones (us, rows kernel
+// and, one round of them whatever the rows, tiles: 4 experts, 2 x 512 x 7168,
+// 512 pieces: 12 / 14 / 18 / 23 / 40 and 68 to 75; 1024 columns, 1024 pieces: 20 /
+// 25 / 30 / 42 / 76; 2048 columns, 2048 pieces: 37 / 46 / 57 / 81 / 153; 32
+// experts, 256 columns: 39 / 49 / 61 / 84 / 149; 4 experts, 512 columns, K =
+// 2048: 7 / 8 / 10 / 14 / 14 and 27 to 29). Mostly full segments near the limit
+// are the price of the few rows that decoding has in them.
+inline bool grouped_rows(int64_t m_total, int64_t n) {
+    const int64_t wgs = m_total / 64 * parts_of(n, kRowsColumns);
+    return wgs <= 2048 * parts_of(m_total / 128 * parts_of(n, 128), 256) && m_total <= 1 << 20;
+}
+inline int grouped_rows_waves(int64_t k) {
+    const int64_t slabs = k >= 128 ? k / 128 : 1, steps = parts_of(slabs, 32);
+    return (int)parts_of(slabs, 2 * steps);
+}
 // (every 256-row tile of an expert holds at least 128 of its rows)
 inline LaunchShape grouped_shape(int64_t m_total, int64_t n) {
     return {parts_of(m_total / 128 * parts_of(n, 128), 256) * 256, 512};
@@ -51,6 +68,10 @@ inline LaunchShape grouped_shape(int64_t m_total, int64_t n) {
 // Bytes of FP32 scratch that E4M3 output goes through: the 128 columns of a
 // scale belong to 16 workgroups of the rows kernel.
 inline int64_t workspace_bytes(int64_t m, int64_t n, int64_t k) { return rows_form(m, n, k).ms ? m * n * 4 : 0; }
+
+inline int64_t grouped_workspace_bytes(int64_t m_total, int64_t n) {
+    return grouped_rows(m_total, n) ? m_total * n * 4 : 0;
+}
 
 // Gradient: 8 columns of a row per thread, or panels of 128 x 128.
 constexpr int kBackwardThreads = 256;

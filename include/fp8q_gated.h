@@ -73,15 +73,18 @@ int fp8_gated_gemm(int64_t m, int64_t n, int64_t k, const uint8_t *a, int64_t ld
  * (offsets in whole 128 rows, group_offsets[groups] == m_total). Rows of a
  * segment past its group_rows[e] are padding: their rows of out (codes and
  * scales too) and of gate_up are written as zeros, whatever A holds there.
+ * workspace: for E4M3 output, fp8_grouped_gated_workspace_bytes(m_total, n).
  * Everything else as fp8_gated_gemm with m = m_total. FP8Q_DEBUG applies as in
  * fp8_grouped_gemm.
  */
+int64_t fp8_grouped_gated_workspace_bytes(int64_t m_total, int64_t n);
+
 int fp8_grouped_gated_gemm(int32_t groups, const int32_t *group_offsets, const int32_t *group_rows, int64_t m_total,
                            int64_t n, int64_t k, const uint8_t *a, int64_t lda, const float *a_scale, int64_t ld_as,
                            const uint8_t *b, int64_t ldb, int64_t stride_b, int64_t stride_e, const float *b_scale,
                            int64_t ld_bs, int64_t stride_bs, int64_t stride_es, int act, void *out, int64_t ldo,
                            int out_dtype, float *out_scale, int64_t ld_os, uint16_t *gate_up, int64_t ldg,
-                           hipStream_t stream);
+                           void *workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /*
  * fp8_gated_backward -- the gradients of gate and up.

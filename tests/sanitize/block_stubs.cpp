@@ -8,7 +8,7 @@
 namespace fp8q {
 namespace gated {
 hipError_t launch_gated(const GatedArgs&, float*, hipStream_t) { return hipErrorNoDevice; }
-hipError_t launch_grouped_gated(const GatedArgs&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_grouped_gated(const GatedArgs&, float*, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_backward(const BackwardArgs&, hipStream_t) { return hipErrorNoDevice; }
 }  // namespace gated
 namespace gemv {

@@ -19,6 +19,9 @@ extern "C" void rows_form(int64_t m, int64_t n, int64_t k, int* out) {
     const fp8q::gated::RowsForm f = fp8q::gated::rows_form(m, n, k);
     out[0] = f.ms; out[1] = f.nt; out[2] = f.waves;
 }
+extern "C" void grouped_form(int64_t m, int64_t n, int64_t k, int* out) {
+    out[0] = fp8q::gated::grouped_rows(m, n); out[1] = fp8q::gated::grouped_rows_waves(k);
+}
 extern "C" void gemv_form(int64_t t, int64_t topk, int64_t e, int64_t n, int64_t k, int gated, int* out) {
     const fp8q::gemv::Form f = fp8q::gemv::form(t, topk, e, n, k, gated != 0);
     out[0] = f.ms; out[1] = f.nt; out[2] = f.waves; out[3] = f.tiles; out[4] = (int)f.rows;
@@ -56,6 +59,21 @@ def test_gated_forms(rules):
                 assert ms == 0 or m <= 16 * ms * 65535
                 if ms:
                     assert 1 <= waves <= (8 if ms * nt >= 8 else 16) and waves * nt * ms <= 64  # KB of LDS
+
+
+def test_grouped_forms(rules):
+    import test_gpu_gated as gpu
+    seen = set()
+    for rows, more in gpu.EXPERTS:
+        m = sum(-(-r // 128) * 128 for r in rows) + more
+        for n, k in gpu.COLUMNS:
+            seen.add((rules("grouped_form", m, n, k, size=2)[0], n % 128 == 0))
+    assert seen == {(0, False), (0, True), (1, False), (1, True)}
+    for m in (128, 1024, 8192, 1 << 20, 1 << 23, 1 << 30):
+        for n in (1, 8, 128, 2048, 1 << 20):
+            for k in (0, 128, 1024, 7168, 1 << 20):
+                rows, waves = rules("grouped_form", m, n, k, size=2)
+                assert not rows or (m <= 64 * 65535 and 1 <= waves <= 16)  # 4 KB of LDS per wave
 
 
 def test_gemv_forms(rules):

@@ -29,7 +29,7 @@ def _lib():
 def test_header_is_exported_and_bound():
     text = open(os.path.join(ROOT, "include", "fp8q_gated.h")).read()
     names = re.findall(r"^\s*int(?:64_t)?\s+(\w+)\s*\(", re.sub(r"/\*.*?\*/", "", text, flags=re.S), flags=re.M)
-    assert len(names) == 4
+    assert len(names) == 5
     _lib()
     raw = ctypes.CDLL(fq.library_path())
     for name in names:
@@ -71,9 +71,9 @@ def test_gemm_refusals(kw, want):
 
 
 def _gg(groups=3, off=D, rows=D + 64, m=384, n=256, k=512, a=A, lda=512, a_s=AS, ld_as=384, b=B, ldb=512, sb=131072,
-        se=262144, b_s=BS, ld_bs=4, sbs=8, ses=16, act=0, out=C, ldo=256, dt=0, os_=0, ld_os=0, gu=0, ldg=0):
+        se=262144, b_s=BS, ld_bs=4, sbs=8, ses=16, act=0, out=C, ldo=256, dt=0, os_=0, ld_os=0, gu=0, ldg=0, ws=0, wsb=0):
     return _lib().fp8_grouped_gated_gemm(groups, off, rows, m, n, k, a, lda, a_s, ld_as, b, ldb, sb, se, b_s, ld_bs, sbs,
-                                         ses, act, out, ldo, dt, os_, ld_os, gu, ldg, None)
+                                         ses, act, out, ldo, dt, os_, ld_os, gu, ldg, ws, wsb, None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -81,7 +81,7 @@ def _gg(groups=3, off=D, rows=D + 64, m=384, n=256, k=512, a=A, lda=512, a_s=AS,
     (dict(m=300), ERR_SHAPE), (dict(n=200, dt=2, os_=CS, ld_os=384), ERR_SHAPE), (dict(se=-16), ERR_SHAPE), (dict(ses=-1), ERR_SHAPE),
     (dict(se=24), ERR_ALIGN), (dict(off=D + 2), ERR_ALIGN), (dict(rows=D + 1), ERR_ALIGN), (dict(act=-1), ERR_ENUM),
     (dict(dt=9), ERR_ENUM), (dict(a=0), ERR_NULL), (dict(dt=2), ERR_NULL), (dict(ldo=248), ERR_SHAPE),
-    (dict(m=1 << 31, ld_as=1 << 26), ERR_SHAPE)])
+    (dict(m=1 << 31, ld_as=1 << 26), ERR_SHAPE), (dict(ws=W + 8, wsb=64), ERR_ALIGN), (dict(wsb=-1), ERR_SHAPE)])
 def test_grouped_refusals(kw, want):
     assert _gg(**kw) == want
 
@@ -114,6 +114,9 @@ def test_workspace():
     assert L.fp8_gated_workspace_bytes(5, 256, 512) == 5 * 256 * 4
     assert L.fp8_gated_workspace_bytes(4096, 2048, 7168) == 0
     assert L.fp8_gated_workspace_bytes(-1, 256, 512) == 0
+    assert L.fp8_grouped_gated_workspace_bytes(512, 256) == 512 * 256 * 4
+    assert L.fp8_grouped_gated_workspace_bytes(8192, 2048) == 0
+    assert L.fp8_grouped_gated_workspace_bytes(512, -1) == 0
 
 
 def test_slopes_against_differences():
