@@ -205,6 +205,7 @@ def fp8_grouped_gated_gemm(group_offsets: torch.Tensor, group_rows: torch.Tensor
     ``group_offsets`` int32 ``[E+1]``, multiples of 128, its last entry
     ``m_total``, the rows of ``a``; ``b[E][2][n][k]`` with
     ``b_scale[E][2][ceil(n/128)][k/128]``. Padding rows of all outputs are zeros.
+    ``workspace`` is that of E4M3 output, as there.
     """
     dev = _on_gpu(a, a_scale, b, b_scale, group_offsets, group_rows, out, scale, gate_up, workspace)
     m, n, k, lda, ld_as, (ldb, stride_b), (ld_bs, stride_bs) = _operands(a, a_scale, b, b_scale, 1)

@@ -427,6 +427,36 @@ def test_streams_and_replays():
             assert torch.equal(x, y)
 
 
+def test_a_stream_of_its_own_and_experts_in_a_graph():
+    """`stream=`: outputs and scratch of two calls at once; experts' few rows captured, with scratch of the graph."""
+    rows = np.array([3, 0, 128, 40])
+    off = np.concatenate([[0], np.cumsum(-(-rows // 128) * 128)])
+    n, k = 256, 512
+    d = [_dev(off.astype(np.int32), rows.astype(np.int32), *_problem(s, int(off[-1]), n, k, (4,))) for s in (1, 2)]
+    few = [_dev(*_problem(s, 9, n, k)) for s in (3, 4)]
+    run = lambda i, **kw: (*fq.fp8_grouped_gated_gemm(*d[i], "gelu", E4M3, **kw),  # noqa: E731
+                           *fq.fp8_gated_gemm(*few[i], "silu", E4M3, **kw), fq.fp8_grouped_gated_gemm(*d[i], **kw))
+    want = [[t.clone() for t in run(i)] for i in (0, 1)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[run(i, stream=streams[i]) for i in (0, 1)] for _ in range(4)]
+    torch.cuda.synchronize()
+    same = lambda x, y: torch.equal(x.view(torch.uint8), y.view(torch.uint8))  # noqa: E731
+    for pair in got:
+        for i in (0, 1):
+            assert all(same(x, y) for x, y in zip(pair[i], want[i]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = run(0)
+    for _ in range(3):
+        for t in kept:
+            t.view(torch.uint8).zero_()
+        graph.replay()
+        run(1)
+        torch.cuda.synchronize()
+        assert all(same(x, y) for x, y in zip(kept, want[0]))
+
+
 def test_refusals():
     d = _dev(*_problem(1, 16, 200, 256))
     E = fq.Fp8qError
