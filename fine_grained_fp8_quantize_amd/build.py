@@ -22,9 +22,10 @@ LIB = os.path.join(HERE, "libfp8q.so")
 SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "mx4/mx4_api.cpp", "mx4/mx4_quant.hip", "mx4/mx4_gemm.hip",
            "moe/moe_api.cpp", "moe/moe.hip", "gated/gated_api.cpp", "gated/gated_gemm.hip",
            "gated/gated_backward.hip", "gemv/gemv_api.cpp", "gemv/gemv.hip", "adamw/adamw_api.cpp", "adamw/adamw.hip"]
-HEADERS = ["fp8q_device.h", "gemm_common.h", "gemm_kernel.h", "launch.h", "host_checks.hpp", "launch_shape.hpp",
-           "mx4/mx4.h", "mx4/mx4_launch.hpp", "mx4/mx4_mfma.h", "moe/moe.h", "moe/moe_launch.hpp", "gated/act.h",
-           "gated/gated.h", "gated/gated_launch.hpp", "gemv/gemv.h", "gemv/gemv_launch.hpp", "adamw/adamw.h"]
+HEADERS = ["fp8q_device.h", "gemm_common.h", "gemm_kernel.h", "expert_tiles.h", "launch.h", "host_checks.hpp",
+           "launch_shape.hpp", "mx4/mx4.h", "mx4/mx4_launch.hpp", "mx4/mx4_mfma.h", "moe/moe.h", "moe/moe_launch.hpp",
+           "gated/act.h", "gated/gated.h", "gated/gated_launch.hpp", "gemv/gemv.h", "gemv/gemv_launch.hpp",
+           "adamw/adamw.h"]
 PUBLIC_HEADERS = ["fp8q.h", "fp8q_mx4.h", "fp8q_moe.h", "fp8q_gated.h", "fp8q_gemv.h", "fp8q_adamw.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -4,6 +4,7 @@
 // LDS swizzle and small device helpers.
 #pragma once
 
+#include "expert_tiles.h"
 #include "fp8q_device.h"
 #include "launch.h"
 
@@ -222,9 +223,9 @@ __device__ __forceinline__ bool grouped_slot(const Params& p, int slot, TileRows
             int rows = kBM;
             if constexpr (EVEN) {
                 if (real > (k - 1) * kBM) {
-                    const int quarters = (seg + 63) / 64, first = mt * quarters / k;
-                    t.m0 = x.beg + (int64_t)first * 64;
-                    rows = ((mt + 1) * quarters / k - first) * 64;
+                    const TileSpan span = even_span(seg, k, mt);
+                    t.m0 = x.beg + (int64_t)span.first;
+                    rows = span.rows;
                 }
             }
             // offsets that break the contract must not move stores outside C
