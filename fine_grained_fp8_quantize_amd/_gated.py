@@ -238,7 +238,8 @@ def fp8_gated_backward(dh: torch.Tensor, gate_up: torch.Tensor, act: str = "silu
     ``out_dtype=torch.float8_e4m3fn``: returns codes ``[m][2n]`` and scales
     ``[2n/128][m]`` in 1x128 tiles (for the product with the transposed weights,
     dX) and, with ``transposed``, codes ``[2n][m]`` and scales ``[m/128][2n]`` in
-    128x1 token tiles too (for the product with X, dW; m a multiple of 128).
+    128x1 token tiles too (for the product with X, dW; m a multiple of 128). A
+    tile that holds a NaN or an infinity reads back with nothing finite in it.
     ``torch.bfloat16``: returns D in bf16, any n.
     """
     dev = _on_gpu(dh, gate_up, out, scale, out_t, scale_t)

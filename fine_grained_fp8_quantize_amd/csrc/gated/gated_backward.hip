@@ -93,11 +93,14 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, c
     uint32_t w = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], (int)w, true);
 }
-// (a NaN does not count here: it has a code of its own)
+// A NaN is the largest (v_maximum3_f32): its tile gets a scale of NaN, which
+// its other elements, zeros among them, could not hide.
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float max_abs(float m, float a, float b) {
-    return __builtin_fmaxf(__builtin_fmaxf(m, __builtin_fabsf(a)), __builtin_fabsf(b));
+    return max_nan(max_nan(m, __builtin_fabsf(a)), __builtin_fabsf(b));
 }
-// The largest of 16 lanes' values >= 0, whose bits are ordered as they are.
+// The largest of 16 lanes' values >= 0, whose bits are ordered as they are (a
+// NaN's, of either sign, behind them).
 __device__ __forceinline__ float row_max(float m) { return __uint_as_float(row16_max(__float_as_uint(m))); }
 
 // Eight columns of a row per thread; 16 lanes hold a 1x128 tile.
@@ -148,10 +151,10 @@ __device__ __forceinline__ float fold(float a, float b) {
     const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
     if constexpr (HALF == 32) {
         const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-        return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+        return max_nan(__uint_as_float(r[0]), __uint_as_float(r[1]));
     } else {
         const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
-        return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+        return max_nan(__uint_as_float(r[0]), __uint_as_float(r[1]));
     }
 }
 
@@ -224,7 +227,7 @@ __global__ __launch_bounds__(kPanelThreads, 4) void backward_panel_kernel(Backwa
         const int o = t >> 7, c = t & 127;
         float top = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, red[w][o][c]);
+        for (int w = 0; w < kWaves; ++w) top = max_nan(top, red[w][o][c]);
         const TileScale ts = tile_scale(top);
         col_top[o][c] = top;
         p.out_t_scale[tb * p.ld_ts + o * p.n + c0 + c] = ts.s;
