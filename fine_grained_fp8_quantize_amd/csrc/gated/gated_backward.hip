@@ -4,8 +4,8 @@
 // in bf16, 2 in E4M3 along the rows and 2 more along the columns. HBM bounds
 // it. Both E4M3 tilings are made in one pass over the inputs: apart they would
 // be a pass that writes bf16 and two that read it, 22 bytes instead of 10.
-// 8192 x 2048: 36.3 us with both tilings, 4.6 TB/s (16384 x 2048: 63, 5.3), 26.0
-// along the rows alone, 5.2 TB/s; 203 x 512: 3.5 us, the launch. A CU holds two
+// 8192 x 2048: 38.2 us with both tilings, 4.4 TB/s (16384 x 2048: 66, 5.1), 27.8
+// along the rows alone, 4.8 TB/s; 203 x 512: 3.5 us, the launch. A CU holds two
 // panels, so that 8192 x 2048 is two rounds whose loads, arithmetic and stores
 // overlap little.
 #include "gated/gated.h"
@@ -39,10 +39,10 @@ __device__ __forceinline__ Eight load8(const uint16_t* p, int64_t left) {
     }
 }
 
-// The logistic is that of act.h, correction included: without it, and with 1 / s
-// rounded up to a last place more, twice as many codes as in the same formulas
-// in FP32 lay on the other side of a border (8192 x 2048: 123 for 57 of 33.5
-// million), at 0.9 us less. From +-16 on gelu's share is 0 or 1 exactly: the
+// The logistic is that of act.h, correction included: with it as many codes as
+// in the same formulas in elementary FP32 operations lie on the other side of a
+// border from the exact gradient's (8192 x 2048: 58 and 58 of 33.5 million);
+// without it, and with 1 / s uncorrected, 123. From +-16 on gelu's share is 0 or 1 exactly: the
 // powers of g that would overflow are taken of that (but a NaN stays).
 __device__ __forceinline__ void gradients(int act, float dh, float g, float u, float& dg, float& du) {
     float w = g, by = 1.0f, c = g;
@@ -58,13 +58,16 @@ __device__ __forceinline__ void gradients(int act, float dh, float g, float u, f
     dg = (ds * u) * (act != FP8Q_ACT_SILU ? __builtin_fmaf(r, by, 1.0f) : 1.0f + r);
 }
 
-// The scale of a tile, fl(amax / 448) (one correction of the product with the
-// rounded reciprocal), and what its elements are multiplied with: 1 / s, rounded
-// once. A quotient in place of the product would take as many operations again
-// as everything else here, and would differ where it lies within 2^-23 of the
-// border of two codes. (The largest may come out a last place above 448, which
-// rounds to the code of 448 as well.) Tiny scales, whose reciprocals are not
-// finite, take the quotient.
+// The scale of a tile and what its quotients take, by the library's contract:
+// s = fl(amax / 448), codes of fl(x / s). Both quotients are made of a product
+// with a reciprocal and one correction of its residual (Markstein's, as in
+// fp8q_device.h): fl(1 / 448) is a constant, and v_rcp_f32 corrected in the
+// same way is fl(1 / s) (for every significand of s, compared on the GPU, where
+// 1 / s is normal, s < 2^126; a scale is below 2^120). The sign is that of x,
+// zeros' included: the residual is negated twice, so that +-0 stays as it is.
+// Scales whose residuals may be subnormal, zero, NaN and infinity take divisions.
+// The product with fl(1 / s) alone would be 1.8 us less of 38 (8192 x 2048, both
+// tilings) and give other codes next to a border.
 struct TileScale {
     float s, y;
     bool slow;
@@ -75,20 +78,26 @@ __device__ __forceinline__ TileScale tile_scale(float amax) {
     const float q = amax * kBy;
     t.s = __builtin_fmaf(__builtin_fmaf(-q, kE4M3Max, amax), kBy, q);
     t.slow = !(t.s >= kSmallScale);
+    if (t.slow) t.s = amax / kE4M3Max;
     const float y = __builtin_amdgcn_rcpf(t.s);
     t.y = __builtin_fmaf(__builtin_fmaf(-t.s, y, 1.0f), y, y);
     return t;
 }
-__device__ __forceinline__ float tiny_quotient(float x, float s) {
+__device__ __forceinline__ float quotient(float x, const TileScale& t) {
+    const float q = x * t.y;
+    return __builtin_fmaf(-__builtin_fmaf(q, t.s, -x), t.y, q);
+}
+__device__ __forceinline__ float slow_quotient(float x, float s) {
     return s == 0.0f ? __builtin_copysignf(0.0f, x) : __builtin_fminf(__builtin_fmaxf(x / s, -kE4M3Max), kE4M3Max);
 }
+// (the largest quotient may lie a last place above 448, whose code it gets)
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, const TileScale& t) {
-    float q[4] = {a * t.y, b * t.y, c * t.y, d * t.y};
+    float q[4] = {quotient(a, t), quotient(b, t), quotient(c, t), quotient(d, t)};
     if (t.slow) {
-        q[0] = tiny_quotient(a, t.s);
-        q[1] = tiny_quotient(b, t.s);
-        q[2] = tiny_quotient(c, t.s);
-        q[3] = tiny_quotient(d, t.s);
+        q[0] = slow_quotient(a, t.s);
+        q[1] = slow_quotient(b, t.s);
+        q[2] = slow_quotient(c, t.s);
+        q[3] = slow_quotient(d, t.s);
     }
     uint32_t w = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], (int)w, true);
@@ -174,7 +183,7 @@ __global__ __launch_bounds__(kPanelThreads, 4) void backward_panel_kernel(Backwa
     __shared__ __attribute__((aligned(16))) uint8_t codes[2][128 * 128];
     __shared__ float red[kWaves][2][128];
     __shared__ float row_s[2][128];
-    __shared__ float col_top[2][128];
+    __shared__ float2 col_scale[2][128];  // a tile's s and y
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, g = t & 15, r = t >> 4;
     const int64_t panels = p.n / 128, tb = blockIdx.x / panels, cb = blockIdx.x - tb * panels;
     const int64_t t0 = tb * 128, c0 = cb * 128;
@@ -229,7 +238,7 @@ __global__ __launch_bounds__(kPanelThreads, 4) void backward_panel_kernel(Backwa
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) top = max_nan(top, red[w][o][c]);
         const TileScale ts = tile_scale(top);
-        col_top[o][c] = top;
+        col_scale[o][c] = make_float2(ts.s, ts.y);
         p.out_t_scale[tb * p.ld_ts + o * p.n + c0 + c] = ts.s;
         p.out_scale[(o * p.n + c0) / 128 * p.ld_os + t0 + c] = row_s[o][c];
     }
@@ -239,7 +248,8 @@ __global__ __launch_bounds__(kPanelThreads, 4) void backward_panel_kernel(Backwa
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int c = 8 * g + k;
-            const TileScale ts = tile_scale(col_top[o][c]);
+            const float2 sy = col_scale[o][c];
+            const TileScale ts = {sy.x, sy.y, !(sy.x >= kSmallScale) || sy.x == __builtin_inff()};
             *reinterpret_cast<uint32_t*>(&codes[o][c * 128 + panel_chunk(r >> 2, c) * 16 + (r & 3) * 4]) =
                 codes4(d[o][0][k], d[o][1][k], d[o][2][k], d[o][3][k], ts);
         }

@@ -101,7 +101,8 @@ int fp8_grouped_gated_gemm(int32_t groups, const int32_t *group_offsets, const i
  *             128 == 0), codes TRANSPOSED, out_t [2n][ld_t], ld_t >= m, with
  *             scales out_t_scale [m/128][ld_ts], ld_ts >= 2n, in 128x1 token
  *             tiles (A of the product with X, dW). Both from one pass, each
- *             rounded once from the FP32 values. A tile that holds a NaN or an
+ *             of the FP32 values: scale fl32(amax / 448), codes E4M3(fl32(x /
+ *             scale)), as everywhere (fp8q.h). A tile that holds a NaN or an
  *             infinity reads back with nothing finite in it.
  * dh          bf16 [m][ld_dh], ld_dh >= n; gate_up bf16 [m][ldg], ldg >= 2n.
  * Alignment: bf16 output: elements only (16-byte aligned rows are faster).
