@@ -1,0 +1,59 @@
+"""Blocks of the 8-bit optimizer states as their definition has them: NaN for a
+block whose moment or root is infinite."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import fine_grained_fp8_quantize_amd as fq
+from oracle import adamw as model
+
+pytestmark = pytest.mark.gpu
+
+HYPER = dict(lr=1e-3, beta1=0.5, beta2=0.75, eps=1e-8, weight_decay=0.1)
+
+
+def _first_step(g):
+    """The arrays of one tensor after a first step from zero states."""
+    n = len(g)
+    t = {"p": torch.ones(n, device="cuda"), "m": torch.zeros(n, dtype=torch.uint8, device="cuda"),
+         "r": torch.zeros(n, dtype=torch.uint8, device="cuda")}
+    s = {k: torch.zeros(-(-n // 128), device="cuda") for k in ("m", "r")}
+    plan = fq.adamw_plan([t["p"]], [t["m"]], [t["r"]], [s["m"]], [s["r"]])
+    fq.adamw_step(plan, [torch.from_numpy(g).cuda()], 1, seed=3, **HYPER)
+    return plan, {k: x.cpu().numpy() for k, x in t.items()}, {k: x.cpu().numpy() for k, x in s.items()}
+
+
+def _values(codes, scale):
+    with np.errstate(invalid="ignore"):
+        return model.decode_e4m3(codes) * scale[np.arange(len(codes)) // 128]
+
+
+@pytest.mark.parametrize("bad,m_too", [(float("inf"), True), (-float("inf"), True), (float("nan"), True), (1e20, False),
+                                       (-3e38, False)])
+@pytest.mark.parametrize("at", [0, 300, 999])
+def test_blocks_that_pass_float32(bad, m_too, at):
+    """An infinite gradient, and a finite one whose square is infinite: the block reads back as NaN, so that its
+    elements do not stand still unnoticed; its neighbours keep their bits."""
+    rng = np.random.default_rng(4)
+    g = rng.standard_normal(1000).astype(np.float32)
+    _, clean, clean_s = _first_step(g)
+    g[at] = bad
+    plan, got, got_s = _first_step(g)
+    block = np.arange(1000) // 128 == at // 128
+    m, r = _values(got["m"], got_s["m"]), _values(got["r"], got_s["r"])
+    assert np.isnan(r[block]).all()
+    assert np.isnan(m[block]).all() if m_too else np.isfinite(m).all()
+    for name in ("m", "r"):
+        assert np.array_equal(got[name][~block], clean[name][~block])
+        assert np.array_equal(np.delete(got_s[name], at // 128), np.delete(clean_s[name], at // 128))
+    # the step that meets it takes the moments as they were computed: the others of the block move as ever
+    others = np.arange(1000) != at
+    assert np.array_equal(got["p"][others], clean["p"][others])
+    with np.errstate(all="ignore"):
+        one, bits = np.ones(1000, np.float32), model.random_bits(1000, 0, 1, 3)
+        p, wm, wr, _ = model.step32(one, g, 0 * one, 0 * one, step=1, **HYPER)
+        wants = model.encode(wm, bits & np.uint64(0xFFFF), False), model.encode(wr, bits >> np.uint64(16), True)
+    for (codes, scale), name in zip(wants, ("m", "r")):
+        assert np.array_equal(codes[~block], got[name][~block]) and np.array_equal(scale, got_s[name], equal_nan=True)
