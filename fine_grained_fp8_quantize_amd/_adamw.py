@@ -78,7 +78,7 @@ def adamw_plan(params, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale
     """The tensors that :func:`adamw_step` updates, looked over once.
 
     ``params``: FP32 or bf16 tensors (all of one dtype), contiguous, of any
-    number and shape. ``exp_avg``, ``exp_avg_sq``: states of the same shapes,
+    number and shape, up to 2^34 - 1024 elements each. ``exp_avg``, ``exp_avg_sq``: states of the same shapes,
     zero at the start of training: FP32, or E4M3 codes (``float8_e4m3fn`` or
     uint8) for states in 8 bits, where ``exp_avg_sq`` holds the ROOT of the
     second moment and ``exp_avg_scale``, ``exp_avg_sq_scale`` are FP32

@@ -57,6 +57,10 @@ constexpr int kVec = 4;                                // consecutive elements o
 constexpr int kChunk = kThreads * kVec;                // elements of a workgroup
 constexpr int kBlock = 128;                            // elements that share a scale
 static_assert(kBlock == 32 * kVec, "a block is half a wave");
+constexpr int64_t kMostBlocks = FP8Q_ADAMW_MAX_NUMEL / kChunk;  // of one tensor
+static_assert(FP8Q_ADAMW_MAX_NUMEL % kChunk == 0 && kMostBlocks * kThreads <= 0xFFFFFFFFLL &&
+                  (kMostBlocks + 1) * kThreads > 0xFFFFFFFFLL,
+              "the largest tensor is the largest launch");
 
 struct Entry {
     void* param;
@@ -353,10 +357,7 @@ hipError_t launch_tables(int32_t count, const fp8q_adamw_tensor* tensors, const 
             const fp8q_adamw_tensor& t = tensors[at];
             const void* const grad = grads[at];
             const int64_t need = grad ? (t.numel + kChunk - 1) / kChunk : 0;
-            if (!launchable({blocks + need, kThreads})) {
-                if (table.count == 0) return hipErrorInvalidValue;
-                break;
-            }
+            if (!launchable({blocks + need, kThreads})) break;  // (no tensor alone: kMostBlocks)
             const int j = table.count++;
             ++at;
             table.t[j] = Entry{t.param, grad, t.exp_avg, t.exp_avg_sq, t.copy, t.numel};

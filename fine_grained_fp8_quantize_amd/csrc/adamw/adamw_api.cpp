@@ -18,6 +18,7 @@ constexpr int64_t kMaxNumel = 1LL << 40;
 int check_tensor(const fp8q_adamw_tensor& t, const void* grad, bool param_f32, bool grad_f32, bool bits8) {
     if (t.numel < 0 || t.numel > kMaxNumel) return FP8Q_ERR_SHAPE;
     if (t.numel == 0 || !grad) return FP8Q_OK;
+    if (t.numel > FP8Q_ADAMW_MAX_NUMEL) return FP8Q_ERR_SHAPE;  // (before any other tensor's launch)
     if (!t.param || !t.exp_avg || !t.exp_avg_sq) return FP8Q_ERR_NULL;
     if (bits8 != (t.exp_avg_scale != nullptr) || bits8 != (t.exp_avg_sq_scale != nullptr)) return FP8Q_ERR_NULL;
     if (t.copy && !param_f32) return FP8Q_ERR_ENUM;

@@ -17,6 +17,8 @@ extern "C" {
 #define FP8Q_ADAMW_BF16 0 /* parameters or gradients in bf16 */
 #define FP8Q_ADAMW_F32  1 /* ... in FP32                     */
 
+#define FP8Q_ADAMW_MAX_NUMEL ((1LL << 34) - 1024) /* elements of one tensor with a gradient */
+
 /*
  * One tensor of a step: device arrays of `numel` elements, contiguous.
  *   param      updated in place.
@@ -74,7 +76,7 @@ typedef struct fp8q_adamw_tensor {
  *             replayed takes their values of that time).
  * grad_scale  DEVICE FP32 [1] or NULL for 1. A scale that is not finite makes
  *             the step leave every array as it was.
- * Shapes: count >= 0, numel >= 0, step >= 1 (a device step below 1 acts as 1),
+ * Shapes: count >= 0, 0 <= numel <= FP8Q_ADAMW_MAX_NUMEL, step >= 1 (a device step below 1 acts as 1),
  *         0 <= beta1, beta2 < 1, eps >= 0 (with 0, elements whose moments are
  *         all zero become NaN: 0 / 0).
  * One launch for each 64 tensors (56 with 8-bit states). count == 0, or no elements: FP8Q_OK.
