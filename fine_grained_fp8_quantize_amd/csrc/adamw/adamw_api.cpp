@@ -41,9 +41,10 @@ int adamw_step(int32_t count, const fp8q_adamw_tensor* tensors, const void* cons
         (grad_dtype != FP8Q_ADAMW_BF16 && grad_dtype != FP8Q_ADAMW_F32) || (state_bits != 32 && state_bits != 8))
         return FP8Q_ERR_ENUM;
     if (count < 0 || (!step_dev && step < 1)) return FP8Q_ERR_SHAPE;
-    // (comparisons that a NaN fails)
+    // (comparisons that a NaN fails; eps is an FP32 number in the kernels, and 0 only where the caller's is)
+    const float eps32 = (float)eps;
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) ||
-        !std::isfinite(eps) || !std::isfinite(lr) || !std::isfinite(weight_decay))
+        !std::isfinite(eps32) || (eps32 == 0.0f && eps > 0.0) || !std::isfinite(lr) || !std::isfinite(weight_decay))
         return FP8Q_ERR_SHAPE;
     if (count == 0) return FP8Q_OK;
     if (!tensors || !grads) return FP8Q_ERR_NULL;
@@ -58,7 +59,7 @@ int adamw_step(int32_t count, const fp8q_adamw_tensor* tensors, const void* cons
     if (!work) return FP8Q_OK;
     Options o = {};
     o.lr = lr; o.beta1 = beta1; o.beta2 = beta2; o.weight_decay = weight_decay;
-    o.eps = (float)eps; o.step = step;
+    o.eps = eps32; o.step = step;
     o.lr_dev = lr_dev; o.step_dev = step_dev; o.grad_scale = grad_scale; o.seed = seed;
     o.param_f32 = param_f32; o.grad_f32 = grad_f32; o.bits8 = state_bits == 8;
     return hip_status(launch_step(count, tensors, grads, o, stream));

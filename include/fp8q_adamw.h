@@ -78,7 +78,8 @@ typedef struct fp8q_adamw_tensor {
  *             the step leave every array as it was.
  * Shapes: count >= 0, 0 <= numel <= FP8Q_ADAMW_MAX_NUMEL, step >= 1 (a device step below 1 acts as 1),
  *         0 <= beta1, beta2 < 1, eps >= 0 (with 0, elements whose moments are
- *         all zero become NaN: 0 / 0).
+ *         all zero become NaN: 0 / 0; a positive eps that FP32 rounds to 0 or
+ *         to infinity is refused).
  * One launch for each 64 tensors (56 with 8-bit states). count == 0, or no elements: FP8Q_OK.
  * Errors: FP8Q_ERR_NULL, FP8Q_ERR_SHAPE (also for the options' ranges),
  *         FP8Q_ERR_ALIGN, FP8Q_ERR_ENUM, FP8Q_ERR_HIP. Everything is checked

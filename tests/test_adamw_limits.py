@@ -44,3 +44,10 @@ def test_a_tensor_past_a_launch(numel, bits):
     assert _step([0] * 130 + [numel], [True] * 131, bits) == ERR_SHAPE
     # (one that takes no part in the step may have any size)
     assert _step([MOST, numel], [False, False], bits) == OK
+
+
+@pytest.mark.parametrize("eps,want", [(0.0, OK), (1e-8, OK), (1e-45, OK), (3.4e38, OK), (1e-46, ERR_SHAPE),
+                                      (1e-50, ERR_SHAPE), (5e-324, ERR_SHAPE), (1e39, ERR_SHAPE), (1e308, ERR_SHAPE)])
+def test_eps_is_what_float32_has_of_it(eps, want):
+    """A positive eps that FP32 rounds to 0 would make elements without any gradient yet NaN (0 / 0)."""
+    assert _step([0], [True], eps=eps) == want
