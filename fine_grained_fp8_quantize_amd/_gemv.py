@@ -120,7 +120,9 @@ def fp4_gemv_mx(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, n: int 
                 ids: torch.Tensor | None = None, first: int = 0, out_dtype=torch.bfloat16,
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Few bf16 rows times an FP4 weight: ``y = x deq(w)^T``, the weight-only
-    product of serving. FP32 sums; ``y`` in bf16 or FP32.
+    product of serving. FP32 sums, in an order that the sizes alone choose (a
+    row's does not depend on what the others hold, but on their number); ``y`` in
+    bf16 or FP32.
 
     ``x[m][k]``; ``w``, ``w_scale``: an FP4 matrix of ``n`` rows with K = ``k``
     from :func:`fp4_quantize_mx` (``n``: whole tiles of 16 when left out).

@@ -81,7 +81,7 @@ __device__ __forceinline__ void store4(const Args& p, int64_t route, int64_t n, 
 struct Routes {
     uint32_t mask[kMaxExperts / 32];
     int count;
-    uint16_t list[kMaxRoutes];  // in no particular order: a row's result does not depend on the others
+    uint16_t list[kMaxRoutes];  // in no particular order: a row's result does not depend on its place
 };
 
 __device__ __forceinline__ void append(Routes& r, bool mine, int route) {

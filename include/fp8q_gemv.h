@@ -38,8 +38,10 @@ extern "C" {
  * The weights are exact in bf16 except where codes times 2^e pass its largest
  * value (infinite there). Every weight row is read once for up to 16 rows of X
  * (64 with more than 32 rows, 32 with more than 16); products of many rows
- * belong to fp4_gemm_mx and fp4_grouped_gemm_mx. The sums are taken in a fixed
- * order; a row's result does not depend on the other rows.
+ * belong to fp4_gemm_mx and fp4_grouped_gemm_mx. The sums are taken in an order
+ * that the sizes alone (tokens, topk, experts, n, k) choose: results repeat bit
+ * for bit, and a row's do not depend on its place or on what the other rows
+ * hold. How many they are may change the last places of its FP32 sums.
  * k == 0, and with ids experts == 0 (a rank without any), write zeros (x and
  * weights may be NULL). tokens, topk or n == 0: returns FP8Q_OK without
  * launching.
