@@ -99,7 +99,7 @@ int fp8_gated_gemm(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t ld
                                out_dtype, out_scale, ld_os, gate_up, ldg);
     if (st != FP8Q_OK) return st;
     if (!is_aligned(workspace, 16)) return FP8Q_ERR_ALIGN;
-    // (the rows kernel is chosen for a few thousand workgroups at the most)
+    // (the rows kernel's launches are within kRowsMostPieces by its rule)
     if (mul_limit(m, n, kMaxBytes) < 0 || !launchable(tiles_shape(m, n))) return FP8Q_ERR_SHAPE;
     const GatedArgs p = gated_args(m, n, k, a, lda, a_scale, ld_as, b, ldb, stride_b, b_scale, ld_bs, stride_bs, act,
                                    out, ldo, out_dtype, out_scale, ld_os, gate_up, ldg);

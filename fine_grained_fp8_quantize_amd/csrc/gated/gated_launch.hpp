@@ -19,6 +19,13 @@ struct RowsForm {
     int waves;
 };
 constexpr int kRowsColumns = 8;
+// The most workgroups that rows_form and grouped_rows choose a rows kernel for: a
+// tile's share of the limit is 8 pieces, so that rows of many tiles take the
+// rows kernel only where n is so small that a tile has no more of them (n up to
+// 16, experts' 128-row segments up to 32), and the 2^20 rows that either rule
+// allows end that: 32 columns of that many are 2^16, a 64th of what a launch may
+// hold.
+constexpr int64_t kRowsMostPieces = 1 << 16;
 // (eight accumulators and more take more than 128 registers)
 constexpr int rows_waves(int accumulators) { return accumulators >= 8 ? 8 : 16; }
 
