@@ -290,7 +290,7 @@ hipError_t launch_gated(const GatedArgs& g, float* workspace, hipStream_t stream
 
 hipError_t launch_grouped_gated(const GatedArgs& g, float* workspace, hipStream_t stream) {
     Params p = gated_params(g);
-    if (grouped_rows(p.m, p.n) && (!g.e4m3 || workspace)) {
+    if (grouped_rows(p.m, p.n, p.group_rows == nullptr) && (!g.e4m3 || workspace)) {
         if (g.e4m3) to_workspace(p, workspace);
         const int waves = grouped_rows_waves(p.k);
         const dim3 grid((unsigned)parts_of(p.n, kRowsColumns), (unsigned)(p.m / 64)), block(64 * waves);

@@ -58,10 +58,15 @@ inline LaunchShape tiles_shape(int64_t m, int64_t n) { return {parts_of(tiles_of
 // 25 / 30 / 42 / 76; 2048 columns, 2048 pieces: 37 / 46 / 57 / 81 / 153; 32
 // experts, 256 columns: 39 / 49 / 61 / 84 / 149; 4 experts, 512 columns, K =
 // 2048: 7 / 8 / 10 / 14 / 14 and 27 to 29). Mostly full segments near the limit
-// are the price of the few rows that decoding has in them.
-inline bool grouped_rows(int64_t m_total, int64_t n) {
+// are the price of the few rows that decoding has in them. `full`: the host
+// knows that all rows are real (no group_rows). Then half the pieces (us, rows
+// kernel and tiles, K = 7168 / 2048 / 512: 4 experts of 128 rows, 768 pieces:
+// 58 and 66 / 20 and 26 / 8 and 14; 1024: 76 and 68 / 24 and 27 / 9 and 14, of
+// one expert of 512 rows 75 and 85 / 23 and 33 / 8 and 17; 1536: 115 and 68 / 35
+// and 27 / 12 and 14; 2048: 154 and 70 / 46 and 28 / 15 and 15).
+inline bool grouped_rows(int64_t m_total, int64_t n, bool full = false) {
     const int64_t wgs = m_total / 64 * parts_of(n, kRowsColumns);
-    return wgs <= 2048 * parts_of(m_total / 128 * parts_of(n, 128), 256) && m_total <= 1 << 20;
+    return wgs <= (full ? 1024 : 2048) * parts_of(m_total / 128 * parts_of(n, 128), 256) && m_total <= 1 << 20;
 }
 inline int grouped_rows_waves(int64_t k) {
     const int64_t slabs = k >= 128 ? k / 128 : 1, steps = parts_of(slabs, 32);

@@ -31,6 +31,7 @@ extern "C" int dense(int64_t m, int64_t n, int64_t k) {
 extern "C" int grouped(int64_t m, int64_t n, int64_t k) {
     return grouped_rows(m, n) ? bad(parts_of(n, kRowsColumns), m / 64, grouped_rows_waves(k)) : 0;
 }
+extern "C" int segments(int64_t m, int64_t n, int full) { return grouped_rows(m, n, full != 0); }
 extern "C" int64_t largest() { return most; }
 // every n up to `to`, and both ends of the steps of m, at one K
 extern "C" int sweep(int64_t to, int64_t k) {
@@ -56,6 +57,7 @@ def rules(tmp_path_factory):
     L = ctypes.CDLL(str(d / "bounds.so"))
     L.sweep.argtypes = [ctypes.c_int64] * 2
     L.dense.argtypes = L.grouped.argtypes = [ctypes.c_int64] * 3
+    L.segments.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
     L.largest.restype = ctypes.c_int64
     return L
 
@@ -68,3 +70,10 @@ def test_the_rows_kernels_launches(rules):
             for m in (1, 16, 17, 32, 33, 64, 65, 128, 1000, 1 << 14, 1 << 20):
                 assert rules.dense(m, n, k) == 0 and rules.grouped(-(-m // 128) * 128, n, k) == 0
     assert rules.largest() == 1 << 16  # the bound is met: experts' 2^20 rows of 25 to 32 columns
+
+
+def test_full_segments_take_tiles_earlier(rules):
+    """Where the host knows that all rows are real, the rows kernel has half the pieces."""
+    for m, n, some, full in ((512, 512, 1, 1), (512, 1024, 1, 1), (512, 1536, 1, 0), (512, 2048, 1, 0), (4096, 256, 1, 0),
+                             (1024, 2048, 0, 0)):
+        assert (rules.segments(m, n, 0), rules.segments(m, n, 1)) == (some, full), (m, n)
