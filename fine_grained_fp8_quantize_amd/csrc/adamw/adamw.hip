@@ -192,13 +192,13 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], const uint32_t 
     top = umax32(top, (uint32_t)__shfl_xor((int)top, 16));
     // A block that FP32 does not hold reads back as NaN: with an infinite scale the codes of 1 that roots above zero get
     // at least would be infinities, beside which their elements would never move again.
-    scale = top < 0x7F800000u ? __uint_as_float(top) / kE4M3Max : __builtin_nanf("");
+    scale = top < 0x7F800000u ? __uint_as_float(top) * (1.0f / kE4M3Max) : __builtin_nanf("");
     // the quotient of IEEE division, by the reciprocal and one correction (see fp8q_device.h) but for tiny scales; a
     // scale of zero, or a NaN, divides nothing
     GroupScale gs;
     gs.s = scale > 0.0f ? scale : 1.0f;
     gs.slow = !(gs.s >= kSmallScale);
-    gs.y = recip(gs.s);
+    gs.y = 1.0f / gs.s;
     float y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = quot_fast(__builtin_fabsf(x[i]), gs);

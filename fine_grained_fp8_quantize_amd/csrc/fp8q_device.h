@@ -76,14 +76,6 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 
 // ------------------------------------------------------------ group scale
 
-// fl32(1 / s) where that is normal (2^-126 < s < 2^126): v_rcp_f32 and one
-// correction of its residual, equal to IEEE division's for every significand of
-// s (compared on the GPU), in four operations.
-__device__ __forceinline__ float recip(float s) {
-    const float y = __builtin_amdgcn_rcpf(s);
-    return __builtin_fmaf(__builtin_fmaf(-s, y, 1.0f), y, y);
-}
-
 // The per-group scale and its correctly rounded reciprocal.
 //   s = fl32(amax / 448) (IEEE division), y = fl32(1 / s).
 // For s >= 2^-60 the quotient fl32(x / s) of every bf16 |x| <= amax is

@@ -42,9 +42,8 @@ __device__ __forceinline__ Eight load8(const uint16_t* p, int64_t left) {
 // The logistic is that of act.h, correction included: with it as many codes as
 // in the same formulas in elementary FP32 operations lie on the other side of a
 // border from the exact gradient's (8192 x 2048: 58 and 58 of 33.5 million);
-// without it, and with 1 / s uncorrected, 123. From +-16 on gelu's share is 0 or
-// 1 exactly: the powers of g that would overflow are taken of that (but a NaN
-// stays).
+// without it, and with 1 / s uncorrected, 123. From +-16 on gelu's share is 0 or 1 exactly: the
+// powers of g that would overflow are taken of that (but a NaN stays).
 __device__ __forceinline__ void gradients(int act, float dh, float g, float u, float& dg, float& du) {
     float w = g, by = 1.0f, c = g;
     if (act != FP8Q_ACT_SILU) {
@@ -60,22 +59,28 @@ __device__ __forceinline__ void gradients(int act, float dh, float g, float u, f
 }
 
 // The scale of a tile and what its quotients take, by the library's contract:
-// s = fl(amax / 448), codes of fl(x / s). The quotient is a product with fl(1 /
-// s) and one correction of its residual (see fp8q_device.h). The sign is that of
-// x, zeros' included: the residual is negated twice, so that +-0 stays as it is.
-// Scales whose residuals may be subnormal, zero, NaN and infinity take
-// divisions. (A product with fl(1 / s) alone, and fl(amax / 448) from one with
-// fl(1 / 448), would be 2 us less of 38, 8192 x 2048 in both tilings, and give
-// other codes next to a border.)
+// s = fl(amax / 448), codes of fl(x / s). Both quotients are made of a product
+// with a reciprocal and one correction of its residual (Markstein's, as in
+// fp8q_device.h): fl(1 / 448) is a constant, and v_rcp_f32 corrected in the
+// same way is fl(1 / s) (for every significand of s, compared on the GPU, where
+// 1 / s is normal, s < 2^126; a scale is below 2^120). The sign is that of x,
+// zeros' included: the residual is negated twice, so that +-0 stays as it is.
+// Scales whose residuals may be subnormal, zero, NaN and infinity take divisions.
+// The product with fl(1 / s) alone would be 1.8 us less of 38 (8192 x 2048, both
+// tilings) and give other codes next to a border.
 struct TileScale {
     float s, y;
     bool slow;
 };
 __device__ __forceinline__ TileScale tile_scale(float amax) {
+    constexpr float kBy = 1.0f / kE4M3Max;
     TileScale t;
-    t.s = amax / kE4M3Max;
-    t.slow = !(t.s >= kSmallScale) || t.s == __builtin_inff();
-    t.y = recip(t.s);
+    const float q = amax * kBy;
+    t.s = __builtin_fmaf(__builtin_fmaf(-q, kE4M3Max, amax), kBy, q);
+    t.slow = !(t.s >= kSmallScale);
+    if (t.slow) t.s = amax / kE4M3Max;
+    const float y = __builtin_amdgcn_rcpf(t.s);
+    t.y = __builtin_fmaf(__builtin_fmaf(-t.s, y, 1.0f), y, y);
     return t;
 }
 __device__ __forceinline__ float quotient(float x, const TileScale& t) {

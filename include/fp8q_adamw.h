@@ -54,8 +54,8 @@ typedef struct fp8q_adamw_tensor {
  * even, and changes below half its last place are lost: train FP32 parameters
  * with a bf16 copy where that matters.
  *
- * 8-bit states: a block of 128 elements has the scale s = fl32(amax / 448) and
- * codes E4M3(fl32(x / s)), rounded STOCHASTICALLY: the code above with the probability of
+ * 8-bit states: a block of 128 elements has the scale s = amax / 448 and codes
+ * E4M3(x / s), rounded STOCHASTICALLY: the code above with the probability of
  * the part that is cut off. (Rounded to nearest, a moment whose step is less
  * than half a code's, as those of beta2 near 1 are, would never move.) The 16
  * random bits of an element and state are a hash of seed, step, the tensor's

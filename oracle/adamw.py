@@ -51,7 +51,7 @@ def encode(x: np.ndarray, bits16: np.ndarray, root: bool):
     pad = -len(x) % BLOCK
     b = np.pad(np.abs(x), (0, pad)).reshape(-1, BLOCK)
     top = b.max(axis=1)
-    scale = np.where(np.isfinite(top), top / F(448.0), F(np.nan)).astype(F)
+    scale = np.where(np.isfinite(top), top * F(1.0 / 448.0), F(np.nan)).astype(F)
     y = (b / np.where(scale > 0, scale, F(1)).astype(F)[:, None]).reshape(-1)[:len(x)]
     code = stochastic_e4m3(y, bits16)
     if root:
