@@ -190,6 +190,8 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], const uint32_t 
     for (int i = 0; i < 4; ++i) top = umax32(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
     top = row16_max(top);
     top = umax32(top, (uint32_t)__shfl_xor((int)top, 16));
+    // The scale is a product by its definition; the quotient would differ in the last place of about half of the scales
+    // (64M elements: 198.7 us, with a division 203.2).
     // A block that FP32 does not hold reads back as NaN: with an infinite scale the codes of 1 that roots above zero get
     // at least would be infinities, beside which their elements would never move again.
     scale = top < 0x7F800000u ? __uint_as_float(top) * (1.0f / kE4M3Max) : __builtin_nanf("");

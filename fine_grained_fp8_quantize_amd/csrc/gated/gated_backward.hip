@@ -42,8 +42,9 @@ __device__ __forceinline__ Eight load8(const uint16_t* p, int64_t left) {
 // The logistic is that of act.h, correction included: with it as many codes as
 // in the same formulas in elementary FP32 operations lie on the other side of a
 // border from the exact gradient's (8192 x 2048: 58 and 58 of 33.5 million);
-// without it, and with 1 / s uncorrected, 123. From +-16 on gelu's share is 0 or 1 exactly: the
-// powers of g that would overflow are taken of that (but a NaN stays).
+// without it, and with 1 / s uncorrected, 123. From +-16 on gelu's share is 0 or
+// 1 exactly: the powers of g that would overflow are taken of that (but a NaN
+// stays).
 __device__ __forceinline__ void gradients(int act, float dh, float g, float u, float& dg, float& du) {
     float w = g, by = 1.0f, c = g;
     if (act != FP8Q_ACT_SILU) {

@@ -54,13 +54,14 @@ typedef struct fp8q_adamw_tensor {
  * even, and changes below half its last place are lost: train FP32 parameters
  * with a bf16 copy where that matters.
  *
- * 8-bit states: a block of 128 elements has the scale s = amax / 448 and codes
- * E4M3(x / s), rounded STOCHASTICALLY: the code above with the probability of
- * the part that is cut off. (Rounded to nearest, a moment whose step is less
- * than half a code's, as those of beta2 near 1 are, would never move.) The 16
- * random bits of an element and state are a hash of seed, step, the tensor's
- * place in the call and the element's number, so a step can be repeated
- * exactly. A root of the second moment above zero is never stored as zero: its
+ * 8-bit states: a block of 128 elements has the scale s = fl32(amax * fl32(1 /
+ * 448)), within a last place of the quotient that the quantizers of fp8q.h take,
+ * and codes E4M3(fl32(x / s)), rounded STOCHASTICALLY: the code above with the
+ * probability of the part that is cut off. (Rounded to nearest, a moment whose
+ * step is less than half a code's, as those of beta2 near 1 are, would never
+ * move.) The 16 random bits of an element and state are a hash of seed, step,
+ * the tensor's place in the call and the element's number, so a step can be
+ * repeated exactly. A root of the second moment above zero is never stored as zero: its
  * element would take a far too large step next time. A block of either moment
  * with an infinity or a NaN reads back as NaN; a gradient whose square passes
  * FP32 (from 1.8e19 on) makes the second moment one.

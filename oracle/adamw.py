@@ -50,7 +50,7 @@ def encode(x: np.ndarray, bits16: np.ndarray, root: bool):
     """Codes and block scales of one tensor's new state."""
     pad = -len(x) % BLOCK
     b = np.pad(np.abs(x), (0, pad)).reshape(-1, BLOCK)
-    top = b.max(axis=1)
+    top = b.max(axis=1)  # (the scale is a product, by the header: it may differ from top / 448 in the last place)
     scale = np.where(np.isfinite(top), top * F(1.0 / 448.0), F(np.nan)).astype(F)
     y = (b / np.where(scale > 0, scale, F(1)).astype(F)[:, None]).reshape(-1)[:len(x)]
     code = stochastic_e4m3(y, bits16)

@@ -1,5 +1,5 @@
-"""Blocks of the 8-bit optimizer states as their definition has them: NaN for a
-block whose moment or root is infinite."""
+"""Blocks of the 8-bit optimizer states as their definition has them: the scale
+fl32(amax * fl32(1 / 448)), and NaN for a block whose moment or root is infinite."""
 from __future__ import annotations
 
 import numpy as np
@@ -28,6 +28,19 @@ def _first_step(g):
 def _values(codes, scale):
     with np.errstate(invalid="ignore"):
         return model.decode_e4m3(codes) * scale[np.arange(len(codes)) // 128]
+
+
+def test_scales_are_the_product():
+    rng = np.random.default_rng(2)
+    g = (rng.standard_normal(128 * 500 + 37) * np.exp(rng.standard_normal(128 * 500 + 37))).astype(np.float32)
+    _, _, s = _first_step(g)
+    one = np.ones(len(g), np.float32)
+    _, m, r, _ = model.step32(one, g, 0 * one, 0 * one, step=1, **HYPER)
+    for name, x in (("m", m), ("r", r)):
+        top = np.abs(np.pad(x, (0, -len(x) % 128))).reshape(-1, 128).max(1)
+        want = top * (np.float32(1) / np.float32(448))
+        assert (want != top / np.float32(448)).sum() > 100
+        assert np.array_equal(s[name].view(np.int32), want.view(np.int32)), name
 
 
 @pytest.mark.parametrize("bad,m_too", [(float("inf"), True), (-float("inf"), True), (float("nan"), True), (1e20, False),
