@@ -169,7 +169,8 @@ def adamw_step(plan: AdamwPlan, grads, step, lr, beta1: float = 0.9, beta2: floa
     one launch for each 64 tensors (56 with 8-bit states).
 
     ``grads``: bf16 or FP32 tensors (all of one dtype), contiguous, of the
-    params' shapes; None leaves a tensor as it is. ``step``: 1 in the first
+    params' shapes, sharing no memory with the plan's tensors; None leaves a
+    tensor as it is. ``step``: 1 in the first
     step; ``step`` and ``lr`` are numbers, or GPU tensors of one element (int64,
     float32) that are read when the step runs, as a captured step that is
     replayed needs. ``grad_scale``: a GPU tensor of one float32 element that the

@@ -2,8 +2,8 @@
 //
 // The step is a stream: with FP32 parameters, bf16 gradients and a bf16 copy
 // it reads and writes 28 bytes an element with 32-bit states, 16.1 with 8-bit
-// ones, and HBM bounds it: 64M elements 305 us, 5.9 TB/s, and 128M in 8 bits 383
-// us, 5.4 TB/s (a copy of 1 GiB: 5.1). A launch takes up to 64 tensors (56 with
+// ones, and HBM bounds it: 64M elements 305 us, 5.9 TB/s, and 128M in 8 bits 373
+// us, 5.5 TB/s (a copy of 1 GiB: 5.1). A launch takes up to 64 tensors (56 with
 // 8-bit states), whose table is a kernel argument: it is captured with the
 // launch, and nothing has to be copied to the device first. A workgroup takes
 // 1024 elements of one of them, a thread four consecutive ones, so that every

@@ -61,10 +61,10 @@ typedef struct fp8q_adamw_tensor {
  * step is less than half a code's, as those of beta2 near 1 are, would never
  * move.) The 16 random bits of an element and state are a hash of seed, step,
  * the tensor's place in the call and the element's number, so a step can be
- * repeated exactly. A root of the second moment above zero is never stored as zero: its
- * element would take a far too large step next time. A block of either moment
- * with an infinity or a NaN reads back as NaN; a gradient whose square passes
- * FP32 (from 1.8e19 on) makes the second moment one.
+ * repeated exactly. A root of the second moment above zero is never stored as
+ * zero: its element would take a far too large step next time. A block of either
+ * moment with an infinity or a NaN reads back as NaN; a gradient whose square
+ * passes FP32 (from 1.8e19 on) makes the second moment one.
  *
  * tensors     HOST array of `count` entries, read during the call.
  * grads       HOST array of `count` device addresses, read during the call: the
