@@ -200,7 +200,8 @@ def fp8_grouped_gated_gemm(group_offsets: torch.Tensor, group_rows: torch.Tensor
                            workspace: torch.Tensor | None = None):
     """:func:`fp8_gated_gemm` for the experts of an expert-sorted row layout
     (:func:`moe_dispatch` with ``align=128``): rows ``[off[e], off[e+1])`` of ``a``
-    with ``b[e]``, of which the first ``group_rows[e]`` are real (None: all).
+    with ``b[e]``, of which the first ``group_rows[e]`` are real (None: all,
+    which may take the sums in another order than counts that say the same).
 
     ``group_offsets`` int32 ``[E+1]``, multiples of 128, its last entry
     ``m_total``, the rows of ``a``; ``b[E][2][n][k]`` with

@@ -73,6 +73,8 @@ int fp8_gated_gemm(int64_t m, int64_t n, int64_t k, const uint8_t *a, int64_t ld
  * (offsets in whole 128 rows, group_offsets[groups] == m_total). Rows of a
  * segment past its group_rows[e] are padding: their rows of out (codes and
  * scales too) and of gate_up are written as zeros, whatever A holds there.
+ * Without group_rows all rows are real, and the sums may be taken in another
+ * order than with counts that say the same.
  * workspace: for E4M3 output, fp8_grouped_gated_workspace_bytes(m_total, n).
  * Everything else as fp8_gated_gemm with m = m_total. FP8Q_DEBUG applies as in
  * fp8_grouped_gemm.
